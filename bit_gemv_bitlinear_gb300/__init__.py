@@ -8,7 +8,9 @@ or ``__graft_entry__.build()``).
 
 Function names follow the C ABI: ``bw_quant_act``, ``bw_repack``,
 ``bw_unrepack``, ``bw_gemv_w2a8``, ``bw_gemv_w2a8_acc``, ``bw_gemm_w2a8``,
-``bw_gemm_w2a8_acc``, ``bw_attn_decode``, ``bw_attn_decode_ex``.
+``bw_gemm_w2a8_acc``, ``bw_attn_decode``, ``bw_attn_decode_ex``,
+``bw_qk_norm_rope_append``, ``bw_attn_paged_decode``,
+``bw_attn_paged_prefill``.
 """
 from __future__ import annotations
 
@@ -45,10 +47,15 @@ EXPORTS = ("bw_status_string", "bw_last_cuda_error", "bw_version",
            "bw_stack_create_kv",
            "bw_stack_read_kv", "bw_stack_reset_kv", "bw_gemv_w2a8_lut",
            "bw_gemv_w2a8_lut_acc", "bw_gemm_workspace_bytes", "bw_gemm_w2a8",
-           "bw_gemm_w2a8_acc")
+           "bw_gemm_w2a8_acc", "bw_qk_norm_rope_append",
+           "bw_attn_paged_decode_workspace_bytes", "bw_attn_paged_decode",
+           "bw_attn_paged_prefill_workspace_bytes", "bw_attn_paged_prefill")
 
 _P = ctypes.c_void_p
 _I = ctypes.c_int
+_L = ctypes.c_int64
+_F = ctypes.c_float
+_Z = ctypes.c_size_t
 _SIGS = {
     "bw_status_string": (ctypes.c_char_p, [_I]),
     "bw_last_cuda_error": (_I, []),
@@ -83,6 +90,14 @@ _SIGS = {
     "bw_attn_decode_ex": (_I, [_P, _P, _I, _I, _I, _I, ctypes.c_float, _P,
                                _P, _P, _P, ctypes.c_size_t, ctypes.c_uint,
                                _P]),
+    "bw_qk_norm_rope_append": (_I, [_P, _L, _I, _P, _I, _P, _P, _F, _F, _P,
+                                    _P, _L, _P]),
+    "bw_attn_paged_decode_workspace_bytes": (_Z, [_I] * 4),
+    "bw_attn_paged_decode": (_I, [_P, _L, _I, _P, _F, _I, _I, _P, _L, _I, _P,
+                                  _Z, _P]),
+    "bw_attn_paged_prefill_workspace_bytes": (_Z, [_I] * 5),
+    "bw_attn_paged_prefill": (_I, [_P, _L, _I, _P, _I, _P, _F, _I, _I, _P,
+                                   _L, _P, _Z, _P]),
 }
 for _name, (_res, _args) in _SIGS.items():
     _fn = getattr(_lib, _name)
@@ -437,6 +452,245 @@ def bw_attn_decode_ex(qkv: torch.Tensor, pos: torch.Tensor, H: int,
         _dev(out, torch.float32, "out"),
         _dev(workspace, torch.uint8, "workspace"), workspace.numel(),
         int(flags), _stream(stream)), "bw_attn_decode_ex")
+    return out
+
+
+class _PagedKV(ctypes.Structure):
+    _fields_ = [("k_pages", _P), ("v_pages", _P), ("page_table", _P),
+                ("kv_len", _P), ("page_stride", _L), ("n_pages", _I),
+                ("page_size", _I), ("n_kv_heads", _I), ("head_dim", _I),
+                ("n_seqs", _I), ("max_pages", _I)]
+
+
+def _same_device(dev, *tensors):
+    for t in tensors:
+        if t is not None and t.device != dev:
+            raise ValueError(f"tensors on {t.device} and {dev}: one call's "
+                             "tensors must be on one device")
+
+
+def _paged_kv(k_pages: torch.Tensor, v_pages: torch.Tensor,
+              page_table: torch.Tensor, kv_len: torch.Tensor) -> _PagedKV:
+    """The bw_paged_kv of four tensors.  The pools [n_pages][Hkv][page][D] may
+    be strided from page to page (two views of one pool, say)."""
+    for t, name in ((k_pages, "k_pages"), (v_pages, "v_pages")):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        if t.dtype != torch.bfloat16:
+            raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+        if t.dim() != 4:
+            raise ValueError(f"{name} must be [n_pages][Hkv][page][D]")
+    shape, st = k_pages.shape, k_pages.stride()
+    if v_pages.shape != shape or v_pages.stride() != st:
+        raise ValueError("k_pages and v_pages must have one shape and strides")
+    n_pages, hkv, page, D = shape
+    if (D > 1 and st[3] != 1) or (page > 1 and st[2] != D) or \
+            (hkv > 1 and st[1] != page * D):
+        raise ValueError("a page of k_pages and v_pages must be contiguous")
+    table, lens = _dev(page_table, torch.int32, "page_table"), \
+        _dev(kv_len, torch.int32, "kv_len")
+    if page_table.dim() != 2 or kv_len.dim() != 1 or \
+            page_table.shape[0] != kv_len.shape[0]:
+        raise ValueError("page_table must be [n_seqs][max_pages] and kv_len "
+                         "[n_seqs]")
+    _same_device(k_pages.device, v_pages, page_table, kv_len)
+    return _PagedKV(k_pages.data_ptr(), v_pages.data_ptr(), table, lens,
+                    st[0] if n_pages > 1 else hkv * page * D, n_pages, page,
+                    hkv, D, page_table.shape[0], page_table.shape[1])
+
+
+def _rows(t: torch.Tensor, dtypes, rows: int, H: int, D: int, name: str):
+    """(pointer, row stride) of [rows][H][D] with contiguous rows."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be {' or '.join(map(str, dtypes))}, "
+                        f"got {t.dtype}")
+    if tuple(t.shape) != (rows, H, D):
+        raise ValueError(f"{name} must be [{rows}][{H}][{D}], got "
+                         f"{tuple(t.shape)}")
+    st = t.stride()
+    if (D > 1 and st[2] != 1) or (H > 1 and st[1] != D):
+        raise ValueError(f"a row of {name} must be contiguous")
+    return t.data_ptr(), (st[0] if rows > 1 else H * D)
+
+
+def _device_of_stream(stream):
+    dev = getattr(stream, "device", None)
+    return dev if isinstance(dev, torch.device) else None
+
+
+class _OnDevice:
+    """Makes `dev` the current device and `stream` (None: its current stream)
+    the stream that new tensors belong to, for the length of one call; costs
+    nothing where they are current already."""
+
+    def __init__(self, dev, stream):
+        sdev = _device_of_stream(stream)
+        if sdev is not None and sdev != dev:
+            raise ValueError(f"stream on {sdev}, tensors on {dev}")
+        self._dev = None if dev.index == torch.cuda.current_device() \
+            else torch.cuda.device(dev)
+        self._stream = None
+        if stream is None:
+            self.stream = torch.cuda.current_stream(dev).cuda_stream
+        else:
+            self.stream = _stream(stream)
+            obj = stream if hasattr(stream, "cuda_stream") else \
+                torch.cuda.ExternalStream(self.stream, device=dev)
+            self._stream = torch.cuda.stream(obj)
+
+    def __enter__(self):
+        if self._dev is not None:
+            self._dev.__enter__()
+        if self._stream is not None:
+            self._stream.__enter__()
+        return self.stream
+
+    def __exit__(self, *exc):
+        if self._stream is not None:
+            self._stream.__exit__(*exc)
+        if self._dev is not None:
+            self._dev.__exit__(*exc)
+
+
+def bw_qk_norm_rope_append(qkv: torch.Tensor, k_pages: torch.Tensor,
+                           v_pages: torch.Tensor, page_table: torch.Tensor,
+                           kv_len: torch.Tensor, H: int,
+                           q_start: torch.Tensor | None = None,
+                           q_gamma: torch.Tensor | None = None,
+                           k_gamma: torch.Tensor | None = None,
+                           eps: float = 1e-5, theta: float = 500000.0,
+                           q_out: torch.Tensor | None = None,
+                           stream=None) -> torch.Tensor:
+    """New tokens' bf16 qkv [n_tokens][(H + 2 Hkv) D] (rows may be strided):
+    the RMS norm of each query and key head (where its fp32 gamma [D] is
+    given), RoPE at the token's position, keys and values appended to the
+    pages; returns the queries, bf16 q_out [n_tokens][H][D] (which may be a
+    view of qkv's own query columns).  kv_len counts the new tokens; q_start
+    int32 [n_seqs + 1] gives each sequence's rows, None one row each.  Rows of
+    no sequence are left as they are (zeros in a q_out made here)."""
+    kv = _paged_kv(k_pages, v_pages, page_table, kv_len)
+    dev, D = k_pages.device, kv.head_dim
+    if not isinstance(qkv, torch.Tensor) or qkv.dim() != 2:
+        raise ValueError("qkv must be [n_tokens][(H + 2 Hkv) D]")
+    n = qkv.shape[0]
+    heads = H + 2 * kv.n_kv_heads
+    if H < 1 or qkv.shape[1] != heads * D:
+        raise ValueError(f"qkv must have {heads * D} columns")
+    ptr, ld = _rows(qkv.unflatten(1, (heads, D)), (torch.bfloat16,), n, heads,
+                    D, "qkv")
+    _same_device(dev, qkv, q_start, q_gamma, k_gamma, q_out)
+    starts = None
+    if q_start is not None:
+        starts = _dev(q_start, torch.int32, "q_start")
+        _need(q_start, kv.n_seqs + 1, "q_start")
+    gammas = []
+    for g, name in ((q_gamma, "q_gamma"), (k_gamma, "k_gamma")):
+        gammas.append(None if g is None else _dev(g, torch.float32, name))
+        if g is not None:
+            _need(g, D, name)
+    with _OnDevice(dev, stream) as s:
+        if q_out is None:
+            q_out = torch.zeros((n, H, D), dtype=torch.bfloat16, device=dev)
+        out, out_ld = _rows(q_out, (torch.bfloat16,), n, H, D, "q_out")
+        if out == ptr and n == 1:
+            out_ld = ld  # in place: one row has no stride of its own
+        _check(_lib.bw_qk_norm_rope_append(
+            ptr, ld, n, starts, H, gammas[0], gammas[1], eps, theta,
+            ctypes.byref(kv), out, out_ld, s), "bw_qk_norm_rope_append")
+    return q_out
+
+
+def bw_attn_paged_decode_workspace_bytes(n_seqs: int, H: int, Hkv: int,
+                                         D: int) -> int:
+    """Device scratch bw_attn_paged_decode needs (0: unsupported)."""
+    return int(_lib.bw_attn_paged_decode_workspace_bytes(n_seqs, H, Hkv, D))
+
+
+def bw_attn_paged_decode(q: torch.Tensor, k_pages: torch.Tensor,
+                         v_pages: torch.Tensor, page_table: torch.Tensor,
+                         kv_len: torch.Tensor, window: int = 0,
+                         sinks: int = 0, scale: float | None = None,
+                         out: torch.Tensor | None = None,
+                         workspace: torch.Tensor | None = None,
+                         stream=None) -> torch.Tensor:
+    """Attention of one new token per sequence over its pages: bf16 q
+    [n_seqs][H][D] (rotated) -> out [n_seqs][H][D], fp32 (the default) or
+    bf16 by the tensor given.  window > 0: the last `window` positions and
+    the first `sinks` ones.  scale: 1/sqrt(D) if None.  `workspace`: a uint8
+    device tensor of at least bw_attn_paged_decode_workspace_bytes bytes,
+    zeroed before its first use; if omitted, one is made for this call."""
+    kv = _paged_kv(k_pages, v_pages, page_table, kv_len)
+    dev, D, n = k_pages.device, kv.head_dim, kv.n_seqs
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        raise ValueError("q must be [n_seqs][H][D]")
+    H = q.shape[1]
+    ptr, ld = _rows(q, (torch.bfloat16,), n, H, D, "q")
+    _same_device(dev, q, out, workspace)
+    with _OnDevice(dev, stream) as s:
+        if out is None:
+            out = torch.empty((n, H, D), dtype=torch.float32, device=dev)
+        if workspace is None:
+            workspace = torch.zeros((max(16, bw_attn_paged_decode_workspace_bytes(
+                n, H, kv.n_kv_heads, D)),), dtype=torch.uint8, device=dev)
+        o, out_ld = _rows(out, (torch.float32, torch.bfloat16), n, H, D, "out")
+        _check(_lib.bw_attn_paged_decode(
+            ptr, ld, H, ctypes.byref(kv),
+            1.0 / D ** 0.5 if scale is None else scale, window, sinks, o,
+            out_ld, out.dtype == torch.bfloat16,
+            _dev(workspace, torch.uint8, "workspace"), workspace.numel(), s),
+            "bw_attn_paged_decode")
+    return out
+
+
+def bw_attn_paged_prefill_workspace_bytes(n_tokens: int, n_seqs: int, H: int,
+                                          Hkv: int, D: int) -> int:
+    """Device scratch bw_attn_paged_prefill needs (0: unsupported)."""
+    return int(_lib.bw_attn_paged_prefill_workspace_bytes(n_tokens, n_seqs, H,
+                                                          Hkv, D))
+
+
+def bw_attn_paged_prefill(q: torch.Tensor, k_pages: torch.Tensor,
+                          v_pages: torch.Tensor, page_table: torch.Tensor,
+                          kv_len: torch.Tensor, q_start: torch.Tensor,
+                          window: int = 0, sinks: int = 0,
+                          scale: float | None = None,
+                          out: torch.Tensor | None = None,
+                          workspace: torch.Tensor | None = None,
+                          stream=None) -> torch.Tensor:
+    """Causal attention of the new tokens' bf16 q [n_tokens][H][D] (rotated)
+    over their sequences' pages -> bf16 out [n_tokens][H][D].  q_start int32
+    [n_seqs + 1]: sequence b owns rows q_start[b] .. q_start[b + 1] - 1, its
+    last positions; rows of no sequence are left as they are (zeros in an out
+    made here).  window, sinks, scale, workspace as for bw_attn_paged_decode
+    (bw_attn_paged_prefill_workspace_bytes)."""
+    kv = _paged_kv(k_pages, v_pages, page_table, kv_len)
+    dev, D = k_pages.device, kv.head_dim
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        raise ValueError("q must be [n_tokens][H][D]")
+    n, H = q.shape[0], q.shape[1]
+    ptr, ld = _rows(q, (torch.bfloat16,), n, H, D, "q")
+    starts = _dev(q_start, torch.int32, "q_start")
+    _need(q_start, kv.n_seqs + 1, "q_start")
+    _same_device(dev, q, q_start, out, workspace)
+    with _OnDevice(dev, stream) as s:
+        if out is None:
+            out = torch.zeros((n, H, D), dtype=torch.bfloat16, device=dev)
+        if workspace is None:
+            workspace = torch.zeros((max(16, bw_attn_paged_prefill_workspace_bytes(
+                n, kv.n_seqs, H, kv.n_kv_heads, D)),), dtype=torch.uint8,
+                device=dev)
+        o, out_ld = _rows(out, (torch.bfloat16,), n, H, D, "out")
+        _check(_lib.bw_attn_paged_prefill(
+            ptr, ld, n, starts, H, ctypes.byref(kv),
+            1.0 / D ** 0.5 if scale is None else scale, window, sinks, o,
+            out_ld, _dev(workspace, torch.uint8, "workspace"),
+            workspace.numel(), s), "bw_attn_paged_prefill")
     return out
 
 

@@ -481,6 +481,149 @@ bw_status bw_attn_decode_ex(const bw_bf16 *qkv, const int *pos, int H,
                             void *workspace, size_t workspace_bytes,
                             unsigned int flags, bw_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Paged key-value cache: many sequences of unlike lengths served together
+ * ([W2A8] §六 item 2 preallocates one cache per sequence; here the cache is
+ * cut into pages so that sequences share one pool).  Position j of sequence
+ * b lies in row j mod page_size of page page_table[b][j div page_size] of
+ * both pools.
+ *   k_pages, v_pages  bf16 [n_pages][n_kv_heads][page_size][head_dim] device,
+ *              16-byte aligned, page i at i * page_stride elements.
+ *   page_table int32 [n_seqs][max_pages] device, 4-byte aligned.  Entries of
+ *              positions that a call neither writes nor lets any of its
+ *              tokens see are not used: they may hold anything.
+ *   kv_len     int32 [n_seqs] device, 4-byte aligned: the positions of each
+ *              sequence, the new tokens of the step included.
+ *   page_stride  elements from page to page, the same in both pools:
+ *              a multiple of 8, at least n_kv_heads * page_size * head_dim,
+ *              below 2^38.
+ *   page_size  a power of two from 16 to 256; head_dim 64 or 128; 1 <=
+ *              n_kv_heads <= BW_ATTN_MAX_KV_HEADS; 1 <= n_seqs <=
+ *              BW_PAGED_MAX_SEQS; n_pages, max_pages >= 1; max_pages *
+ *              page_size <= BW_PAGED_MAX_LEN.
+ * The struct is HOST memory, read before the call returns.
+ * The lengths, the page table and q_start are read on the device, so a
+ * captured graph serves every step.  What they hold cannot be checked on the
+ * host.  Bit 256 of the device error word is set (bw_device_error then
+ * returns BW_ERR_INVALID_ARG) for a length outside [0, max_pages *
+ * page_size], a token range of a sequence that is not within [0, n_tokens]
+ * or is longer than the sequence, and a used entry outside [0, n_pages).
+ * Nothing outside the buffers is read or written for them: a bad sequence
+ * counts as one without visible positions (its attention rows are zeros, it
+ * appends nothing), and a bad page reads as zeros and is not written.
+ * q_start (int32 [n_seqs + 1] device, 4-byte aligned): sequence b owns the
+ * rows q_start[b] .. q_start[b + 1] - 1 of the call's n_tokens rows, its last
+ * q_start[b + 1] - q_start[b] positions; q_start does not decrease.  Rows
+ * before q_start[0] and from q_start[n_seqs] on belong to no sequence and are
+ * left as they are.
+ * Distinct positions that a call appends must not share a page row.
+ * Ordering of the three calls below: launched with programmatic dependent
+ * launch; everything is read and written after the preceding work on
+ * `stream` has completed.  Asynchronous; they allocate nothing.
+ * ---------------------------------------------------------------------- */
+#define BW_PAGED_MAX_SEQS 4096
+#define BW_PAGED_MAX_LEN (1 << 24)
+#define BW_PAGED_MAX_TOKENS (1 << 20)
+#define BW_PAGED_MAX_GROUP 16
+typedef struct {
+    bw_bf16 *k_pages;
+    bw_bf16 *v_pages;
+    const int *page_table;
+    const int *kv_len;
+    int64_t page_stride;
+    int n_pages;
+    int page_size;
+    int n_kv_heads;
+    int head_dim;
+    int n_seqs;
+    int max_pages;
+} bw_paged_kv;
+
+/* bw_qk_norm_rope_append -- for each new token: the RMS norm of every query
+ * and key head, their rotation at the token's position, and the append of
+ * key and value to the pages, in one pass.
+ *   norm  n(x) = x / sqrt(mean(x^2) + eps) * gamma over the D = head_dim
+ *         values of a head, where the gamma of that kind is given;
+ *   RoPE  pair (x[2i], x[2i+1]) turns by the angle p theta^(-2i/D), adjacent
+ *         pairs as in bw_attn_decode; the angle is reduced exactly (64-bit
+ *         fixed point), so far positions keep their precision.
+ * fp32 arithmetic, one rounding to bf16 (nearest even); values are copied.
+ *   qkv      bf16 [n_tokens][qkv_ld] device, 16-byte aligned: q | k | v of H,
+ *            Hkv, Hkv heads of D (a fused projection's rows); qkv_ld a
+ *            multiple of 8, at least (H + 2 Hkv) D.
+ *   q_start  as above, or NULL: one new token per sequence (n_tokens ==
+ *            n_seqs), and a sequence of length 0 is skipped.
+ *   q_gamma, k_gamma  fp32 [D] device, 16-byte aligned, or NULL (no norm).
+ *   eps >= 0; 1 <= theta < 3e38 (host).
+ *   q_out    bf16 [n_tokens][q_ld] device, 16-byte aligned, q_ld a multiple
+ *            of 8, at least H D: the normed and rotated queries.  It may be
+ *            qkv itself with q_ld == qkv_ld (in place), else must not
+ *            overlap it.
+ *   1 <= n_tokens <= BW_PAGED_MAX_TOKENS; Hkv divides H, H / Hkv <=
+ *   BW_PAGED_MAX_GROUP; strides of rows below 2^31.  A token whose page is
+ *   bad writes its q_out row but no key or value; a token of a bad sequence
+ *   writes nothing. */
+bw_status bw_qk_norm_rope_append(const bw_bf16 *qkv, int64_t qkv_ld,
+                                 int n_tokens, const int *q_start, int H,
+                                 const float *q_gamma, const float *k_gamma,
+                                 float eps, float theta,
+                                 const bw_paged_kv *kv, bw_bf16 *q_out,
+                                 int64_t q_ld, bw_stream_t stream);
+
+/* bw_attn_paged_decode -- attention of one new token per sequence over its
+ * pages: with G = H / Hkv, p = kv_len[b] - 1,
+ *   out[b][h] = sum_j softmax_j(scale q[b][h] . k[h/G][j]) v[h/G][j]
+ * over the positions j <= p that the token sees: all of them (window 0), or
+ * j > p - window and j < sinks (window > 0: a sliding window of `window`
+ * positions, the token's own included, and `sinks` first positions that stay
+ * visible).  An empty sequence gets zeros.  The new token's key and value
+ * must be in the pages already (bw_qk_norm_rope_append).
+ * Pages that hold no visible position are not read; rows of the others that
+ * are not visible may hold anything (NaN included).  Scores, softmax and
+ * sums are fp32, and the fp32 output keeps fp32 precision.
+ *   q         bf16 [n_seqs][q_ld] device, 16-byte aligned: H rotated heads of
+ *             D; q_ld a multiple of 8, at least H D.
+ *   out       fp32 or (out_bf16 nonzero) bf16 [n_seqs][out_ld] device,
+ *             16-byte aligned; out_ld a multiple of 8, at least H D.
+ *   scale > 0 (usually 1/sqrt(D)), window >= 0, sinks >= 0 (host).
+ *   workspace device scratch of at least
+ *             bw_attn_paged_decode_workspace_bytes(n_seqs, H, Hkv, D) bytes,
+ *             16-byte aligned, owned by the caller.  Zero it once before its
+ *             first use: it holds one counter per sequence and key-value
+ *             head, which every call leaves at zero again.  Calls that share
+ *             a workspace (captured graphs too) must not overlap on the GPU.
+ *   Hkv divides H, H / Hkv <= BW_PAGED_MAX_GROUP; strides of rows below
+ *   2^31. */
+size_t bw_attn_paged_decode_workspace_bytes(int n_seqs, int H, int Hkv, int D);
+bw_status bw_attn_paged_decode(const bw_bf16 *q, int64_t q_ld, int H,
+                               const bw_paged_kv *kv, float scale, int window,
+                               int sinks, void *out, int64_t out_ld,
+                               int out_bf16, void *workspace,
+                               size_t workspace_bytes, bw_stream_t stream);
+
+/* bw_attn_paged_prefill -- causal attention of many new tokens per sequence
+ * (whole prompts, or chunks behind an earlier past) over the pages.  Row t
+ * of sequence b has position p = kv_len[b] - q_start[b + 1] + t and sees the
+ * positions j <= p, with a window those of bw_attn_paged_decode.
+ * Products run on the tensor cores with fp32 accumulation; the exp weights
+ * are rounded to bf16, like the output.  What a position that some new token
+ * of its sequence sees holds must be finite; others may hold anything.
+ *   q         bf16 [n_tokens][q_ld] device, out bf16 [n_tokens][out_ld]
+ *             device: 16-byte aligned, both strides multiples of 8, at least
+ *             H D and below 2^31; out must not overlap q.
+ *   q_start   as above (required).
+ *   scale, window, sinks, H  as for bw_attn_paged_decode.
+ *   workspace as above, bw_attn_paged_prefill_workspace_bytes(n_tokens,
+ *             n_seqs, H, Hkv, D) bytes, zeroed once before its first use. */
+size_t bw_attn_paged_prefill_workspace_bytes(int n_tokens, int n_seqs, int H,
+                                             int Hkv, int D);
+bw_status bw_attn_paged_prefill(const bw_bf16 *q, int64_t q_ld, int n_tokens,
+                                const int *q_start, int H,
+                                const bw_paged_kv *kv, float scale, int window,
+                                int sinks, bw_bf16 *out, int64_t out_ld,
+                                void *workspace, size_t workspace_bytes,
+                                bw_stream_t stream);
+
 /* bw_device_error -- reads and clears the library's device error word.
  * Kernels that wait on an mbarrier or poll for another CTA's data bound
  * every wait (about one second); a wait that runs out sets a bit here and
@@ -491,9 +634,10 @@ bw_status bw_attn_decode_ex(const bw_bf16 *qkv, const int *pos, int H,
  * and 64 are the self-test's).  Bit 16: bw_attn_decode was given a position
  * outside its cache.  Bit 128: bw_attn_decode_ex with BW_ATTN_PAST_READY
  * read a different position after its dependency wait than before it (the
- * promise was broken; the call used the later one).
- * Returns BW_ERR_TIMEOUT if any bit other than 16 and 128 was set, else
- * BW_ERR_INVALID_ARG if bit 16 or 128 was, else BW_OK; *bits receives the
+ * promise was broken; the call used the later one).  Bit 256: a call over
+ * a paged cache met a bad length, token range or page number.
+ * Returns BW_ERR_TIMEOUT if any bit other than 16, 128 and 256 was set, else
+ * BW_ERR_INVALID_ARG if one of these was, else BW_OK; *bits receives the
  * word.
  * SYNCHRONISES `stream`; not for the hot path. */
 bw_status bw_device_error(unsigned int *bits, bw_stream_t stream);
