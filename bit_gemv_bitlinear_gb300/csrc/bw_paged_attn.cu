@@ -87,12 +87,7 @@ cudaError_t launch(const PagedView &v, const PagedAttnLaunch &l,
 
 }  // namespace
 
-size_t paged_decode_workspace_bytes(int, int, int, int) { return 16; }
 size_t paged_prefill_workspace_bytes(int, int, int, int, int) { return 16; }
-cudaError_t launch_paged_decode(const PagedView &v, const PagedAttnLaunch &l,
-                                cudaStream_t stream) {
-  return launch(v, l, stream);
-}
 cudaError_t launch_paged_prefill(const PagedView &v, const PagedAttnLaunch &l,
                                  cudaStream_t stream) {
   return launch(v, l, stream);

@@ -1,0 +1,718 @@
+// bw_paged_decode.cu -- attention of one new token per sequence over a paged
+// key-value cache, split over the cache's length and joined.
+//
+// Sources: "BitNet GPU 推理框架：从零构建 W2A8 的 2-bit 大模型 CUDA GEMV 内核",
+// §一 (grouped key-value heads), §六 item 2 (a preallocated KV cache and a
+// flash path).
+//
+// Mathematics, per sequence and key-value head, for its G query heads: over
+// any set of positions keep m = max s_j, l = sum 2^(s_j - m) and
+// o = sum 2^(s_j - m) v_j with s_j = scale log2(e) q.k_j; two sets join as
+// m = max(m1, m2), l = 2^(m1 - m) l1 + 2^(m2 - m) l2, o likewise; the answer is
+// o / l.
+//
+// Bound by the bytes of the visible keys and values.  Layout:
+//  * Work is cut into tiles of 64 positions of one (sequence, head); all
+//    tiles in order are dealt to the CTAs in equal contiguous shares, found
+//    on the device from the lengths, so ragged batches and long single
+//    sequences balance alike and one launch serves every step of a graph.
+//  * A producer warp looks up the pages and brings a tile's keys and values
+//    into a ring of shared-memory stages with tiled copies (128-byte
+//    swizzle), a lane per box; positions nobody sees are not read.
+//  * Four warps take 16 positions each: scores K Q^T with the heads as the 8
+//    columns of an mma.sync, a running softmax in registers, and V^T P^T with
+//    the weights transposed in registers (movmatrix).  mma.sync and not
+//    tcgen05: with at most 16 heads a 128-row tile would be mostly empty, and
+//    the weights stay in registers.  Heads as columns: half the products of
+//    heads as the 16 rows.  The weights enter as a sum of two (bf16 output)
+//    or three (fp32 output) bf16 values, so an fp32 result keeps fp32
+//    precision.
+//  * At the end of a share's part of a (sequence, head) the warps join in
+//    shared memory.  A part that is the whole goes straight to the output;
+//    others go to the workspace, and the CTA that finishes last (a fence and
+//    a counter; nothing waits) joins them in order and sets the counter back.
+#include "bw_paged_tc.cuh"
+
+namespace bw {
+namespace {
+
+constexpr int kDcWarps = 4;                      // consumers
+constexpr int kDcThreads = (kDcWarps + 1) * 32;  // and the producer
+constexpr int kDcTile = 64;
+constexpr int kDcMaxCtas = 320;
+
+struct DecodeArgs {
+  PagedView v;
+  const __nv_bfloat16 *q;
+  int64_t q_ld;
+  void *out;
+  int64_t out_ld;
+  float *part;          // [2 kDcMaxCtas][part_floats(G, D)]
+  unsigned int *count;  // [n_seqs][Hkv]
+  int H, G;
+  float scale2;         // scale log2(e)
+  int window, sinks;
+  int box_rows;
+  int min_tiles;
+};
+
+template <int D, int GH>
+struct DcCfg {
+  static constexpr uint32_t kHalf = kDcTile * 128;        // 64 dims
+  static constexpr uint32_t kKBytes = kHalf * (D / 64);
+  static constexpr uint32_t kStage = 2 * kKBytes;
+  // about 100 KB of stages a CTA and two CTAs an SM; with 16 heads' partial
+  // sums one CTA of twice the stages
+  static constexpr int kStages = (D == 128 ? 3 : 6) * GH;
+  static constexpr int kCtas = GH == 1 ? 2 : 1;
+  static constexpr int kPad = D + 4;                       // floats a row
+  static constexpr uint32_t kDump = kStages * kStage;      // [2][8 GH][kPad]
+  static constexpr uint32_t kDumpBytes = 2u * 8 * GH * kPad * 4;
+  static constexpr uint32_t kMl = kDump + kDumpBytes;      // [4][8 GH] float2
+  static constexpr uint32_t kBars = kMl + kDcWarps * 8 * GH * 8;
+  static constexpr uint32_t kTotal = kBars + 2 * kStages * 8;
+  static constexpr uint32_t kSmem = kTotal + 1024;
+};
+
+__device__ __forceinline__ uint32_t sw128(int row, int dim, uint32_t half) {
+  return uint32_t(dim >> 6) * half + uint32_t(row) * 128u +
+         ((uint32_t((dim & 63) >> 3) ^ uint32_t(row & 7)) << 4);
+}
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile(
+      "ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+      : "r"(addr)
+      : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile(
+      "ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+      : "r"(addr)
+      : "memory");
+}
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4],
+                                         uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 "
+      "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// The transpose of an 8 x 8 matrix of 16-bit values in fragment layout (lane
+// l: row l / 4, columns 2 (l mod 4) and the next).
+__device__ __forceinline__ uint32_t transpose8(uint32_t a) {
+  uint32_t d;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;"
+               : "=r"(d)
+               : "r"(a));
+  return d;
+}
+__device__ __forceinline__ void consumers_sync() {
+  asm volatile("bar.sync 1, %0;" ::"n"(kDcWarps * 32) : "memory");
+}
+// (a, b) as a bf16 pair; what the rounding leaves goes back into a and b.
+__device__ __forceinline__ uint32_t take_bf16(float &a, float &b) {
+  const __nv_bfloat162 t = __floats2bfloat162_rn(a, b);
+  a -= __low2float(t);
+  b -= __high2float(t);
+  return *reinterpret_cast<const uint32_t *>(&t);
+}
+
+// The tiles of sequence b per key-value head, and its plan.
+__device__ __forceinline__ TilePlan seq_plan(int len, int window, int sinks) {
+  if (len <= 0) return TilePlan{};
+  return tile_plan(len - 1, len - 1, window, sinks, kDcTile);
+}
+
+// A CTA's share, tiles [begin, end) of `total`, and where it starts.
+struct Share {
+  int64_t begin, end, total, item0;  // item0: first tile of sequence b
+  int b, n_ctas;
+};
+
+// The (sequence, head) items of a share, in order.
+struct Item {
+  int b, g, len;
+  TilePlan plan;
+  int64_t first;  // first tile of the item
+};
+
+// Both return false past the last sequence, which only lengths that change
+// under the call can bring about.
+__device__ __forceinline__ bool item_start(const DecodeArgs &a, const Share &s,
+                                           int64_t at, Item &it) {
+  // at: a tile of the share within sequence s.b or a later one
+  int64_t base = s.item0;
+  for (it.b = s.b; it.b < a.v.n_seqs; ++it.b) {
+    it.len = seq_len(a.v, it.b);
+    it.plan = seq_plan(it.len, a.window, a.sinks);
+    const int64_t n = int64_t(it.plan.n) * a.v.hkv;
+    if (at < base + n) {
+      it.g = int((at - base) / it.plan.n);
+      it.first = base + int64_t(it.g) * it.plan.n;
+      return true;
+    }
+    base += n;
+  }
+  return false;
+}
+__device__ __forceinline__ bool item_next(const DecodeArgs &a, Item &it) {
+  it.first += it.plan.n;
+  if (++it.g < a.v.hkv) return true;
+  it.g = 0;
+  for (++it.b; it.b < a.v.n_seqs; ++it.b) {
+    it.len = seq_len(a.v, it.b);
+    it.plan = seq_plan(it.len, a.window, a.sinks);
+    if (it.plan.n > 0) return true;
+  }
+  return false;
+}
+// Floats of a part in the workspace: o [G][D], then (m, l) [G], padded so that
+// every part is 16-byte aligned.
+__host__ __device__ constexpr int part_floats(int G, int D) {
+  return (G * (D + 2) + 3) / 4 * 4;
+}
+
+__device__ __forceinline__ int owner_of(const Share &s, int64_t tile) {
+  return int(((tile + 1) * s.n_ctas - 1) / s.total);
+}
+
+template <int D, int GH, bool BF16>
+__global__ void __launch_bounds__(kDcThreads, (DcCfg<D, GH>::kCtas))
+decode_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap kmap,
+              const __grid_constant__ CUtensorMap vmap) {
+  using C = DcCfg<D, GH>;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t *smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
+  uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::kBars);
+  uint64_t *empty = full + C::kStages;
+  __shared__ Share s_share;
+  __shared__ long long s_sum[kDcThreads / 32];
+  __shared__ int s_last;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) {
+    prefetch_map(&kmap);
+    prefetch_map(&vmap);
+    for (int i = 0; i < C::kStages; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], kDcWarps);
+    }
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    s_share.b = -1;
+  }
+  pdl_wait();
+  pdl_trigger();
+
+  // ---- every CTA finds its share: thread t counts the tiles of sequences
+  // [t per, (t + 1) per), a scan over the CTA gives their first tiles ----
+  const int per = (a.v.n_seqs + kDcThreads - 1) / kDcThreads;
+  const int b_lo = min(tid * per, a.v.n_seqs);
+  const int b_hi = min(b_lo + per, a.v.n_seqs);
+  long long mine = 0;
+  for (int b = b_lo; b < b_hi; ++b) {
+    const int len = seq_len(a.v, b);
+    mine += int64_t(seq_plan(len, a.window, a.sinks).n) * a.v.hkv;
+    if (len <= 0 && b % int(gridDim.x) == int(blockIdx.x)) {
+      // an empty sequence: zeros
+      for (int e = 0; e < a.H * D; e += 8) {
+        const int64_t at = int64_t(b) * a.out_ld + e;
+        const uint4 z = make_uint4(0u, 0u, 0u, 0u);
+        if (BF16) {
+          *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + at) = z;
+        } else {
+          *reinterpret_cast<uint4 *>(static_cast<float *>(a.out) + at) = z;
+          *reinterpret_cast<uint4 *>(static_cast<float *>(a.out) + at + 4) = z;
+        }
+      }
+    }
+  }
+  long long incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long t = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += t;
+  }
+  if (lane == 31) s_sum[warp] = incl;
+  __syncthreads();
+  long long before = incl - mine, total = 0;
+#pragma unroll
+  for (int w = 0; w < kDcThreads / 32; ++w) {
+    if (w < warp) before += s_sum[w];
+    total += s_sum[w];
+  }
+  long long n_ctas = (total + a.min_tiles - 1) / a.min_tiles;
+  if (n_ctas > gridDim.x) n_ctas = gridDim.x;
+  if (blockIdx.x >= n_ctas) return;  // the whole CTA, also without any tile
+  const long long begin = blockIdx.x * total / n_ctas;
+  const long long end = (blockIdx.x + 1) * total / n_ctas;
+  if (begin >= before && begin < before + mine)
+    s_share = Share{begin, end, total, before, b_lo, int(n_ctas)};
+  __syncthreads();
+  const Share sh = s_share;
+  if (sh.b < 0) return;  // lengths that changed under the call
+
+  if (warp == kDcWarps) {
+    // ---- producer ----
+    // Lane i copies box i of a tile (at most 16: 4 page parts, 2 halves, keys
+    // and values).  A tile's pages are looked up while the one before it
+    // waits for its stage: the lookup takes as long as a fifth of a stage's
+    // copy.
+    const int per_kv = (kDcTile / a.box_rows) * (D / 64);
+    const bool is_v = lane >= per_kv;
+    const int j = is_v ? lane - per_kv : lane;
+    const int half = j % (D / 64), r0 = j / (D / 64) * a.box_rows;
+    const uint32_t dst = (is_v ? C::kKBytes : 0u) + half * C::kHalf + r0 * 128;
+    const bool mine_box = lane < 2 * per_kv;
+    Item it;
+    int stage = 0;
+    uint32_t round = 0;
+    bool ok = item_start(a, sh, sh.begin, it);
+    int64_t t = sh.begin;
+    int pos = 0, page = 0;
+    auto look_up = [&] {
+      pos = tile_pos(it.plan, int(t - it.first), kDcTile) + r0;
+      page = mine_box ? box_page(a.v, it.b, pos, a.box_rows, it.plan.s1,
+                                 it.plan.lo, it.len)
+                      : 0;
+    };
+    if (ok) look_up();
+    while (ok && t < sh.end) {
+      if (round > 0 && !warp_wait(&empty[stage], (round - 1) & 1u)) {
+        ok = false;
+        break;
+      }
+      if (lane == 0) mbar_arrive_expect_tx(&full[stage], C::kStage);
+      __syncwarp();
+      if (mine_box)
+        tma_load_4d(smem + stage * C::kStage + dst, is_v ? &vmap : &kmap,
+                    half * 64, pos & ((1 << a.v.page_shift) - 1), it.g, page,
+                    &full[stage]);
+      if (++stage == C::kStages) {
+        stage = 0;
+        ++round;
+      }
+      if (++t == sh.end) break;
+      if (t >= it.first + it.plan.n && !item_next(a, it)) {
+        ok = false;
+        break;
+      }
+      look_up();
+    }
+    // The stages in flight land before the CTA may leave (only after a
+    // time-out are they not consumed first).
+    if (!ok) {
+      if (lane == 0) atomicOr(a.v.err, 4u);
+      const int64_t done = int64_t(round) * C::kStages + stage;
+      for (int64_t i = done > C::kStages ? done - C::kStages : 0; i < done; ++i)
+        if (!warp_wait(&full[i % C::kStages], uint32_t(i / C::kStages) & 1u) &&
+            lane == 0)
+          atomicOr(a.v.err, 2u);
+    }
+    return;
+  }
+
+  // ---- consumers: 16 positions of every tile a warp ----
+  const int fr = lane >> 2, fc = (lane & 3) * 2;  // fragment row, column pair
+  const int G = a.G;
+  float *dump = reinterpret_cast<float *>(smem + C::kDump);
+  float2 *ml = reinterpret_cast<float2 *>(smem + C::kMl);
+  Item it;
+  int stage = 0;
+  uint32_t round = 0;
+  int64_t t = sh.begin;
+  // After a wait that ran out (never expected; reported, the result is lost)
+  // a warp goes through the rest without waiting, so that no barrier of the
+  // CTA and no counter is left short.
+  bool ok = true;
+  bool more = item_start(a, sh, sh.begin, it);
+  while (more && t < sh.end) {
+    const int64_t part_end = min(sh.end, it.first + it.plan.n);
+    const bool from_start = t == it.first;
+    // the queries of this head group as B fragments (columns past G: zero)
+    uint32_t qf[GH][D / 16][2];
+    {
+      const __nv_bfloat16 *q0 =
+          a.q + int64_t(it.b) * a.q_ld + int64_t(it.g) * G * D;
+#pragma unroll
+      for (int nt = 0; nt < GH; ++nt)
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+#pragma unroll
+          for (int u = 0; u < 2; ++u)
+            qf[nt][kk][u] =
+                8 * nt + fr < G
+                    ? __ldcg(reinterpret_cast<const unsigned int *>(
+                          q0 + (8 * nt + fr) * D + 16 * kk + fc + 8 * u))
+                    : 0u;
+    }
+    // Output^T: rows dims 16 i + fr (+ 8), columns heads 8 nt + fc (+ 1);
+    // maximum and sum of those two heads.
+    float o[GH][D / 16][4] = {};
+    float m[GH][2], l[GH][2];
+#pragma unroll
+    for (int nt = 0; nt < GH; ++nt) {
+      m[nt][0] = m[nt][1] = -INFINITY;
+      l[nt][0] = l[nt][1] = 0.0f;
+    }
+    for (; t < part_end; ++t) {
+      const int pos = tile_pos(it.plan, int(t - it.first), kDcTile) + 16 * warp;
+      if (ok && !warp_wait(&full[stage], round & 1u)) {
+        if (lane == 0) atomicOr(a.v.err, 4u);
+        ok = false;
+      }
+      const int s1 = it.plan.s1, lo = it.plan.lo, hi = it.len;
+      auto sees = [&](int j) { return j < hi && (j >= lo || j < s1); };
+      const bool all = pos >= lo && pos + 16 <= hi;
+      const bool none = pos >= hi || (pos >= s1 && pos + 16 <= lo);
+      uint8_t *ks = smem + stage * C::kStage;
+      uint8_t *vs = ks + C::kKBytes;
+      if (!none && ok) {
+        float c[GH][2][4] = {};  // even and odd steps: shorter chains
+        const int krow = 16 * warp + (lane & 15);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          uint32_t ka[4];
+          ldsm4(smem_addr(ks) + sw128(krow, 16 * kk + 8 * (lane >> 4), C::kHalf),
+                ka);
+#pragma unroll
+          for (int nt = 0; nt < GH; ++nt)
+            mma16816(c[nt][kk & 1], ka, qf[nt][kk][0], qf[nt][kk][1]);
+        }
+        if (!all) {
+          // what nobody sees: no weight, and zeros for values (a NaN there
+          // would not vanish)
+          const bool see0 = sees(pos + fr), see1 = sees(pos + fr + 8);
+#pragma unroll
+          for (int nt = 0; nt < GH; ++nt) {
+            if (!see0) c[nt][0][0] = c[nt][0][1] = -INFINITY, c[nt][1][0] = c[nt][1][1] = 0.0f;
+            if (!see1) c[nt][0][2] = c[nt][0][3] = -INFINITY, c[nt][1][2] = c[nt][1][3] = 0.0f;
+          }
+          for (int e = lane; e < 16 * (D / 8); e += 32) {
+            const int r = e / (D / 8), d = (e % (D / 8)) * 8;
+            if (!sees(pos + r))
+              *reinterpret_cast<uint4 *>(vs + sw128(16 * warp + r, d, C::kHalf)) =
+                  make_uint4(0u, 0u, 0u, 0u);
+          }
+          __syncwarp();
+        }
+        constexpr int kTerms = BF16 ? 2 : 3;
+        uint32_t pb[GH][kTerms][2];  // the weights as B fragments
+#pragma unroll
+        for (int nt = 0; nt < GH; ++nt) {
+          float w[4];
+#pragma unroll
+          for (int u = 0; u < 4; ++u) w[u] = c[nt][0][u] + c[nt][1][u];
+          // ---- running softmax of heads fc, fc + 1 ----
+          float mn[2];
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            float mx = fmaxf(w[u], w[2 + u]);
+#pragma unroll
+            for (int off = 4; off < 32; off <<= 1)
+              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+            mn[u] = fmaxf(m[nt][u], mx * a.scale2);
+          }
+          if (__any_sync(0xffffffffu, mn[0] != m[nt][0] || mn[1] != m[nt][1])) {
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              const float f = mn[u] == -INFINITY ? 1.0f : ex2(m[nt][u] - mn[u]);
+              l[nt][u] *= f;
+#pragma unroll
+              for (int i = 0; i < D / 16; ++i) {
+                o[nt][i][u] *= f;
+                o[nt][i][2 + u] *= f;
+              }
+              m[nt][u] = mn[u];
+            }
+          }
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const float mu = m[nt][u] == -INFINITY ? 0.0f : m[nt][u];
+            w[u] = ex2(fmaf(w[u], a.scale2, -mu));
+            w[2 + u] = ex2(fmaf(w[2 + u], a.scale2, -mu));
+            l[nt][u] += w[u] + w[2 + u];
+          }
+#pragma unroll
+          for (int k = 0; k < kTerms; ++k) {
+            pb[nt][k][0] = transpose8(take_bf16(w[0], w[1]));
+            pb[nt][k][1] = transpose8(take_bf16(w[2], w[3]));
+          }
+        }
+        // ---- weights times values ----
+        const int vrow = 16 * warp + ((lane >> 4) << 3) + (lane & 7);
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+          uint32_t va[4];
+          ldsm4t(smem_addr(vs) + sw128(vrow, 16 * i + (((lane >> 3) & 1) << 3),
+                                       C::kHalf),
+                 va);
+#pragma unroll
+          for (int nt = 0; nt < GH; ++nt) {
+            if (BF16) {
+#pragma unroll
+              for (int k = kTerms - 1; k >= 0; --k)
+                mma16816(o[nt][i], va, pb[nt][k][0], pb[nt][k][1]);
+            } else {
+              // The tensor cores' accumulation truncates: over a long axis
+              // that adds up (2e-6 of the result at 131071 positions), so a
+              // tile's product is added to the running one in the fp32 pipe
+              // (4e-7).
+              float x[4] = {};
+#pragma unroll
+              for (int k = kTerms - 1; k >= 0; --k)
+                mma16816(x, va, pb[nt][k][0], pb[nt][k][1]);
+#pragma unroll
+              for (int u = 0; u < 4; ++u) o[nt][i][u] += x[u];
+            }
+          }
+        }
+      }
+      // the stage is refilled by a copy of the asynchronous proxy
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&empty[stage]);
+      if (++stage == C::kStages) {
+        stage = 0;
+        ++round;
+      }
+    }
+
+    // ---- the four warps join: weights for each, then the sums in pairs ----
+#pragma unroll
+    for (int nt = 0; nt < GH; ++nt)
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+#pragma unroll
+        for (int off = 4; off < 32; off <<= 1)
+          l[nt][u] += __shfl_xor_sync(0xffffffffu, l[nt][u], off);
+        if (fr == 0)
+          ml[(warp * GH + nt) * 8 + fc + u] = make_float2(m[nt][u], l[nt][u]);
+      }
+    consumers_sync();
+    float M[GH][2], L[GH][2];
+#pragma unroll
+    for (int nt = 0; nt < GH; ++nt)
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        float2 x[kDcWarps];
+        M[nt][u] = -INFINITY;
+        L[nt][u] = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kDcWarps; ++w) {
+          x[w] = ml[(w * GH + nt) * 8 + fc + u];
+          M[nt][u] = fmaxf(M[nt][u], x[w].x);
+        }
+#pragma unroll
+        for (int w = 0; w < kDcWarps; ++w)
+          if (x[w].x != -INFINITY)
+            L[nt][u] = fmaf(ex2(x[w].x - M[nt][u]), x[w].y, L[nt][u]);
+        const float f = m[nt][u] == -INFINITY ? 0.0f : ex2(m[nt][u] - M[nt][u]);
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+          o[nt][i][u] *= f;
+          o[nt][i][2 + u] *= f;
+        }
+      }
+    // where element u of o[nt][i] lies in a [8 GH][kPad] block
+    auto at = [&](int nt, int i, int u) {
+      return (8 * nt + fc + (u & 1)) * C::kPad + 16 * i + fr + 8 * (u >> 1);
+    };
+#pragma unroll
+    for (int step = 2; step > 0; step >>= 1) {
+      if (warp >= step && warp < 2 * step) {
+        float *to = dump + (warp - step) * 8 * GH * C::kPad;
+#pragma unroll
+        for (int nt = 0; nt < GH; ++nt)
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+            for (int u = 0; u < 4; ++u) to[at(nt, i, u)] = o[nt][i][u];
+      }
+      consumers_sync();
+      if (warp < step) {
+        const float *from = dump + warp * 8 * GH * C::kPad;
+#pragma unroll
+        for (int nt = 0; nt < GH; ++nt)
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+            for (int u = 0; u < 4; ++u) o[nt][i][u] += from[at(nt, i, u)];
+      }
+      consumers_sync();
+    }
+
+    // ---- out, or to the workspace ----
+    const int c0 = owner_of(sh, it.first);
+    const int parts = owner_of(sh, it.first + it.plan.n - 1) - c0 + 1;
+    const int64_t row = int64_t(it.b) * a.out_ld + int64_t(it.g) * G * D;
+    const int stride = part_floats(G, D);
+    if (warp == 0) {
+      float *p = a.part + int64_t(2 * blockIdx.x + (from_start ? 1 : 0)) * stride;
+#pragma unroll
+      for (int nt = 0; nt < GH; ++nt)
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const int h = 8 * nt + fc + u;
+          if (h >= G) continue;
+          if (parts == 1) {
+            const float inv = 1.0f / L[nt][u];
+#pragma unroll
+            for (int i = 0; i < 2 * (D / 16); ++i) {
+              const int64_t e = row + h * D + 8 * i + fr;
+              const float y = o[nt][i >> 1][2 * (i & 1) + u] * inv;
+              if (BF16)
+                static_cast<__nv_bfloat16 *>(a.out)[e] = __float2bfloat16_rn(y);
+              else
+                static_cast<float *>(a.out)[e] = y;
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < 2 * (D / 16); ++i)
+              p[h * D + 8 * i + fr] = o[nt][i >> 1][2 * (i & 1) + u];
+            if (fr == 0)
+              *reinterpret_cast<float2 *>(p + G * D + 2 * h) =
+                  make_float2(M[nt][u], L[nt][u]);
+          }
+        }
+    }
+    if (parts > 1) {
+      if (warp == 0) {
+        __threadfence();
+        __syncwarp();
+        if (lane == 0) {
+          unsigned int *cnt = a.count + int64_t(it.b) * a.v.hkv + it.g;
+          const bool last = atomicAdd(cnt, 1u) == unsigned(parts) - 1u;
+          if (last) *cnt = 0u;
+          s_last = last;
+        }
+      }
+      consumers_sync();
+      if (s_last) {
+        // The first part's slot is 2 c0 + 1, the others' 2 c.
+        __threadfence();
+        for (int e = tid; e < G * D / 4; e += kDcWarps * 32) {
+          const int h = e / (D / 4);
+          auto slot = [&](int i) {
+            return a.part + int64_t(2 * (c0 + i) + (i == 0 ? 1 : 0)) * stride;
+          };
+          float mx = -INFINITY;
+#pragma unroll 8
+          for (int i = 0; i < parts; ++i)
+            mx = fmaxf(mx, __ldcg(slot(i) + G * D + 2 * h));
+          float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          float sum = 0.0f;
+#pragma unroll 8
+          for (int i = 0; i < parts; ++i) {
+            const float *p = slot(i);
+            const float2 x = __ldcg(reinterpret_cast<const float2 *>(p + G * D + 2 * h));
+            const float4 y = __ldcg(reinterpret_cast<const float4 *>(p + 4 * e));
+            const float w = x.x == -INFINITY ? 0.0f : ex2(x.x - mx);
+            sum = fmaf(w, x.y, sum);
+            acc.x = fmaf(w, y.x, acc.x);
+            acc.y = fmaf(w, y.y, acc.y);
+            acc.z = fmaf(w, y.z, acc.z);
+            acc.w = fmaf(w, y.w, acc.w);
+          }
+          const float inv = 1.0f / sum;
+          const int64_t at = row + 4 * e;
+          if (BF16) {
+            const __nv_bfloat162 y0 = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
+            const __nv_bfloat162 y1 = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
+            uint2 w;
+            w.x = *reinterpret_cast<const uint32_t *>(&y0);
+            w.y = *reinterpret_cast<const uint32_t *>(&y1);
+            *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.out) + at) = w;
+          } else {
+            *reinterpret_cast<float4 *>(static_cast<float *>(a.out) + at) =
+                make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+          }
+        }
+      }
+      consumers_sync();  // s_last is read before it is written again
+    }
+    if (t < sh.end) more = item_next(a, it);
+  }
+}
+
+size_t align256(size_t b) { return (b + 255) / 256 * 256; }
+
+size_t part_bytes(int G, int D) {
+  return align256(size_t(2) * kDcMaxCtas * part_floats(G, D) * sizeof(float));
+}
+
+template <int D, int GH, bool BF16>
+cudaError_t launch_t(const DecodeArgs &a, const CUtensorMap &kmap,
+                     const CUtensorMap &vmap, cudaStream_t stream) {
+  static std::atomic<int> cached[64];
+  int resident = 0;
+  const cudaError_t e =
+      paged_resident(decode_kernel<D, GH, BF16>, cached, kDcThreads,
+                     DcCfg<D, GH>::kSmem, &resident);
+  if (e != cudaSuccess) return e;
+  // Shares of at least min_tiles tiles: more CTAs than that have nothing to
+  // do, however long the sequences may be.
+  int64_t ctas = resident < kDcMaxCtas ? resident : kDcMaxCtas;
+  const int64_t most = int64_t(a.v.n_seqs) * a.v.hkv *
+                       ((int64_t(a.v.max_pages) << a.v.page_shift) / kDcTile + 1);
+  const int64_t useful = (most + a.min_tiles - 1) / a.min_tiles;
+  if (ctas > useful) ctas = useful;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(ctas));
+  cfg.blockDim = dim3(kDcThreads);
+  cfg.dynamicSmemBytes = DcCfg<D, GH>::kSmem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, decode_kernel<D, GH, BF16>, a, kmap, vmap);
+}
+
+template <int D>
+cudaError_t launch_d(const DecodeArgs &a, const CUtensorMap &kmap,
+                     const CUtensorMap &vmap, bool bf16, cudaStream_t stream) {
+  if (a.G <= 8)
+    return bf16 ? launch_t<D, 1, true>(a, kmap, vmap, stream)
+                : launch_t<D, 1, false>(a, kmap, vmap, stream);
+  return bf16 ? launch_t<D, 2, true>(a, kmap, vmap, stream)
+              : launch_t<D, 2, false>(a, kmap, vmap, stream);
+}
+
+}  // namespace
+
+size_t paged_decode_workspace_bytes(int n_seqs, int H, int Hkv, int D) {
+  return part_bytes(H / Hkv, D) +
+         align256(size_t(n_seqs) * Hkv * sizeof(unsigned int));
+}
+
+cudaError_t launch_paged_decode(const PagedView &v, const PagedAttnLaunch &l,
+                                cudaStream_t stream) {
+  DecodeArgs a{};
+  a.v = v;
+  a.q = l.q;
+  a.q_ld = l.q_ld;
+  a.out = l.out;
+  a.out_ld = l.out_ld;
+  a.H = l.H;
+  a.G = l.H / v.hkv;
+  a.part = static_cast<float *>(l.workspace);
+  a.count = reinterpret_cast<unsigned int *>(
+      static_cast<uint8_t *>(l.workspace) + part_bytes(a.G, l.D));
+  a.scale2 = l.scale * kLog2e;
+  a.window = l.window;
+  a.sinks = l.sinks;
+  const int page = 1 << v.page_shift;
+  a.box_rows = page < kDcTile ? page : kDcTile;
+  a.min_tiles = 1;
+  CUtensorMap kmap, vmap;
+  if (!encode_pool(&kmap, v.k, v, l.D, a.box_rows) ||
+      !encode_pool(&vmap, v.v, v, l.D, a.box_rows))
+    return cudaErrorInvalidValue;
+  return l.D == 64 ? launch_d<64>(a, kmap, vmap, l.out_bf16, stream)
+                   : launch_d<128>(a, kmap, vmap, l.out_bf16, stream);
+}
+
+}  // namespace bw
