@@ -73,6 +73,24 @@ __device__ __forceinline__ SeqTokens seq_tokens(const PagedView &v,
   return r;
 }
 
+// The sequence of row t: the last b with q_start[b] <= t (0 if none), by 32
+// probes at a time.  Every lane of the warp gets it.
+__device__ __forceinline__ int find_seq(const int *q_start, int n_seqs,
+                                        int t) {
+  int lo = 0, n = n_seqs;  // the answer lies in [lo, lo + n)
+  const int lane = threadIdx.x & 31;
+  while (n > 1) {
+    const int step = (n + 31) / 32;
+    const int i = lane * step;
+    const bool le = i < n && __ldcg(q_start + lo + i) <= t;
+    const unsigned m = __ballot_sync(0xffffffffu, le);
+    const int last = m ? 31 - __clz(m) : 0;
+    lo += last * step;
+    n = min(step, n - last * step);
+  }
+  return lo;
+}
+
 // ---- host side (bw_paged_api.cu checks the arguments) ----
 PagedView paged_view(const bw_paged_kv &kv);
 

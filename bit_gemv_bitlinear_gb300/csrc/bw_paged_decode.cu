@@ -66,8 +66,15 @@ struct DcCfg {
   static constexpr int kStages = (D == 128 ? 3 : 6) * GH;
   static constexpr int kCtas = GH == 1 ? 2 : 1;
   static constexpr int kPad = D + 4;                       // floats a row
-  static constexpr uint32_t kDump = kStages * kStage;      // [2][8 GH][kPad]
-  static constexpr uint32_t kDumpBytes = 2u * 8 * GH * kPad * 4;
+  // the warps' sums [2][8 GH][kPad]; the last CTA's (m, l) and lanes' sums
+  static constexpr int kMlMax = 512 * GH;
+  static constexpr uint32_t kDump = kStages * kStage;
+  static constexpr uint32_t kSums = kDump + kMlMax * 8;
+  static constexpr uint32_t kSumsBytes = kDcWarps * 32 * 20;
+  static constexpr uint32_t kDumpBytes =
+      2u * 8 * GH * kPad * 4 > kMlMax * 8 + kSumsBytes
+          ? 2u * 8 * GH * kPad * 4
+          : kMlMax * 8 + kSumsBytes;
   static constexpr uint32_t kMl = kDump + kDumpBytes;      // [4][8 GH] float2
   static constexpr uint32_t kBars = kMl + kDcWarps * 8 * GH * 8;
   static constexpr uint32_t kTotal = kBars + 2 * kStages * 8;
@@ -130,6 +137,7 @@ __device__ __forceinline__ TilePlan seq_plan(int len, int window, int sinks) {
 struct Share {
   int64_t begin, end, total, item0;  // item0: first tile of sequence b
   int b, n_ctas;
+  int len;  // sequence b's
 };
 
 // The (sequence, head) items of a share, in order.
@@ -146,7 +154,7 @@ __device__ __forceinline__ bool item_start(const DecodeArgs &a, const Share &s,
   // at: a tile of the share within sequence s.b or a later one
   int64_t base = s.item0;
   for (it.b = s.b; it.b < a.v.n_seqs; ++it.b) {
-    it.len = seq_len(a.v, it.b);
+    it.len = it.b == s.b ? s.len : seq_len(a.v, it.b);
     it.plan = seq_plan(it.len, a.window, a.sinks);
     const int64_t n = int64_t(it.plan.n) * a.v.hkv;
     if (at < base + n) {
@@ -211,8 +219,10 @@ decode_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap kmap,
   const int b_lo = min(tid * per, a.v.n_seqs);
   const int b_hi = min(b_lo + per, a.v.n_seqs);
   long long mine = 0;
+  int len0 = 0;
   for (int b = b_lo; b < b_hi; ++b) {
     const int len = seq_len(a.v, b);
+    if (b == b_lo) len0 = len;
     mine += int64_t(seq_plan(len, a.window, a.sinks).n) * a.v.hkv;
     if (len <= 0 && b % int(gridDim.x) == int(blockIdx.x)) {
       // an empty sequence: zeros
@@ -248,7 +258,7 @@ decode_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap kmap,
   const long long begin = blockIdx.x * total / n_ctas;
   const long long end = (blockIdx.x + 1) * total / n_ctas;
   if (begin >= before && begin < before + mine)
-    s_share = Share{begin, end, total, before, b_lo, int(n_ctas)};
+    s_share = Share{begin, end, total, before, b_lo, int(n_ctas), len0};
   __syncthreads();
   const Share sh = s_share;
   if (sh.b < 0) return;  // lengths that changed under the call
@@ -590,43 +600,95 @@ decode_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap kmap,
       }
       consumers_sync();
       if (s_last) {
-        // The first part's slot is 2 c0 + 1, the others' 2 c.
+        // The first part's slot is 2 c0 + 1, the others' 2 c.  Thread (vector
+        // v, lane gi) sums the parts gi, gi + ng, ... of four outputs; (m, l)
+        // of up to kMlMax / G parts at a time lie in shared memory, and 16
+        // outputs' loads are in flight at once (the first before the maximum
+        // is known).
         __threadfence();
-        for (int e = tid; e < G * D / 4; e += kDcWarps * 32) {
-          const int h = e / (D / 4);
-          auto slot = [&](int i) {
-            return a.part + int64_t(2 * (c0 + i) + (i == 0 ? 1 : 0)) * stride;
-          };
-          float mx = -INFINITY;
-#pragma unroll 8
-          for (int i = 0; i < parts; ++i)
-            mx = fmaxf(mx, __ldcg(slot(i) + G * D + 2 * h));
+        const int nv = G * D / 4, ng = nv >= kDcWarps * 32 ? 1 : kDcWarps * 32 / nv;
+        const int chunk = C::kMlMax / G;
+        float2 *mlc = reinterpret_cast<float2 *>(dump);
+        float4 *sums = reinterpret_cast<float4 *>(smem + C::kSums);
+        float *sums_l = reinterpret_cast<float *>(sums + kDcWarps * 32);
+        auto slot = [&](int i) {
+          return a.part + int64_t(2 * (c0 + i) + (i == 0 ? 1 : 0)) * stride;
+        };
+        for (int v0 = 0; v0 < nv; v0 += kDcWarps * 32) {
+          const int gi = tid / nv, v = v0 + tid - gi * nv;
+          const bool on = v < nv && gi < ng;
+          const int h = on ? v / (D / 4) : 0;
           float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-          float sum = 0.0f;
+          float sum = 0.0f, mx = -INFINITY;
+          for (int p0 = 0; p0 < parts; p0 += chunk) {
+            const int n = min(chunk, parts - p0);
+            float4 x[16];
+            auto load = [&](int i0) {
+#pragma unroll
+              for (int u = 0; u < 16; ++u)
+                if (on && i0 + u * ng < n)
+                  x[u] = __ldcg(reinterpret_cast<const float4 *>(
+                                    slot(p0 + i0 + u * ng)) + v);
+            };
+            load(gi);
+            for (int e = tid; e < n * G; e += kDcWarps * 32)
+              mlc[e] = __ldcg(reinterpret_cast<const float2 *>(
+                                  slot(p0 + e / G) + G * D) + e % G);
+            consumers_sync();
+            const float m_old = mx;
 #pragma unroll 8
-          for (int i = 0; i < parts; ++i) {
-            const float *p = slot(i);
-            const float2 x = __ldcg(reinterpret_cast<const float2 *>(p + G * D + 2 * h));
-            const float4 y = __ldcg(reinterpret_cast<const float4 *>(p + 4 * e));
-            const float w = x.x == -INFINITY ? 0.0f : ex2(x.x - mx);
-            sum = fmaf(w, x.y, sum);
-            acc.x = fmaf(w, y.x, acc.x);
-            acc.y = fmaf(w, y.y, acc.y);
-            acc.z = fmaf(w, y.z, acc.z);
-            acc.w = fmaf(w, y.w, acc.w);
+            for (int i = 0; i < n; ++i) mx = fmaxf(mx, mlc[i * G + h].x);
+            const float f = m_old == -INFINITY ? 0.0f : ex2(m_old - mx);
+            sum *= f;
+            acc.x *= f;
+            acc.y *= f;
+            acc.z *= f;
+            acc.w *= f;
+            for (int i0 = gi; i0 < n; i0 += 16 * ng) {
+              if (i0 != gi) load(i0);
+#pragma unroll
+              for (int u = 0; u < 16; ++u) {
+                const int i = i0 + u * ng;
+                if (i >= n) break;
+                const float2 y = mlc[i * G + h];
+                const float w = y.x == -INFINITY ? 0.0f : ex2(y.x - mx);
+                sum = fmaf(w, y.y, sum);
+                acc.x = fmaf(w, x[u].x, acc.x);
+                acc.y = fmaf(w, x[u].y, acc.y);
+                acc.z = fmaf(w, x[u].z, acc.z);
+                acc.w = fmaf(w, x[u].w, acc.w);
+              }
+            }
+            consumers_sync();
           }
-          const float inv = 1.0f / sum;
-          const int64_t at = row + 4 * e;
-          if (BF16) {
-            const __nv_bfloat162 y0 = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
-            const __nv_bfloat162 y1 = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
-            uint2 w;
-            w.x = *reinterpret_cast<const uint32_t *>(&y0);
-            w.y = *reinterpret_cast<const uint32_t *>(&y1);
-            *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.out) + at) = w;
-          } else {
-            *reinterpret_cast<float4 *>(static_cast<float *>(a.out) + at) =
-                make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+          if (ng > 1) {
+            sums[tid] = acc;
+            sums_l[tid] = sum;
+            consumers_sync();
+            if (gi == 0)
+              for (int k = 1; k < ng; ++k) {
+                const float4 y = sums[k * nv + v];
+                acc.x += y.x;
+                acc.y += y.y;
+                acc.z += y.z;
+                acc.w += y.w;
+                sum += sums_l[k * nv + v];
+              }
+          }
+          if (on && gi == 0) {
+            const float inv = 1.0f / sum;
+            const int64_t e = row + 4 * v;
+            if (BF16) {
+              const __nv_bfloat162 y0 = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
+              const __nv_bfloat162 y1 = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
+              uint2 w;
+              w.x = *reinterpret_cast<const uint32_t *>(&y0);
+              w.y = *reinterpret_cast<const uint32_t *>(&y1);
+              *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.out) + e) = w;
+            } else {
+              *reinterpret_cast<float4 *>(static_cast<float *>(a.out) + e) =
+                  make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+            }
           }
         }
       }
