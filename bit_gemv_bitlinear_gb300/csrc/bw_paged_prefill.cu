@@ -5,13 +5,13 @@
 // §一 (prefill and decode as separate paths, grouped key-value heads), §六
 // item 2 (a preallocated KV cache and a flash path).
 //
-// Mathematics, per token and head: a running m >= max s_j - 8, l = sum
-// 2^(s_j - m), o = sum 2^(s_j - m) v_j over the visible positions, with s_j =
-// scale log2(e) q.k_j; the answer is o / l.  m follows the maximum only when
-// that grows by more than 8 (a factor of 2^8, harmless in fp32 and in bf16's
-// exponent), so the running output is rescaled rarely.  The weights are
-// rounded to bf16 for the second product, like the output; l sums them
-// unrounded in fp32.
+// Mathematics, per token and head: some m, l = sum 2^(s_j - m), o = sum
+// 2^(s_j - m) v_j over the visible positions, with s_j = scale log2(e) q.k_j;
+// the answer is o / l for any m that keeps the sums within range.  m is the
+// maximum of the first positions seen and follows only when weights sum to
+// more than 2^16, so most tiles need no maximum and the running output is
+// rescaled rarely.  The weights are rounded to bf16 for the second product,
+// like the output; l sums them unrounded in fp32.
 //
 // Bound by the tensor cores (4 D flops for each visible pair); few tokens over
 // a long past are bound by the bytes of the past.  Layout:
@@ -19,15 +19,18 @@
 //    key-value head: 128 rows, so every staged key serves all of them and
 //    the causal edge wastes at most 128 columns of TQ tokens.  A CTA takes
 //    two such tiles (2 TQ tokens) against the same keys.
-//  * One producer warp copies the tiles of 128 positions (a lane per page
-//    part), one warp zeroes value rows that nobody sees (what lies there may
-//    be NaN), one warp issues tcgen05.mma, and two warpgroups do the
+//  * One producer warp copies the tiles of 64 positions (a lane per page
+//    part), one warp finds the items and zeroes value rows that nobody sees
+//    (what lies there may be NaN), two warps issue tcgen05.mma, and two warpgroups do the
 //    softmax, a thread per row: S (128 x 128, fp32) is read from tensor
 //    memory, P goes back as bf16 into S's own columns and is the A operand
 //    of the second product; O stays in tensor memory.  While one tile's
 //    softmax runs, the other tile's two products do.
 //  * Values are taken as they lie (positions by dims): the B operand of the
 //    second product in its transposed ("MN-major") form.
+//  * CTAs stay: one per SM, each goes through its items (a scheduler warp
+//    finds them), so the next item's copies and first scores run while the
+//    last one's softmax and output do.
 //  * Where there are too few tiles for the device, the key axis is cut too:
 //    the parts' o and (m, l) go to the workspace and a second kernel joins
 //    them, a warp per row.
@@ -39,13 +42,14 @@ namespace {
 constexpr int kPfTile = 128;       // positions of a key tile
 constexpr int kPfRows = 128;       // rows of a query tile
 constexpr int kPfSoftWarps = 8;    // two warpgroups, one per query tile
-constexpr int kPfMmaWarp = 8;
-constexpr int kPfLoadWarp = 9;
-constexpr int kPfZeroWarp = 10;
+constexpr int kPfMmaWarp = 8;      // and 9: one per query tile
+constexpr int kPfLoadWarp = 10;
+constexpr int kPfItemWarp = 11;     // finds the items, zeroes unseen values
 constexpr int kPfThreads = 384;
 // Registers a thread after the split (launched with 168 each).
-constexpr int kPfSoftRegs = 232;
-constexpr int kPfOtherRegs = 40;
+constexpr int kPfSoftRegs = 224;
+constexpr int kPfOtherRegs = 56;
+constexpr int kPfScan = 256;       // threads that count items
 constexpr int kPfTargetCtas = 152;  // one CTA per SM
 constexpr int kPfMaxSplit = 16;
 constexpr int kPfMinTiles = 4;      // key tiles of a part, at least
@@ -67,12 +71,14 @@ struct PrefillArgs {
 
 template <int D>
 struct PfCfg {
-  static constexpr uint32_t kHalf = 128 * 128;            // 128 rows x 64 dims
+  static constexpr uint32_t kQHalf = kPfRows * 128;       // 128 rows x 64 dims
+  static constexpr uint32_t kQBytes = kQHalf * (D / 64);
+  static constexpr uint32_t kHalf = kPfTile * 128;        // 128 rows x 64 dims
   static constexpr uint32_t kTileBytes = kHalf * (D / 64);
   static constexpr int kKStages = D == 128 ? 3 : 6;
-  static constexpr int kVStages = D == 128 ? 2 : 5;
+  static constexpr int kVStages = D == 128 ? 2 : 4;
   static constexpr uint32_t kQ = 0;                       // two tiles
-  static constexpr uint32_t kK = kQ + 2 * kTileBytes;
+  static constexpr uint32_t kK = kQ + 2 * kQBytes;
   static constexpr uint32_t kV = kK + kKStages * kTileBytes;
   static constexpr uint32_t kBars = kV + kVStages * kTileBytes;
   // barriers
@@ -82,17 +88,43 @@ struct PfCfg {
   static constexpr int kFullV = kEmptyK + kKStages;
   static constexpr int kReadyV = kFullV + kVStages;
   static constexpr int kEmptyV = kReadyV + kVStages;
-  static constexpr int kFullS = kEmptyV + kVStages;       // per query tile
-  static constexpr int kFullP = kFullS + 2;
-  static constexpr int kFullO = kFullP + 2;
-  static constexpr int kNumBars = kFullO + 2;
+  static constexpr int kFullS = kEmptyV + kVStages;       // [query tile]
+  static constexpr int kReadS = kFullS + 2;               // [query tile]
+  static constexpr int kFullP = kReadS + 2;               // [query tile][half]
+  static constexpr int kDoneO = kFullP + 4;               // [query tile]
+  static constexpr int kFullO = kDoneO + 2;               // [query tile], last
+  static constexpr int kEmptyQ = kFullO + 2;
+  static constexpr int kTurn = kEmptyQ + 1;               // [query tile]
+  static constexpr int kFullItem = kTurn + 2;             // two items
+  static constexpr int kEmptyItem = kFullItem + 2;
+  static constexpr int kNumBars = kEmptyItem + 2;
+  // Arrivals: four warps read a tile's S and write its P, both product warps
+  // free a stage and the queries; every warp but the one that finds the items
+  // reads one.
+  __device__ static int count(int i) {
+    if (i >= kReadS && i < kDoneO) return 4;
+    if (i >= kEmptyItem) return kPfThreads / 32 - 1;
+    const bool freed = (i >= kEmptyK && i < kFullV) ||
+                       (i >= kEmptyV && i < kFullS) || i == kEmptyQ;
+    return freed ? 2 : 1;
+  }
   static constexpr uint32_t kTmem = kBars + kNumBars * 8;
-  static constexpr uint32_t kTotal = kTmem + 16;
+  static constexpr uint32_t kItems = kTmem + 16;          // two, 32 bytes each
+  static constexpr uint32_t kBefore = kItems + 64;        // int [kPfScan]
+  static constexpr uint32_t kSums = kBefore + kPfScan * 4;  // int a warp
+  static constexpr uint32_t kTotal = kSums + kPfScan / 32 * 4;
   static constexpr uint32_t kSmem = kTotal + 1024;
-  static_assert(kSmem <= 227 * 1024 - 256, "shared memory");
+  static_assert(kSmem <= 227 * 1024, "shared memory");
   // tensor memory columns
+  // Tensor memory columns (of 512): scores of 128 columns and outputs of D for
+  // each query tile.  Weights take 64: of their own where D leaves room (the
+  // next scores then need not wait for the product that reads them), else
+  // the scores' first ones.
+  static constexpr bool kOwnP = D == 64;
   static constexpr uint32_t kS = 0;                       // + 128 per tile
   static constexpr uint32_t kO = 256;                     // + D per tile
+  static constexpr uint32_t kP = kOwnP ? kO + 2 * D : kS;
+  static constexpr uint32_t kPStep = kOwnP ? 64 : 128;    // per query tile
 };
 
 // Operands in bf16, fp32 accumulators, M = 128, N = n; B as its rows lie in
@@ -159,15 +191,112 @@ __device__ __forceinline__ void tmem_landed(float *v) {
         "+r"(r[30]), "+r"(r[31])::"memory");
 }
 
-// One CTA's work: 2 TQ tokens of one sequence and key-value head, a part of
-// their key tiles.
+// Bits 0 .. n - 1 (none for n <= 0, all for n >= 32).
+__device__ __forceinline__ uint32_t below(int n) {
+  return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, z, w;\n\t"
+      "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "mov.b64 z, {%6, %7};\n\t"
+      "fma.rn.f32x2 w, x, y, z;\n\tmov.b64 {%0, %1}, w;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, w;\n\t"
+      "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "add.rn.f32x2 w, x, y;\n\tmov.b64 {%0, %1}, w;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+// 64 weights 2^(s scale2 - m) as bf16 pairs; their fp32 sum is added to sum.
+// In this order on purpose: the exponentials of four pairs are under way while
+// the four before them are summed and rounded.  360 cycles a warp (256 are the
+// exponentials' own); pair by pair it is 950, each waiting for the last.
+__device__ __forceinline__ void weights64(const float *s, float scale2, float m,
+                                          uint32_t (&w)[32], float2 &sum) {
+  constexpr int kAhead = 4;
+  const float2 sc = make_float2(scale2, scale2), mm = make_float2(-m, -m);
+  float2 e[2][kAhead];
+  float2 acc[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+  auto exponentials = [&](int k) {
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int c = k * kAhead + i;
+      e[k & 1][i] = fma2(make_float2(s[2 * c], s[2 * c + 1]), sc, mm);
+    }
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      e[k & 1][i].x = ex2(e[k & 1][i].x);
+      e[k & 1][i].y = ex2(e[k & 1][i].y);
+    }
+  };
+  exponentials(0);
+#pragma unroll
+  for (int k = 0; k < 32 / kAhead; ++k) {
+    if (k + 1 < 32 / kAhead) exponentials(k + 1);
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const float2 x = e[k & 1][i];
+      const __nv_bfloat162 t = __floats2bfloat162_rn(x.x, x.y);
+      w[k * kAhead + i] = *reinterpret_cast<const uint32_t *>(&t);
+      acc[i & 1] = add2(acc[i & 1], x);
+    }
+  }
+  sum = add2(sum, add2(acc[0], acc[1]));
+}
+
+// One item of work: up to 2 TQ tokens of one sequence and key-value head, a
+// part of their key tiles.
 struct PfItem {
-  int b, g, s;        // sequence, key-value head, part
+  int b, g, s;        // sequence (-1: no more items), key-value head, part
   int row0;           // first token's row
   int n_tok;          // tokens (1 .. 2 TQ)
   int pos0;           // first token's position
-  bool bad;           // a bad sequence: zeros
+  int bad;            // a bad sequence: zeros
 };
+
+// What every role derives from an item: its key tiles j_lo .. j_lo + n - 1 of
+// the plan, of which query tile i takes the first n_i.
+struct PfWork {
+  TilePlan plan;
+  int tok0, tok1;     // tokens of the query tiles
+  int p1;             // the last token's position
+  int j_lo, n, n0, n1;
+};
+__device__ __forceinline__ PfWork pf_work(const PrefillArgs &a, const PfItem &it) {
+  PfWork w;
+  w.tok0 = min(it.n_tok, a.TQ);
+  w.tok1 = it.n_tok - w.tok0;
+  w.p1 = it.pos0 + it.n_tok - 1;
+  w.plan = tile_plan(it.pos0, w.p1, a.window, a.sinks, kPfTile);
+  int parts = w.plan.n / kPfMinTiles;
+  parts = parts < 1 ? 1 : (parts > a.split ? a.split : parts);
+  int j_hi = 0;
+  w.j_lo = 0;
+  if (it.s < parts && !it.bad) {
+    w.j_lo = it.s * w.plan.n / parts;  // 16 parts, 2^18 tiles: within 32 bits
+    j_hi = (it.s + 1) * w.plan.n / parts;
+  }
+  // Tile 0's tokens end earlier: it leaves out key tiles past its last one.
+  const int pe0 = it.pos0 + w.tok0 - 1;
+  const int end0 = min(j_hi, w.plan.n - (w.p1 / kPfTile - pe0 / kPfTile));
+  w.n0 = max(0, end0 - w.j_lo);
+  w.n1 = w.tok1 > 0 ? j_hi - w.j_lo : 0;
+  w.n = max(w.n0, w.n1);
+  return w;
+}
 
 template <int D>
 __global__ void __launch_bounds__(kPfThreads, 1)
@@ -179,30 +308,31 @@ prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap qmap,
   uint8_t *smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
   uint64_t *bar = reinterpret_cast<uint64_t *>(smem + C::kBars);
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::kTmem);
-  __shared__ PfItem s_item;
-  __shared__ int s_sum[kPfThreads / 32];
+  PfItem *items = reinterpret_cast<PfItem *>(smem + C::kItems);  // [2]
+  int *before = reinterpret_cast<int *>(smem + C::kBefore);      // [kPfScan]
+  int *s_sum = reinterpret_cast<int *>(smem + C::kSums);         // [warps]
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int TQ = a.TQ, G = a.G;
 
   if (tid == 0) {
-    for (int i = 0; i < C::kNumBars; ++i)
-      mbar_init(&bar[i], (i == C::kFullP || i == C::kFullP + 1) ? 4 : 1);
+    for (int i = 0; i < C::kNumBars; ++i) mbar_init(&bar[i], C::count(i));
+    mbar_arrive(&bar[C::kTurn]);  // query tile 0 begins
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    s_item.b = -1;
   }
   if (warp == kPfLoadWarp && lane == 0) {
     prefetch_map(&qmap);
     prefetch_map(&kmap);
     prefetch_map(&vmap);
   }
+  if (warp == kPfMmaWarp) tmem_alloc(tmem_slot, 512);
   pdl_wait();
   pdl_trigger();
 
-  // ---- the CTA's item: tiles of all sequences in order, the last (longest)
-  // first, key-value heads and parts of a tile next to each other ----
+  // ---- items of all sequences: thread t counts those of sequences
+  // [t per, (t + 1) per), before[t] is where they begin ----
+  const int per = (a.v.n_seqs + kPfScan - 1) / kPfScan;  // at most 16
   {
-    const int per = (a.v.n_seqs + kPfThreads - 1) / kPfThreads;
-    const int b_lo = min(tid * per, a.v.n_seqs);
+    const int b_lo = tid < kPfScan ? min(tid * per, a.v.n_seqs) : a.v.n_seqs;
     const int b_hi = min(b_lo + per, a.v.n_seqs);
     int mine = 0;
     for (int b = b_lo; b < b_hi; ++b)
@@ -213,233 +343,340 @@ prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap qmap,
       const int x = __shfl_up_sync(0xffffffffu, incl, o);
       if (lane >= o) incl += x;
     }
-    if (lane == 31) s_sum[warp] = incl;
+    if (lane == 31 && tid < kPfScan) s_sum[warp] = incl;
     __syncthreads();
-    int before = incl - mine, total = 0;
+    int at = incl - mine;
 #pragma unroll
-    for (int w = 0; w < kPfThreads / 32; ++w) {
-      if (w < warp) before += s_sum[w];
-      total += s_sum[w];
-    }
-    const int x = int(blockIdx.x) / (a.v.hkv * a.split);
-    const int rest = int(blockIdx.x) - x * (a.v.hkv * a.split);
-    int u = total - 1 - x;  // below 0: no item
-    if (u >= before && u < before + mine) {
-      u -= before;
-      for (int b = b_lo; b < b_hi; ++b) {
-        const SeqTokens t = seq_tokens(a.v, a.q_start, a.n_tokens, b);
-        const int n = (t.n + 2 * TQ - 1) / (2 * TQ);
-        if (u < n) {
-          s_item.g = rest / a.split;
-          s_item.s = rest - s_item.g * a.split;
-          s_item.row0 = t.q0 + u * 2 * TQ;
-          s_item.n_tok = min(2 * TQ, t.n - u * 2 * TQ);
-          s_item.pos0 = t.pos0 + u * 2 * TQ;
-          s_item.bad = t.bad;
-          s_item.b = b;
-          break;
-        }
-        u -= n;
-      }
-    }
-    __syncthreads();
+    for (int w = 0; w < kPfScan / 32; ++w)
+      if (w < warp) at += s_sum[w];
+    if (tid < kPfScan) before[tid] = at;
   }
-  const PfItem it = s_item;
-  if (it.b < 0) return;  // the whole CTA
-  if (it.bad) {
-    if (it.s == 0)
-      for (int e = tid; e < it.n_tok * G * (D / 8); e += kPfThreads) {
-        const int r = e / (D / 8), d = (e - r * (D / 8)) * 8;
-        *reinterpret_cast<uint4 *>(a.out + int64_t(it.row0 + r / G) * a.out_ld +
-                                   (it.g * G + r % G) * D + d) =
-            make_uint4(0u, 0u, 0u, 0u);
-      }
-    return;
-  }
-
-  // ---- the key tiles of this part, per query tile ----
-  const int tok_of[2] = {min(it.n_tok, TQ), max(0, it.n_tok - TQ)};
-  const int p1 = it.pos0 + it.n_tok - 1;
-  const TilePlan plan = tile_plan(it.pos0, p1, a.window, a.sinks, kPfTile);
-  int parts = plan.n / kPfMinTiles;
-  parts = parts < 1 ? 1 : (parts > a.split ? a.split : parts);
-  int j_lo = 0, j_hi = 0;
-  if (it.s < parts) {
-    j_lo = int(int64_t(it.s) * plan.n / parts);
-    j_hi = int(int64_t(it.s + 1) * plan.n / parts);
-  }
-  // Tile 0's tokens end earlier: it leaves out key tiles past its last one.
-  const int pe0 = it.pos0 + tok_of[0] - 1;
-  const int end_of[2] = {min(j_hi, plan.n - (p1 / kPfTile - pe0 / kPfTile)),
-                         tok_of[1] > 0 ? j_hi : 0};
-  const int n_of[2] = {max(0, end_of[0] - j_lo), max(0, end_of[1] - j_lo)};
-  const int n = max(n_of[0], n_of[1]);  // key tiles this CTA visits
-
-  if (warp == kPfMmaWarp) tmem_alloc(tmem_slot, 512);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
+  // The next item, by every role but the scheduler: item k lies in slot k & 1.
+  int k_item = 0;
+  auto next_item = [&](PfItem &it) {
+    const int slot = k_item & 1;
+    if (!warp_wait(&bar[C::kFullItem + slot], uint32_t(k_item >> 1) & 1u)) {
+      if (lane == 0) atomicOr(a.v.err, 4u);
+      return false;
+    }
+    it = items[slot];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bar[C::kEmptyItem + slot]);
+    ++k_item;
+    return it.b >= 0;
+  };
+
   if (warp >= kPfSoftWarps) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPfOtherRegs));
-    if (warp == kPfLoadWarp) {
-      // ---- copies: queries, then keys (one tile ahead) and values ----
-      const int per = (kPfTile / a.box_rows) * (D / 64);  // boxes, at most 16
-      const int half = lane % (D / 64), r0 = lane / (D / 64) * a.box_rows;
-      const bool mine = lane < per;
-      const uint32_t dst = half * C::kHalf + r0 * 128;
-      bool ok = true;
-      if (n > 0) {
-        const uint32_t box = uint32_t(TQ) * G * 128;
-        const int tiles = n_of[1] > 0 ? 2 : 1;
+    if (warp == kPfItemWarp) {
+      // ---- items in order, the last tiles (the longest) of the sequences
+      // first, key-value heads and parts of a tile next to each other; dealt
+      // to the CTAs to and fro, so that each gets long and short ones alike.
+      // One item ahead of the others, and between two items this warp makes
+      // zeros of the value rows that no token of the item sees. ----
+      int total = 0;
+      for (int w = 0; w < kPfScan / 32; ++w) total += s_sum[w];
+      const int n_items = total * a.v.hkv * a.split;  // below 2^23
+      auto find = [&](int k, PfItem &it) {
+        it = PfItem{-1, 0, 0, 0, 0, 0, 0};
+        const int c = (k & 1) ? int(gridDim.x) - 1 - int(blockIdx.x) : int(blockIdx.x);
+        const int idx = k * int(gridDim.x) + c;
+        if (idx >= n_items) return;
+        const int x = idx / (a.v.hkv * a.split);
+        const int rest = idx - x * (a.v.hkv * a.split);
+        int u = total - 1 - x;
+        int below = 0;  // threads whose items begin at or before u
+        for (int t = lane; t < kPfScan; t += 32) below += before[t] <= u;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+          below += __shfl_xor_sync(0xffffffffu, below, o);
+        u -= before[below - 1];
+        const int b = (below - 1) * per + lane;
+        SeqTokens t{0, 0, 0, false};
+        if (lane < per && b < a.v.n_seqs)
+          t = seq_tokens(a.v, a.q_start, a.n_tokens, b);
+        const int n = (t.n + 2 * TQ - 1) / (2 * TQ);
+        int incl = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int y = __shfl_up_sync(0xffffffffu, incl, o);
+          if (lane >= o) incl += y;
+        }
+        // (no lane: lengths that changed under the call; no more items then)
+        const bool mine = u >= incl - n && u < incl;
+        const int v = (u - (incl - n)) * 2 * TQ;
+        const unsigned who = __ballot_sync(0xffffffffu, mine);
+        const int src = who ? __ffs(int(who)) - 1 : 0;
+        it.b = who ? b - lane + src : -1;
+        it.g = rest / a.split;
+        it.s = rest - it.g * a.split;
+        it.row0 = __shfl_sync(0xffffffffu, t.q0 + v, src);
+        it.n_tok = __shfl_sync(0xffffffffu, min(2 * TQ, t.n - v), src);
+        it.pos0 = __shfl_sync(0xffffffffu, t.pos0 + v, src);
+        it.bad = __shfl_sync(0xffffffffu, int(t.bad), src);
+      };
+      auto give = [&](int k, const PfItem &it) {
+        const int slot = k & 1;
+        if (k >= 2 && !warp_wait(&bar[C::kEmptyItem + slot], uint32_t((k >> 1) - 1) & 1u))
+          return false;
         if (lane == 0) {
-          mbar_arrive_expect_tx(&bar[C::kFullQ], tiles * (D / 64) * box);
-          for (int i = 0; i < tiles; ++i)
-            for (int h = 0; h < D / 64; ++h)
-              asm volatile(
-                  "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier"
-                  "::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
-                      smem_addr(smem + C::kQ + i * C::kTileBytes + h * C::kHalf)),
-                  "l"(reinterpret_cast<uint64_t>(&qmap)), "r"(64 * h),
-                  "r"(it.g * G), "r"(it.row0 + i * TQ),
-                  "r"(smem_addr(&bar[C::kFullQ]))
-                  : "memory");
+          items[slot] = it;
+          mbar_arrive(&bar[C::kFullItem + slot]);
         }
         __syncwarp();
-      }
-      auto page_of = [&](int j) {
-        return mine && j < n ? box_page(a.v, it.b, tile_pos(plan, j_lo + j, kPfTile) + r0,
-                                        a.box_rows, plan.s1, plan.lo, p1 + 1)
-                             : 0;
-      };
-      // the same page serves the keys and the values of a tile
-      auto issue = [&](int j, int page, bool is_v) {
-        const int stages = is_v ? C::kVStages : C::kKStages;
-        const int slot = j % stages, round = j / stages;
-        uint64_t *full = &bar[(is_v ? C::kFullV : C::kFullK) + slot];
-        uint64_t *empty = &bar[(is_v ? C::kEmptyV : C::kEmptyK) + slot];
-        if (round > 0 && !warp_wait(empty, uint32_t(round - 1) & 1u)) return false;
-        if (lane == 0) mbar_arrive_expect_tx(full, C::kTileBytes);
-        __syncwarp();
-        if (mine)
-          tma_load_4d(smem + (is_v ? C::kV : C::kK) + slot * C::kTileBytes + dst,
-                      is_v ? &vmap : &kmap, half * 64,
-                      (tile_pos(plan, j_lo + j, kPfTile) + r0) &
-                          ((1 << a.v.page_shift) - 1),
-                      it.g, page, full);
         return true;
       };
-      int page_k = page_of(0), page_v = page_k;
-      int nk = 0, nv = 0;
-      if (n > 0) ok = issue(nk++, page_k, false);
-      while (ok && nv < n) {
-        const int page_next = page_of(nk);  // looked up while the stages fill
-        if (nk < n) {
-          ok = issue(nk, page_next, false);
-          if (ok) ++nk;
+      int vs = 0, vr = 0;
+      PfItem it, next;
+      find(0, it);
+      bool ok = give(0, it);
+      for (int k = 1; ok && it.b >= 0; ++k) {
+        find(k, next);
+        ok = give(k, next);
+        const PfWork w = pf_work(a, it);
+        for (int j = 0; ok && j < w.n; ++j) {
+          ok = warp_wait(&bar[C::kFullV + vs], uint32_t(vr) & 1u);
+          if (!ok) break;
+          const int x = tile_pos(w.plan, w.j_lo + j, kPfTile);
+          const bool all = x + kPfTile <= w.p1 + 1 &&
+                           (x >= w.plan.lo || x + kPfTile <= w.plan.s1);
+          if (!all) {
+            uint8_t *vt = smem + C::kV + vs * C::kTileBytes;
+            for (int r = lane; r < kPfTile; r += 32) {
+              const int pos = x + r;
+              if (pos <= w.p1 && (pos >= w.plan.lo || pos < w.plan.s1)) continue;
+#pragma unroll
+              for (int h = 0; h < D / 64; ++h)
+#pragma unroll
+                for (int c = 0; c < 8; ++c)
+                  *reinterpret_cast<uint4 *>(vt + h * C::kHalf + r * 128 + c * 16) =
+                      make_uint4(0u, 0u, 0u, 0u);
+            }
+            fence_async_smem();
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bar[C::kReadyV + vs]);
+          if (++vs == C::kVStages) vs = 0, ++vr;
         }
-        if (ok) ok = issue(nv, page_v, true);
-        if (ok) ++nv;
-        page_v = page_next;
+        it = next;
+      }
+      if (!ok && lane == 0) atomicOr(a.v.err, 4u);
+    } else if (warp == kPfLoadWarp) {
+      // ---- copies: queries, keys (two tiles ahead) and values ----
+      const int boxes = (kPfTile / a.box_rows) * (D / 64);  // at most 16
+      const int half = lane % (D / 64), r0 = lane / (D / 64) * a.box_rows;
+      const bool mine = lane < boxes;
+      const uint32_t dst = half * C::kHalf + r0 * 128;
+      const uint32_t q_box = uint32_t(TQ) * G * 128;
+      int ck = 0, cv = 0, cq = 0;  // key tiles, value tiles, queries so far
+      bool ok = true;
+      PfItem it;
+      while (ok && next_item(it)) {
+        const PfWork w = pf_work(a, it);
+        if (w.n == 0) continue;
+        auto pos_of = [&](int j) { return tile_pos(w.plan, w.j_lo + j, kPfTile) + r0; };
+        auto page_of = [&](int j) {
+          return mine && j < w.n ? box_page(a.v, it.b, pos_of(j), a.box_rows,
+                                            w.plan.s1, w.plan.lo, w.p1 + 1)
+                                 : 0;
+        };
+        // a tile's copy into stage c mod stages; the same page serves the keys
+        // and the values of a tile
+        auto issue = [&](int c, int j, int page, bool is_v) {
+          const int stages = is_v ? C::kVStages : C::kKStages;
+          const int slot = c % stages, round = c / stages;
+          uint64_t *full = &bar[(is_v ? C::kFullV : C::kFullK) + slot];
+          uint64_t *empty = &bar[(is_v ? C::kEmptyV : C::kEmptyK) + slot];
+          if (round > 0 && !warp_wait(empty, uint32_t(round - 1) & 1u)) return false;
+          if (lane == 0) mbar_arrive_expect_tx(full, C::kTileBytes);
+          __syncwarp();
+          if (mine)
+            tma_load_4d(smem + (is_v ? C::kV : C::kK) + slot * C::kTileBytes + dst,
+                        is_v ? &vmap : &kmap, half * 64,
+                        pos_of(j) & ((1 << a.v.page_shift) - 1), it.g, page, full);
+          return true;
+        };
+        // pages of the tiles j, j + 1, j + 2
+        int page[3] = {page_of(0), page_of(1), 0};
+        ok = issue(ck, 0, page[0], false);
+        if (!ok) break;
+        ++ck;
+        // the queries, once the item before has made its last scores
+        ok = cq == 0 || warp_wait(&bar[C::kEmptyQ], uint32_t(cq - 1) & 1u);
+        if (!ok) break;
+        const int tiles = w.n1 > 0 ? 2 : 1;
+        if (lane == 0)
+          mbar_arrive_expect_tx(&bar[C::kFullQ], tiles * (D / 64) * q_box);
+        __syncwarp();
+        if (lane < tiles * (D / 64)) {
+          const int i = lane / (D / 64), h = lane % (D / 64);
+          asm volatile(
+              "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier"
+              "::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+                  smem_addr(smem + C::kQ + i * C::kQBytes + h * C::kQHalf)),
+              "l"(reinterpret_cast<uint64_t>(&qmap)), "r"(64 * h),
+              "r"(it.g * G), "r"(it.row0 + i * TQ),
+              "r"(smem_addr(&bar[C::kFullQ]))
+              : "memory");
+        }
+        __syncwarp();
+        ++cq;
+        if (w.n > 1) {
+          ok = issue(ck, 1, page[1], false);
+          if (ok) ++ck;
+        }
+        for (int j = 0; ok && j < w.n; ++j) {
+          page[2] = page_of(j + 2);  // looked up while stages fill
+          if (j + 2 < w.n) {
+            ok = issue(ck, j + 2, page[2], false);
+            if (ok) ++ck;
+          }
+          if (ok) ok = issue(cv, j, page[0], true);
+          if (ok) ++cv;
+          page[0] = page[1];
+          page[1] = page[2];
+        }
       }
       if (!ok) {  // never expected: what is in flight lands first
         if (lane == 0) atomicOr(a.v.err, 4u);
-        bool landed = warp_wait(&bar[C::kFullQ], 0u);
-        for (int j = max(0, nk - C::kKStages); j < nk; ++j)
-          landed &= warp_wait(&bar[C::kFullK + j % C::kKStages],
-                              uint32_t(j / C::kKStages) & 1u);
-        for (int j = max(0, nv - C::kVStages); j < nv; ++j)
-          landed &= warp_wait(&bar[C::kFullV + j % C::kVStages],
-                              uint32_t(j / C::kVStages) & 1u);
+        bool landed = cq == 0 || warp_wait(&bar[C::kFullQ], uint32_t(cq - 1) & 1u);
+        for (int c = max(0, ck - C::kKStages); c < ck; ++c)
+          landed &= warp_wait(&bar[C::kFullK + c % C::kKStages],
+                              uint32_t(c / C::kKStages) & 1u);
+        for (int c = max(0, cv - C::kVStages); c < cv; ++c)
+          landed &= warp_wait(&bar[C::kFullV + c % C::kVStages],
+                              uint32_t(c / C::kVStages) & 1u);
         if (!landed && lane == 0) atomicOr(a.v.err, 2u);
       }
-    } else if (warp == kPfZeroWarp) {
-      // ---- value rows that no token of the item sees become zeros ----
-      for (int j = 0; j < n; ++j) {
-        const int slot = j % C::kVStages;
-        if (!warp_wait(&bar[C::kFullV + slot], uint32_t(j / C::kVStages) & 1u)) {
-          if (lane == 0) atomicOr(a.v.err, 4u);
-          break;
-        }
-        const int x = tile_pos(plan, j_lo + j, kPfTile);
-        const bool all = x + kPfTile <= p1 + 1 &&
-                         (x >= plan.lo || x + kPfTile <= plan.s1);
-        if (!all) {
-          uint8_t *vs = smem + C::kV + slot * C::kTileBytes;
-          for (int r = lane; r < kPfTile; r += 32) {
-            const int pos = x + r;
-            if (pos <= p1 && (pos >= plan.lo || pos < plan.s1)) continue;
-#pragma unroll
-            for (int h = 0; h < D / 64; ++h)
-#pragma unroll
-              for (int c = 0; c < 8; ++c)
-                *reinterpret_cast<uint4 *>(vs + h * C::kHalf + r * 128 + c * 16) =
-                    make_uint4(0u, 0u, 0u, 0u);
-          }
-          fence_async_smem();
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bar[C::kReadyV + slot]);
-      }
-    } else if (warp == kPfMmaWarp && n > 0) {
-      // ---- products ----
+    } else {
+      // ---- products: a warp per query tile, one elected thread of it issues
+      // (the warp around it stays uniform: a lane alone issues at half the
+      // speed).  The tensor cores run one thread's products in order, so
+      // S_i(j + 1) may overwrite the columns of P_i(j) that O_i(j) reads before
+      // it.  What one warp spends on waiting and fetching its code (200 cycles
+      // a step) the other's products fill.  Where the scores wait for the
+      // values (not kOwnP) the warps take turns, a tile's products in one go:
+      // one tile's softmax then runs during the other's products; without
+      // turns both tiles wait, then both compute (10 % slower). ----
+      const int i = __shfl_sync(0xffffffffu, warp - kPfMmaWarp, 0);
       const uint32_t base = smem_addr(smem);
       constexpr uint32_t kIdS = pf_idesc(kPfTile, false);
       constexpr uint32_t kIdO = pf_idesc(D, true);
-      auto scores = [&](int i, int j) {  // S_i = Q_i K_j^T
-        const uint64_t qd = sw128_desc(base + C::kQ + i * C::kTileBytes);
-        const uint64_t kd =
-            sw128_desc(base + C::kK + (j % C::kKStages) * C::kTileBytes);
-        if (elect_one()) {
+      const uint32_t t_s = tmem + C::kS + i * 128, t_o = tmem + C::kO + i * D;
+      const uint32_t t_p = tmem + C::kP + i * C::kPStep;
+      const uint64_t qd = sw128_desc(base + C::kQ + i * C::kQBytes);
+      auto scores = [&](int slot) {  // S_i = Q_i K^T
+        const uint64_t kd = sw128_desc(base + C::kK + slot * C::kTileBytes);
 #pragma unroll
-          for (int ks = 0; ks < D / 16; ++ks) {
-            const uint64_t off = uint64_t((ks >> 2) * (C::kHalf / 16) + (ks & 3) * 2);
-            tc_mma_ss(tmem + C::kS + i * 128, qd + off, kd + off, kIdS, ks > 0);
-          }
-          tc_commit(&bar[C::kFullS + i]);
-        }
-        __syncwarp();
+        for (int ks = 0; ks < D / 16; ++ks)
+          tc_mma_ss(t_s, qd + uint64_t((ks >> 2) * (C::kQHalf / 16) + (ks & 3) * 2),
+                    kd + uint64_t((ks >> 2) * (C::kHalf / 16) + (ks & 3) * 2),
+                    kIdS, ks > 0);
+        tc_commit(&bar[C::kFullS + i]);
       };
-      auto values = [&](int i, int j) {  // O_i += P_i V_j
-        const uint64_t vd = sw128_desc_t(
-            base + C::kV + (j % C::kVStages) * C::kTileBytes, C::kHalf);
-        if (elect_one()) {
+      auto values = [&](int slot, int hh, bool first) {  // O_i += P_i V, a half
+        const uint64_t vd =
+            sw128_desc_t(base + C::kV + slot * C::kTileBytes, C::kHalf);
 #pragma unroll
-          for (int ks = 0; ks < kPfTile / 16; ++ks)
-            tc_mma(tmem + C::kO + i * D, tmem + C::kS + i * 128 + ks * 8,
-                   vd + uint64_t(ks * (2048 / 16)), kIdO, j > 0 || ks > 0);
-          if (j + 1 == n_of[i]) tc_commit(&bar[C::kFullO + i]);
+        for (int k = 0; k < kPfTile / 32; ++k) {
+          const int ks = hh * (kPfTile / 32) + k;
+          tc_mma(t_o, t_p + ks * 8, vd + uint64_t(ks * (2048 / 16)), kIdO,
+                 !first || k > 0);
         }
-        __syncwarp();
       };
-      auto release = [&](int bar_index) {
-        if (elect_one()) tc_commit(&bar[bar_index]);
-        __syncwarp();
-      };
-      bool ok = warp_wait(&bar[C::kFullQ], 0u) && warp_wait(&bar[C::kFullK], 0u);
-      if (ok) {
+      // Three waits at the price of one (over 100 cycles even for what is
+      // there): a lane for each.
+      auto wait3 = [&](int bar1, int par1, int bar2, int par2, int bar3, int par3) {
+        const int which = lane % 3;
+        const bool done = warp_wait(
+            &bar[which == 0 ? bar1 : which == 1 ? bar2 : bar3],
+            uint32_t(which == 0 ? par1 : which == 1 ? par2 : par3) & 1u);
         tc_fence_after();
-        for (int i = 0; i < 2; ++i)
-          if (n_of[i] > 0) scores(i, 0);
-        release(C::kEmptyK);
-      }
-      for (int j = 0; ok && j < n; ++j) {
-        const int vs = j % C::kVStages, kn = (j + 1) % C::kKStages;
-        ok = warp_wait(&bar[C::kReadyV + vs], uint32_t(j / C::kVStages) & 1u) &&
-             (j + 1 >= n ||
-              warp_wait(&bar[C::kFullK + kn], uint32_t((j + 1) / C::kKStages) & 1u));
-        for (int i = 0; ok && i < 2; ++i) {
-          if (j >= n_of[i]) continue;
-          ok = warp_wait(&bar[C::kFullP + i], uint32_t(j) & 1u);
-          if (!ok) break;
-          tc_fence_after();
-          values(i, j);
-          if (j + 1 < n_of[i]) scores(i, j + 1);
+        return done;
+      };
+      int turns = 0;
+      const int t_bar = C::kTurn + i;
+      int ks = 0, kr = 0, vs = 0, vr = 0;  // stages and rounds
+      int used = 0, cq = 0;                // this tile's products, queries
+      const int p_bar = C::kFullP + 2 * i;
+      bool ok = true;
+      PfItem it;
+      while (ok && next_item(it)) {
+        const PfWork w = pf_work(a, it);
+        if (w.n == 0) continue;
+        const int n_mine = i ? w.n1 : w.n0;
+        // Tile 0's scores; then for every j tile j's values and tile j + 1's
+        // scores.  Stages that only the other query tile uses are passed on
+        // (a commit without products of this warp is an arrival).
+        for (int j = -1; ok && j < w.n; ++j) {
+          const bool next = j + 1 < w.n, my_next = j + 1 < n_mine;
+          const bool my_values = j >= 0 && j < n_mine;
+          const int k_bar = C::kFullK + ks, v_bar = C::kReadyV + vs;
+          auto next_stage = [&] {
+            if (next) tc_commit(&bar[C::kEmptyK + ks]);
+            if (j + 2 == w.n) tc_commit(&bar[C::kEmptyQ]);
+          };
+          auto next_scores = [&] {
+            if (my_next) scores(ks);
+            if (!C::kOwnP) mbar_arrive(&bar[C::kTurn + 1 - i]);
+            next_stage();
+          };
+          // (a barrier is named twice where there are fewer to wait for)
+          if (j < 0) {
+            ok = C::kOwnP ? wait3(k_bar, kr, C::kFullQ, cq, k_bar, kr)
+                          : wait3(k_bar, kr, C::kFullQ, cq, t_bar, turns++);
+            if (ok && elect_one()) next_scores();
+          } else if (!my_values) {
+            ok = C::kOwnP ? wait3(v_bar, vr, next ? k_bar : v_bar, next ? kr : vr, v_bar, vr)
+                          : wait3(v_bar, vr, next ? k_bar : v_bar, next ? kr : vr, t_bar,
+                                  turns++);
+            if (ok && elect_one()) {
+              tc_commit(&bar[C::kEmptyV + vs]);
+              next_scores();
+            }
+          } else if (C::kOwnP) {
+            // the next scores as soon as this tile's have been read
+            const int s_bar = C::kReadS + i;
+            ok = wait3(s_bar, used, next ? k_bar : s_bar, next ? kr : used, s_bar, used);
+            if (ok && elect_one()) next_scores();
+            __syncwarp();
+            ok = ok && wait3(p_bar + 1, used, v_bar, vr, p_bar + 1, used);
+            if (ok && elect_one()) {
+              values(vs, 0, j == 0);
+              values(vs, 1, false);
+              tc_commit(&bar[C::kDoneO + i]);
+              if (j + 1 == n_mine) tc_commit(&bar[C::kFullO + i]);
+              tc_commit(&bar[C::kEmptyV + vs]);
+            }
+          } else {
+            ok = wait3(p_bar, used, v_bar, vr, t_bar, turns++);
+            if (ok && elect_one()) {
+              values(vs, 0, j == 0);
+              tc_commit(&bar[C::kDoneO + i]);
+            }
+            __syncwarp();
+            ok = ok && wait3(p_bar + 1, used, next ? k_bar : p_bar + 1,
+                             next ? kr : used, p_bar + 1, used);
+            if (ok && elect_one()) {
+              values(vs, 1, false);
+              if (my_next) scores(ks);
+              mbar_arrive(&bar[C::kTurn + 1 - i]);
+              if (j + 1 == n_mine) tc_commit(&bar[C::kFullO + i]);
+              next_stage();
+              tc_commit(&bar[C::kEmptyV + vs]);
+            }
+          }
+          __syncwarp();
+          used += my_values;
+          if (j >= 0 && ++vs == C::kVStages) vs = 0, ++vr;
+          if (next && ++ks == C::kKStages) ks = 0, ++kr;
         }
-        if (!ok) break;
-        release(C::kEmptyV + vs);
-        if (j + 1 < n) release(C::kEmptyK + kn);
+        ++cq;
       }
       if (!ok && lane == 0) atomicOr(a.v.err, 4u);
     }
@@ -450,131 +687,213 @@ prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap qmap,
     const int r = (warp & 3) * 32 + lane;
     const uint32_t t_lane = tmem + (uint32_t((warp & 3) * 32) << 16);
     const uint32_t t_s = t_lane + C::kS + i * 128;
+    const uint32_t t_p = t_lane + C::kP + i * C::kPStep;
     const uint32_t t_o = t_lane + C::kO + i * D;
     const int tok = r / G;
-    const bool live = tok < tok_of[i];
-    const int first = it.pos0 + i * TQ;                   // tile's positions
-    const int last = first + tok_of[i] - 1;
-    const int p = live ? first + tok : -1;                // -1: sees nothing
-    const int lo_last = seen_from(last, a.window, a.sinks).lo;
-    float m = -INFINITY, l = 0.0f;
+    uint32_t used = 0, outs = 0;  // key tiles and items so far
     bool ok = true;
-    for (int j = 0; j < n_of[i]; ++j) {
-      if (!warp_wait(&bar[C::kFullS + i], uint32_t(j) & 1u)) {
-        ok = false;
-        break;
-      }
-      tc_fence_after();
-      float s[128];
+    PfItem it;
+    while (ok && next_item(it)) {
+      const PfWork w = pf_work(a, it);
+      const int n_mine = i ? w.n1 : w.n0, t_mine = i ? w.tok1 : w.tok0;
+      const bool live = tok < t_mine;
+      const int first = it.pos0 + i * TQ;    // the tile's positions
+      const int p = live ? first + tok : -1; // -1: sees nothing
+      // Key tiles that every row sees in whole: from all_lo or up to the first
+      // tokens' end, and up to all_hi.
+      const int all_hi = first + 1 - kPfTile;
+      const int all_lo =
+          a.window > 0 ? seen_from(first + t_mine - 1, a.window, a.sinks).lo : 0;
+      const int all_sk = a.window > 0 ? a.sinks - kPfTile : -1;
+      const int x_gap = (w.plan.w0 - w.plan.n_sink) * kPfTile;
+      int x = w.j_lo * kPfTile + (w.j_lo < w.plan.n_sink ? 0 : x_gap);
+      // m: -inf until the row has seen something (dead rows: 0, for good).
+      float m = live ? -INFINITY : 0.0f, l = 0.0f;
+      bool unseen = true;  // of this warp's rows some may have m = -inf
+      for (int j = 0; j < n_mine; ++j, ++used) {
+        if (!warp_wait(&bar[C::kFullS + i], used & 1u)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        float s[128];
+        uint32_t wt[32];
+        float2 sum = make_float2(0.0f, 0.0f);
+        const bool all = x <= all_hi && (x >= all_lo || x <= all_sk);
+        // What a row does not see: columns past p - x, those before the
+        // window's start but not below the first tokens' end; a bit each.
+        auto mask = [&] {
+          const int hi = p - x + 1;
+          const int lo = a.window > 0 ? hi - a.window : 0;
+          const int sk = a.window > 0 ? a.sinks - x : 0;
 #pragma unroll
-      for (int c = 0; c < 128; c += 32) tmem_ld32_issue(t_s + c, s + c);
+          for (int c = 0; c < 128; c += 32) {
+            const uint32_t seen =
+                below(hi - c) & (~below(lo - c) | below(sk - c));
 #pragma unroll
-      for (int c = 0; c < 128; c += 32) tmem_landed(s + c);
-      const int x = tile_pos(plan, j_lo + j, kPfTile);
-      const bool all = x + kPfTile <= first + 1 &&
-                       (a.window == 0 || x >= lo_last || x + kPfTile <= a.sinks);
-      if (!all) {
-        const int c_hi = p - x;  // columns 0 .. c_hi, from c_lo or below c_sk
-        const int c_lo = a.window > 0 ? p - a.window + 1 - x : -1;
-        const int c_sk = a.sinks - x;
+            for (int e = 0; e < 32; ++e)
+              if (!(seen >> e & 1u)) s[c + e] = -INFINITY;
+          }
+        };
+        // m follows this tile's maximum where that is more than 8 above; what
+        // was summed before is rescaled, O_i too where it holds something
+        // (has_o), once the products that were issued are done (kDoneO's phase
+        // `phase`, if wait).
+        auto follow = [&](bool has_o, bool wait, uint32_t phase) {
+          float mx[4];
 #pragma unroll
-        for (int c = 0; c < 128; ++c)
-          if (c > c_hi || (c < c_lo && c >= c_sk)) s[c] = -INFINITY;
-      }
-      float mx[4] = {s[0], s[1], s[2], s[3]};
+          for (int k = 0; k < 4; ++k) mx[k] = max3(s[3 * k], s[3 * k + 1], s[3 * k + 2]);
 #pragma unroll
-      for (int c = 4; c < 128; ++c) mx[c & 3] = fmaxf(mx[c & 3], s[c]);
-      const float top =
-          fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale2;
-      const bool grow = top > m + 8.0f;
-      if (__any_sync(0xffffffffu, grow)) {
-        const float f = grow ? ex2(m - top) : 1.0f;
-        if (grow) m = top;
-        l *= f;
-        if (j > 0) {  // S_i(j) is there, so O_i holds tiles 0 .. j - 1
+          for (int c = 12; c < 124; c += 8)
 #pragma unroll
-          for (int c = 0; c < D; c += 32) {
-            float o[32];
-            tmem_ld32_issue(t_o + c, o);
-            tmem_landed(o);
+            for (int k = 0; k < 4; ++k)
+              mx[k] = max3(mx[k], s[c + 2 * k], s[c + 2 * k + 1]);
+          mx[0] = max3(mx[0], s[124], s[125]);
+          mx[1] = max3(mx[1], s[126], s[127]);
+          const float top = max3(mx[0], mx[1], fmaxf(mx[2], mx[3])) * a.scale2;
+          const bool grow = top > m + 8.0f;
+          const float f = grow ? ex2(m - top) : 1.0f;
+          if (grow) m = top;
+          l *= f;
+          if (has_o && __any_sync(0xffffffffu, grow)) {
+            if (wait && !warp_wait(&bar[C::kDoneO + i], phase & 1u)) ok = false;
+            tc_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < D; c += 32) {
+              float o[32];
+              tmem_ld32_issue(t_o + c, o);
+              tmem_landed(o);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] *= f;
-            tmem_st32(t_o + c, *reinterpret_cast<uint32_t(*)[32]>(o));
+              for (int e = 0; e < 32; ++e) o[e] *= f;
+              tmem_st32(t_o + c, *reinterpret_cast<uint32_t(*)[32]>(o));
+            }
+          }
+          unseen = __any_sync(0xffffffffu, m == -INFINITY);
+        };
+        auto hand_over = [&](int hh) {
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bar[C::kFullP + 2 * i + hh]);
+        };
+        // Weights against the m of the tiles before.  Where a row's weights
+        // sum to more than 2^16 (or some row has seen nothing yet, or not all
+        // of the tile is seen), the tile's maximum is looked for; otherwise no
+        // maximum is looked for at all: the scale cancels in o / l, and
+        // neither bf16 nor the fp32 sums lose anything by 2^16.
+        constexpr float kMost = 65536.0f;
+        if constexpr (C::kOwnP) {
+#pragma unroll
+          for (int c = 0; c < 128; c += 32) tmem_ld32_issue(t_s + c, s + c);
+#pragma unroll
+          for (int c = 0; c < 128; c += 32) tmem_landed(s + c);
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bar[C::kReadS + i]);  // next scores
+          if (!all) mask();
+          const bool early = !all || unseen;
+          if (early) follow(j > 0, true, used - 1);
+          weights64(s, a.scale2, m == -INFINITY ? 0.0f : m, wt, sum);
+          if (j > 0) {  // O_i(j - 1) has read the weights before
+            if (!warp_wait(&bar[C::kDoneO + i], (used - 1) & 1u)) ok = false;
+            tc_fence_after();
+          }
+          tmem_st32(t_p, wt);
+          weights64(s + 64, a.scale2, m == -INFINITY ? 0.0f : m, wt, sum);
+          if (!early && __any_sync(0xffffffffu, sum.x + sum.y > kMost)) {
+            follow(j > 0, true, used - 1);
+            sum = make_float2(0.0f, 0.0f);
+            weights64(s, a.scale2, m, wt, sum);
+            tmem_st32(t_p, wt);
+            weights64(s + 64, a.scale2, m, wt, sum);
+          }
+        } else {
+          tmem_ld32_issue(t_s, s);
+          tmem_ld32_issue(t_s + 32, s + 32);
+          tmem_landed(s);
+          tmem_landed(s + 32);
+          // (the second half lands while the first one's weights are made;
+          // nothing branches in between, so nothing touches its registers)
+          tmem_ld32_issue(t_s + 64, s + 64);
+          tmem_ld32_issue(t_s + 96, s + 96);
+          weights64(s, a.scale2, m, wt, sum);
+          tmem_landed(s + 64);
+          tmem_landed(s + 96);
+          if (!all) mask();
+          if (!all || unseen || __any_sync(0xffffffffu, sum.x + sum.y > kMost)) {
+            follow(j > 0, false, 0);  // S_i(j) came after O_i(j - 1)
+            sum = make_float2(0.0f, 0.0f);
+            weights64(s, a.scale2, m == -INFINITY ? 0.0f : m, wt, sum);
+          }
+          tmem_st32(t_p, wt);
+          hand_over(0);  // its product starts
+          l += sum.x + sum.y;
+          sum = make_float2(0.0f, 0.0f);
+          weights64(s + 64, a.scale2, m == -INFINITY ? 0.0f : m, wt, sum);
+          if (__any_sync(0xffffffffu, sum.x + sum.y > kMost)) {
+            follow(true, true, used);  // after the first half's product
+            sum = make_float2(0.0f, 0.0f);
+            weights64(s + 64, a.scale2, m, wt, sum);
           }
         }
+        tmem_st32(t_p + 32, wt);
+        hand_over(1);
+        l += sum.x + sum.y;
+        x += kPfTile;
+        if (w.j_lo + j + 1 == w.plan.n_sink) x += x_gap;
       }
-      const float mu = m == -INFINITY ? 0.0f : m;
-      float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-      for (int hh = 0; hh < 2; ++hh) {
-        uint32_t w[32];
-#pragma unroll
-        for (int c = 0; c < 32; ++c) {
-          const float e0 = ex2(fmaf(s[64 * hh + 2 * c], a.scale2, -mu));
-          const float e1 = ex2(fmaf(s[64 * hh + 2 * c + 1], a.scale2, -mu));
-          sum[(2 * c) & 3] += e0;
-          sum[(2 * c + 1) & 3] += e1;
-          const __nv_bfloat162 t = __floats2bfloat162_rn(e0, e1);
-          w[c] = *reinterpret_cast<const uint32_t *>(&t);
-        }
-        tmem_st32(t_s + 32 * hh, w);
-      }
-      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-      tmem_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bar[C::kFullP + i]);
-    }
-    if (!ok && lane == 0) atomicOr(a.v.err, 4u);
 
-    // ---- out, or this part's sums ----
-    const int row = it.row0 + i * TQ + tok;
-    const int h = it.g * G + r - tok * G;
-    if (n_of[i] > 0 && ok) {
-      ok = warp_wait(&bar[C::kFullO + i], 0u);
-      if (!ok && lane == 0) atomicOr(a.v.err, 4u);
-      tc_fence_after();
-    }
-    if (a.split == 1) {
+      // ---- out, or this part's sums ----
+      const int row = it.row0 + i * TQ + tok;
+      const int h = it.g * G + r - tok * G;
+      if (ok && n_mine > 0) {
+        // (A barrier of its own: kDoneO may be one or two products behind, and
+        // a parity tells a phase only from the next one.)
+        ok = warp_wait(&bar[C::kFullO + i], outs & 1u);
+        ++outs;
+        tc_fence_after();
+      }
+      if (!ok) break;
+      const int64_t at = (int64_t(it.s) * a.n_tokens + row) * a.H + h;
+      const bool direct = a.split == 1 || (it.bad && it.s == 0);
       const float inv = l > 0.0f ? 1.0f / l : 0.0f;
       __nv_bfloat16 *o = a.out + int64_t(row) * a.out_ld + h * D;
+      if (live && a.split > 1) a.ml[at] = make_float2(m, l);
+#pragma unroll 1
+      for (int c = 0; c < D; c += 32) {  // rolled: the code is fetched anew for
+        float v[32];                     // every item
+        if (n_mine > 0) {
+          tmem_ld32_issue(t_o + c, v);
+          tmem_landed(v);
+        } else {
 #pragma unroll
-      for (int c = 0; c < D; c += 32) {
-        float v[32];
-        tmem_ld32_issue(t_o + c, v);
-        tmem_landed(v);
-        if (live && ok) {
+          for (int e = 0; e < 32; ++e) v[e] = 0.0f;
+        }
+        if (!live) continue;
+        if (direct) {
 #pragma unroll
           for (int e = 0; e < 32; e += 8) {
-            uint32_t w[4];
+            uint32_t y[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               const __nv_bfloat162 t = __floats2bfloat162_rn(
                   v[e + 2 * k] * inv, v[e + 2 * k + 1] * inv);
-              w[k] = *reinterpret_cast<const uint32_t *>(&t);
+              y[k] = *reinterpret_cast<const uint32_t *>(&t);
             }
-            *reinterpret_cast<uint4 *>(o + c + e) = make_uint4(w[0], w[1], w[2], w[3]);
+            *reinterpret_cast<uint4 *>(o + c + e) = make_uint4(y[0], y[1], y[2], y[3]);
           }
+        } else if (n_mine > 0) {
+#pragma unroll
+          for (int e = 0; e < 32; e += 4)
+            *reinterpret_cast<float4 *>(a.part + at * D + c + e) =
+                make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
         }
       }
-    } else {
-      const int64_t at = (int64_t(it.s) * a.n_tokens + row) * a.H + h;
-      if (live) a.ml[at] = make_float2(m, n_of[i] > 0 ? l : 0.0f);
-      if (n_of[i] > 0) {
-#pragma unroll
-        for (int c = 0; c < D; c += 32) {
-          float v[32];
-          tmem_ld32_issue(t_o + c, v);
-          tmem_landed(v);
-          if (live && ok) {
-#pragma unroll
-            for (int e = 0; e < 32; e += 4)
-              *reinterpret_cast<float4 *>(a.part + at * D + c + e) =
-                  make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
-          }
-        }
-      }
+      // The next item's first product overwrites O_i only after this
+      // warpgroup has written its P, so after these loads.
+      tc_fence_before();
     }
+    if (!ok && lane == 0) atomicOr(a.v.err, 4u);
   }
   tc_fence_before();
   __syncthreads();  // every tensor-memory access is done
@@ -679,20 +998,6 @@ cudaError_t launch_t(const PagedView &v, const PagedAttnLaunch &l,
   cudaError_t e = paged_resident(prefill_kernel<D>, cached, kPfThreads,
                                  PfCfg<D>::kSmem, &resident);
   if (e != cudaSuccess) return e;
-  // The register split draws on what the CTA is launched with: a build that
-  // gave it fewer is refused, not left waiting.
-  static std::atomic<int> regs{0};
-  int n_regs = regs.load(std::memory_order_relaxed);
-  if (n_regs == 0) {
-    cudaFuncAttributes fa;
-    e = cudaFuncGetAttributes(&fa, prefill_kernel<D>);
-    if (e != cudaSuccess) return e;
-    n_regs = fa.numRegs;
-    regs.store(n_regs, std::memory_order_relaxed);
-  }
-  if (n_regs * kPfThreads < kPfSoftRegs * kPfSoftWarps * 32 +
-                                kPfOtherRegs * (kPfThreads - kPfSoftWarps * 32))
-    return cudaErrorInvalidConfiguration;
   CUtensorMap qmap, kmap, vmap;
   PFN_cuTensorMapEncodeTiled_v12000 fn = tensor_map_encoder();
   if (!fn) return cudaErrorInvalidValue;
@@ -710,8 +1015,8 @@ cudaError_t launch_t(const PagedView &v, const PagedAttnLaunch &l,
       !encode_pool(&vmap, v.v, v, D, a.box_rows))
     return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(
-      max_items(l.n_tokens, v.n_seqs, a.G, v.hkv) * a.split));
+  const int64_t items = max_items(l.n_tokens, v.n_seqs, a.G, v.hkv) * a.split;
+  cfg.gridDim = dim3(unsigned(items < resident ? items : resident));
   cfg.blockDim = dim3(kPfThreads);
   cfg.dynamicSmemBytes = PfCfg<D>::kSmem;
   cfg.stream = stream;
