@@ -257,6 +257,29 @@ __device__ __forceinline__ void weights64(const float *s, float scale2, float m,
   sum = add2(sum, add2(acc[0], acc[1]));
 }
 
+// Lanes 4 k .. 4 k + 3 hold pieces 0..3 of a row each; afterwards lane 4 k + q
+// holds piece q of the four rows.
+__device__ __forceinline__ void exchange4(uint32_t (&y)[4][4]) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int bit = 1; bit < 4; bit <<= 1) {
+    const bool up = lane & bit;
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+      if (p & bit) continue;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t give = up ? y[p][k] : y[p | bit][k];
+        const uint32_t got = __shfl_xor_sync(0xffffffffu, give, bit);
+        if (up)
+          y[p][k] = got;
+        else
+          y[p | bit][k] = got;
+      }
+    }
+  }
+}
+
 // One item of work: up to 2 TQ tokens of one sequence and key-value head, a
 // part of their key tiles.
 struct PfItem {
@@ -690,6 +713,13 @@ prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap qmap,
     const uint32_t t_p = t_lane + C::kP + i * C::kPStep;
     const uint32_t t_o = t_lane + C::kO + i * D;
     const int tok = r / G;
+    // token and head of the four rows that this lane stores a piece of
+    int tok_of[4], head_of[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      tok_of[q] = ((r & ~3) + q) / G;
+      head_of[q] = ((r & ~3) + q) - tok_of[q] * G;
+    }
     uint32_t used = 0, outs = 0;  // key tiles and items so far
     bool ok = true;
     PfItem it;
@@ -844,8 +874,6 @@ prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap qmap,
       }
 
       // ---- out, or this part's sums ----
-      const int row = it.row0 + i * TQ + tok;
-      const int h = it.g * G + r - tok * G;
       if (ok && n_mine > 0) {
         // (A barrier of its own: kDoneO may be one or two products behind, and
         // a parity tells a phase only from the next one.)
@@ -854,14 +882,20 @@ prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap qmap,
         tc_fence_after();
       }
       if (!ok) break;
-      const int64_t at = (int64_t(it.s) * a.n_tokens + row) * a.H + h;
+      const int64_t row0 = int64_t(it.row0) + i * TQ;  // of this query tile
+      const int h0 = it.g * G;
       const bool direct = a.split == 1 || (it.bad && it.s == 0);
       const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-      __nv_bfloat16 *o = a.out + int64_t(row) * a.out_ld + h * D;
-      if (live && a.split > 1) a.ml[at] = make_float2(m, l);
+      if (live && a.split > 1)
+        a.ml[(int64_t(it.s) * a.n_tokens + row0 + tok) * a.H + h0 + r - tok * G] =
+            make_float2(m, l);
+      // 32 columns at a time (rolled: the code is fetched anew for every
+      // item).  Four lanes exchange 16-byte pieces of their four rows, so that
+      // a store covers 64 bytes of each of 8 rows, not 16 bytes of each of 32
+      // (which kept the load/store unit busy for 2000 cycles at D = 64).
 #pragma unroll 1
-      for (int c = 0; c < D; c += 32) {  // rolled: the code is fetched anew for
-        float v[32];                     // every item
+      for (int c = 0; c < D; c += 32) {
+        float v[32];
         if (n_mine > 0) {
           tmem_ld32_issue(t_o + c, v);
           tmem_landed(v);
@@ -869,24 +903,38 @@ prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap qmap,
 #pragma unroll
           for (int e = 0; e < 32; ++e) v[e] = 0.0f;
         }
-        if (!live) continue;
         if (direct) {
+          uint32_t y[4][4];
 #pragma unroll
-          for (int e = 0; e < 32; e += 8) {
-            uint32_t y[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const __nv_bfloat162 t = __floats2bfloat162_rn(
-                  v[e + 2 * k] * inv, v[e + 2 * k + 1] * inv);
-              y[k] = *reinterpret_cast<const uint32_t *>(&t);
-            }
-            *reinterpret_cast<uint4 *>(o + c + e) = make_uint4(y[0], y[1], y[2], y[3]);
+          for (int e = 0; e < 16; ++e) {
+            const __nv_bfloat162 t =
+                __floats2bfloat162_rn(v[2 * e] * inv, v[2 * e + 1] * inv);
+            y[e >> 2][e & 3] = *reinterpret_cast<const uint32_t *>(&t);
           }
+          exchange4(y);
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            if (tok_of[q] < t_mine)
+              *reinterpret_cast<uint4 *>(
+                  a.out + (row0 + tok_of[q]) * a.out_ld + (h0 + head_of[q]) * D +
+                  c + (lane & 3) * 8) = make_uint4(y[q][0], y[q][1], y[q][2], y[q][3]);
         } else if (n_mine > 0) {
 #pragma unroll
-          for (int e = 0; e < 32; e += 4)
-            *reinterpret_cast<float4 *>(a.part + at * D + c + e) =
-                make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+          for (int half = 0; half < 32; half += 16) {
+            uint32_t y[4][4];
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              y[e >> 2][e & 3] = __float_as_uint(v[half + e]);
+            exchange4(y);
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              if (tok_of[q] < t_mine)
+                *reinterpret_cast<uint4 *>(
+                    a.part +
+                    ((int64_t(it.s) * a.n_tokens + row0 + tok_of[q]) * a.H + h0 +
+                     head_of[q]) * D + c + half + (lane & 3) * 4) =
+                    make_uint4(y[q][0], y[q][1], y[q][2], y[q][3]);
+          }
         }
       }
       // The next item's first product overwrites O_i only after this
