@@ -821,21 +821,19 @@ prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap qmap,
           __syncwarp();
           if (lane == 0) mbar_arrive(&bar[C::kReadS + i]);  // next scores
           if (!all) mask();
-          const bool early = !all || unseen;
-          if (early) follow(j > 0, true, used - 1);
-          weights64(s, a.scale2, m == -INFINITY ? 0.0f : m, wt, sum);
-          if (j > 0) {  // O_i(j - 1) has read the weights before
-            if (!warp_wait(&bar[C::kDoneO + i], (used - 1) & 1u)) ok = false;
-            tc_fence_after();
-          }
-          tmem_st32(t_p, wt);
-          weights64(s + 64, a.scale2, m == -INFINITY ? 0.0f : m, wt, sum);
-          if (!early && __any_sync(0xffffffffu, sum.x + sum.y > kMost)) {
-            follow(j > 0, true, used - 1);
+          // (loops, here and below, so that the code, which is fetched anew
+          // whenever the warp comes back to it, is there once)
+          for (bool must = !all || unseen;; must = true) {
+            if (must) follow(j > 0, true, used - 1);
             sum = make_float2(0.0f, 0.0f);
-            weights64(s, a.scale2, m, wt, sum);
+            weights64(s, a.scale2, m == -INFINITY ? 0.0f : m, wt, sum);
+            if (j > 0) {  // O_i(j - 1) has read the weights before
+              if (!warp_wait(&bar[C::kDoneO + i], (used - 1) & 1u)) ok = false;
+              tc_fence_after();
+            }
             tmem_st32(t_p, wt);
-            weights64(s + 64, a.scale2, m, wt, sum);
+            weights64(s + 64, a.scale2, m == -INFINITY ? 0.0f : m, wt, sum);
+            if (must || !__any_sync(0xffffffffu, sum.x + sum.y > kMost)) break;
           }
         } else {
           tmem_ld32_issue(t_s, s);
@@ -858,12 +856,11 @@ prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap qmap,
           tmem_st32(t_p, wt);
           hand_over(0);  // its product starts
           l += sum.x + sum.y;
-          sum = make_float2(0.0f, 0.0f);
-          weights64(s + 64, a.scale2, m == -INFINITY ? 0.0f : m, wt, sum);
-          if (__any_sync(0xffffffffu, sum.x + sum.y > kMost)) {
-            follow(true, true, used);  // after the first half's product
+          for (bool again = false;; again = true) {
             sum = make_float2(0.0f, 0.0f);
-            weights64(s + 64, a.scale2, m, wt, sum);
+            weights64(s + 64, a.scale2, m == -INFINITY ? 0.0f : m, wt, sum);
+            if (again || !__any_sync(0xffffffffu, sum.x + sum.y > kMost)) break;
+            follow(true, true, used);  // after the first half's product
           }
         }
         tmem_st32(t_p + 32, wt);
