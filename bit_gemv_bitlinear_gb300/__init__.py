@@ -14,8 +14,10 @@ Function names follow the C ABI: ``bw_quant_act``, ``bw_repack``,
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -455,107 +457,106 @@ def bw_attn_decode_ex(qkv: torch.Tensor, pos: torch.Tensor, H: int,
     return out
 
 
-class _PagedKV(ctypes.Structure):
-    _fields_ = [("k_pages", _P), ("v_pages", _P), ("page_table", _P),
-                ("kv_len", _P), ("page_stride", _L), ("n_pages", _I),
-                ("page_size", _I), ("n_kv_heads", _I), ("head_dim", _I),
-                ("n_seqs", _I), ("max_pages", _I)]
+# bw_paged_kv as bytes (k_pages, v_pages, page_table, kv_len, page_stride,
+# n_pages, page_size, n_kv_heads, head_dim, n_seqs, max_pages).
+_PAGED_KV = struct.Struct("@PPPPqiiiiii")
+_BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
 
 
-def _same_device(dev, *tensors):
-    for t in tensors:
-        if t is not None and t.device != dev:
-            raise ValueError(f"tensors on {t.device} and {dev}: one call's "
-                             "tensors must be on one device")
-
-
-def _paged_kv(k_pages: torch.Tensor, v_pages: torch.Tensor,
-              page_table: torch.Tensor, kv_len: torch.Tensor) -> _PagedKV:
-    """The bw_paged_kv of four tensors.  The pools [n_pages][Hkv][page][D] may
-    be strided from page to page (two views of one pool, say)."""
-    for t, name in ((k_pages, "k_pages"), (v_pages, "v_pages")):
-        if not isinstance(t, torch.Tensor):
-            raise TypeError(f"{name} must be a torch.Tensor")
-        if not t.is_cuda:
-            raise ValueError(f"{name} must be a CUDA tensor")
-        if t.dtype != torch.bfloat16:
-            raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
-        if t.dim() != 4:
-            raise ValueError(f"{name} must be [n_pages][Hkv][page][D]")
-    shape, st = k_pages.shape, k_pages.stride()
-    if v_pages.shape != shape or v_pages.stride() != st:
-        raise ValueError("k_pages and v_pages must have one shape and strides")
-    n_pages, hkv, page, D = shape
-    if (D > 1 and st[3] != 1) or (page > 1 and st[2] != D) or \
-            (hkv > 1 and st[1] != page * D):
-        raise ValueError("a page of k_pages and v_pages must be contiguous")
-    table, lens = _dev(page_table, torch.int32, "page_table"), \
-        _dev(kv_len, torch.int32, "kv_len")
-    if page_table.dim() != 2 or kv_len.dim() != 1 or \
-            page_table.shape[0] != kv_len.shape[0]:
-        raise ValueError("page_table must be [n_seqs][max_pages] and kv_len "
-                         "[n_seqs]")
-    _same_device(k_pages.device, v_pages, page_table, kv_len)
-    return _PagedKV(k_pages.data_ptr(), v_pages.data_ptr(), table, lens,
-                    st[0] if n_pages > 1 else hkv * page * D, n_pages, page,
-                    hkv, D, page_table.shape[0], page_table.shape[1])
-
-
-def _rows(t: torch.Tensor, dtypes, rows: int, H: int, D: int, name: str):
-    """(pointer, row stride) of [rows][H][D] with contiguous rows."""
+def _refuse(t, dtypes, dev: int, what: str):
+    """Says what is wrong with an argument that failed its checks."""
     if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
+        raise TypeError(f"{what.split(' must')[0]} must be a torch.Tensor")
     if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
+        raise ValueError(f"{what.split(' must')[0]} must be a CUDA tensor")
     if t.dtype not in dtypes:
-        raise TypeError(f"{name} must be {' or '.join(map(str, dtypes))}, "
-                        f"got {t.dtype}")
-    if tuple(t.shape) != (rows, H, D):
-        raise ValueError(f"{name} must be [{rows}][{H}][{D}], got "
-                         f"{tuple(t.shape)}")
-    st = t.stride()
-    if (D > 1 and st[2] != 1) or (H > 1 and st[1] != D):
-        raise ValueError(f"a row of {name} must be contiguous")
-    return t.data_ptr(), (st[0] if rows > 1 else H * D)
+        raise TypeError(f"{what.split(' must')[0]} must be "
+                        f"{' or '.join(map(str, dtypes))}, got {t.dtype}")
+    if dev >= 0 and t.get_device() != dev:
+        raise ValueError(f"tensors on cuda:{t.get_device()} and cuda:{dev}: "
+                         "one call's tensors must be on one device")
+    raise ValueError(f"{what}, got {tuple(t.shape)} with strides {t.stride()}")
 
 
-def _device_of_stream(stream):
-    dev = getattr(stream, "device", None)
-    return dev if isinstance(dev, torch.device) else None
+def _is(t, dtype, dev: int) -> bool:
+    return isinstance(t, torch.Tensor) and t.dtype is dtype and \
+        t.get_device() == dev
 
 
-class _OnDevice:
-    """Makes `dev` the current device and `stream` (None: its current stream)
-    the stream that new tensors belong to, for the length of one call; costs
-    nothing where they are current already."""
+def _paged_kv(k_pages, v_pages, page_table, kv_len):
+    """(bw_paged_kv as bytes, device, n_seqs, Hkv, D) of four tensors.  The
+    pools [n_pages][Hkv][page][D] may be strided from page to page (two views
+    of one pool, say)."""
+    pages = "must be [n_pages][Hkv][page][D] with contiguous pages"
+    if not isinstance(k_pages, torch.Tensor) or not k_pages.is_cuda or \
+            k_pages.dtype is not _BF16 or k_pages.dim() != 4:
+        _refuse(k_pages, (_BF16,), -1, f"k_pages {pages}")
+    dev, shape, st = k_pages.get_device(), k_pages.shape, k_pages.stride()
+    n_pages, hkv, page, D = shape
+    if st[3] != 1 and D > 1 or st[2] != D and page > 1 or \
+            st[1] != page * D and hkv > 1:
+        _refuse(k_pages, (_BF16,), dev, f"k_pages {pages}")
+    if not _is(v_pages, _BF16, dev) or v_pages.shape != shape or \
+            v_pages.stride() != st:
+        _refuse(v_pages, (_BF16,), dev,
+                "v_pages must have the shape and the strides of k_pages")
+    if not _is(kv_len, _I32, dev) or kv_len.dim() != 1 or \
+            not kv_len.is_contiguous():
+        _refuse(kv_len, (_I32,), dev, "kv_len must be a contiguous [n_seqs]")
+    n = kv_len.shape[0]
+    if not _is(page_table, _I32, dev) or page_table.dim() != 2 or \
+            page_table.shape[0] != n or not page_table.is_contiguous():
+        _refuse(page_table, (_I32,), dev,
+                f"page_table must be a contiguous [{n}][max_pages]")
+    return _PAGED_KV.pack(
+        k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(),
+        kv_len.data_ptr(), st[0] if n_pages > 1 else hkv * page * D, n_pages,
+        page, hkv, D, n, page_table.shape[1]), dev, n, hkv, D
 
-    def __init__(self, dev, stream):
-        sdev = _device_of_stream(stream)
-        if sdev is not None and sdev != dev:
-            raise ValueError(f"stream on {sdev}, tensors on {dev}")
-        self._dev = None if dev.index == torch.cuda.current_device() \
-            else torch.cuda.device(dev)
-        self._stream = None
-        if stream is None:
-            self.stream = torch.cuda.current_stream(dev).cuda_stream
-        else:
-            self.stream = _stream(stream)
-            obj = stream if hasattr(stream, "cuda_stream") else \
-                torch.cuda.ExternalStream(self.stream, device=dev)
-            self._stream = torch.cuda.stream(obj)
 
-    def __enter__(self):
-        if self._dev is not None:
-            self._dev.__enter__()
-        if self._stream is not None:
-            self._stream.__enter__()
-        return self.stream
+def _rows(t, dtypes, dev: int, rows: int, H: int, D: int, name: str):
+    """(pointer, row stride) of [rows][H][D] with contiguous rows."""
+    if isinstance(t, torch.Tensor) and t.dtype in dtypes and \
+            t.get_device() == dev and t.shape == (rows, H, D):
+        st = t.stride()
+        if (st[2] == 1 or D == 1) and (st[1] == D or H == 1):
+            return t.data_ptr(), (st[0] if rows > 1 else H * D)
+    _refuse(t, dtypes, dev, f"{name} must be [{rows}][{H}][{D}] with "
+            "contiguous rows")
 
-    def __exit__(self, *exc):
-        if self._stream is not None:
-            self._stream.__exit__(*exc)
-        if self._dev is not None:
-            self._dev.__exit__(*exc)
+
+def _vector(t, dtype, dev: int, count: int, name: str) -> int:
+    """Pointer of a contiguous tensor of at least `count` elements."""
+    if not _is(t, dtype, dev) or not t.is_contiguous() or t.numel() < count:
+        _refuse(t, (dtype,), dev,
+                f"{name} must be contiguous with at least {count} elements")
+    return t.data_ptr()
+
+
+_NO_CONTEXT = contextlib.nullcontext()
+
+
+def _where(dev: int, stream):
+    """(context, stream handle) of a call whose tensors are on device `dev`:
+    in the context that device is the current one and tensors made belong to
+    the stream (None: the device's current one)."""
+    if stream is None:
+        s = torch.cuda.current_stream(dev).cuda_stream \
+            if _raw_stream is None else _raw_stream(dev)
+        if torch.cuda.current_device() == dev:
+            return _NO_CONTEXT, s
+        return torch.cuda.device(dev), s
+    s = _stream(stream)
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(s, device=dev)
+    elif stream.device.index != dev:
+        raise ValueError(f"stream on {stream.device}, tensors on cuda:{dev}")
+    return torch.cuda.stream(stream), s  # makes the stream's device current
+
+
+# The current stream's handle without making a stream object, where this
+# PyTorch has it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def bw_qk_norm_rope_append(qkv: torch.Tensor, k_pages: torch.Tensor,
@@ -574,35 +575,28 @@ def bw_qk_norm_rope_append(qkv: torch.Tensor, k_pages: torch.Tensor,
     view of qkv's own query columns).  kv_len counts the new tokens; q_start
     int32 [n_seqs + 1] gives each sequence's rows, None one row each.  Rows of
     no sequence are left as they are (zeros in a q_out made here)."""
-    kv = _paged_kv(k_pages, v_pages, page_table, kv_len)
-    dev, D = k_pages.device, kv.head_dim
-    if not isinstance(qkv, torch.Tensor) or qkv.dim() != 2:
-        raise ValueError("qkv must be [n_tokens][(H + 2 Hkv) D]")
-    n = qkv.shape[0]
-    heads = H + 2 * kv.n_kv_heads
-    if H < 1 or qkv.shape[1] != heads * D:
-        raise ValueError(f"qkv must have {heads * D} columns")
-    ptr, ld = _rows(qkv.unflatten(1, (heads, D)), (torch.bfloat16,), n, heads,
-                    D, "qkv")
-    _same_device(dev, qkv, q_start, q_gamma, k_gamma, q_out)
-    starts = None
-    if q_start is not None:
-        starts = _dev(q_start, torch.int32, "q_start")
-        _need(q_start, kv.n_seqs + 1, "q_start")
-    gammas = []
-    for g, name in ((q_gamma, "q_gamma"), (k_gamma, "k_gamma")):
-        gammas.append(None if g is None else _dev(g, torch.float32, name))
-        if g is not None:
-            _need(g, D, name)
-    with _OnDevice(dev, stream) as s:
+    kv, dev, n_seqs, hkv, D = _paged_kv(k_pages, v_pages, page_table, kv_len)
+    width = (H + 2 * hkv) * D
+    if H < 1 or not _is(qkv, _BF16, dev) or qkv.dim() != 2 or \
+            qkv.shape[1] != width or qkv.stride(1) != 1:
+        _refuse(qkv, (_BF16,), dev, f"qkv must be [n_tokens][{width}] (H + 2 "
+                "Hkv heads) with contiguous rows")
+    n, ptr = qkv.shape[0], qkv.data_ptr()
+    ld = qkv.stride(0) if n > 1 else width
+    starts = None if q_start is None else \
+        _vector(q_start, _I32, dev, n_seqs + 1, "q_start")
+    gq = None if q_gamma is None else _vector(q_gamma, _F32, dev, D, "q_gamma")
+    gk = None if k_gamma is None else _vector(k_gamma, _F32, dev, D, "k_gamma")
+    context, s = _where(dev, stream)
+    with context:
         if q_out is None:
-            q_out = torch.zeros((n, H, D), dtype=torch.bfloat16, device=dev)
-        out, out_ld = _rows(q_out, (torch.bfloat16,), n, H, D, "q_out")
+            q_out = torch.zeros((n, H, D), dtype=_BF16, device=qkv.device)
+        out, out_ld = _rows(q_out, (_BF16,), dev, n, H, D, "q_out")
         if out == ptr and n == 1:
             out_ld = ld  # in place: one row has no stride of its own
         _check(_lib.bw_qk_norm_rope_append(
-            ptr, ld, n, starts, H, gammas[0], gammas[1], eps, theta,
-            ctypes.byref(kv), out, out_ld, s), "bw_qk_norm_rope_append")
+            ptr, ld, n, starts, H, gq, gk, eps, theta, kv, out, out_ld, s),
+            "bw_qk_norm_rope_append")
     return q_out
 
 
@@ -625,26 +619,24 @@ def bw_attn_paged_decode(q: torch.Tensor, k_pages: torch.Tensor,
     the first `sinks` ones.  scale: 1/sqrt(D) if None.  `workspace`: a uint8
     device tensor of at least bw_attn_paged_decode_workspace_bytes bytes,
     zeroed before its first use; if omitted, one is made for this call."""
-    kv = _paged_kv(k_pages, v_pages, page_table, kv_len)
-    dev, D, n = k_pages.device, kv.head_dim, kv.n_seqs
+    kv, dev, n, hkv, D = _paged_kv(k_pages, v_pages, page_table, kv_len)
     if not isinstance(q, torch.Tensor) or q.dim() != 3:
-        raise ValueError("q must be [n_seqs][H][D]")
+        _refuse(q, (_BF16,), dev, "q must be [n_seqs][H][D]")
     H = q.shape[1]
-    ptr, ld = _rows(q, (torch.bfloat16,), n, H, D, "q")
-    _same_device(dev, q, out, workspace)
-    with _OnDevice(dev, stream) as s:
+    ptr, ld = _rows(q, (_BF16,), dev, n, H, D, "q")
+    context, s = _where(dev, stream)
+    with context:
         if out is None:
-            out = torch.empty((n, H, D), dtype=torch.float32, device=dev)
+            out = torch.empty((n, H, D), dtype=_F32, device=q.device)
         if workspace is None:
             workspace = torch.zeros((max(16, bw_attn_paged_decode_workspace_bytes(
-                n, H, kv.n_kv_heads, D)),), dtype=torch.uint8, device=dev)
-        o, out_ld = _rows(out, (torch.float32, torch.bfloat16), n, H, D, "out")
+                n, H, hkv, D)),), dtype=torch.uint8, device=q.device)
+        o, out_ld = _rows(out, (_F32, _BF16), dev, n, H, D, "out")
         _check(_lib.bw_attn_paged_decode(
-            ptr, ld, H, ctypes.byref(kv),
-            1.0 / D ** 0.5 if scale is None else scale, window, sinks, o,
-            out_ld, out.dtype == torch.bfloat16,
-            _dev(workspace, torch.uint8, "workspace"), workspace.numel(), s),
-            "bw_attn_paged_decode")
+            ptr, ld, H, kv, 1.0 / D ** 0.5 if scale is None else scale, window,
+            sinks, o, out_ld, out.dtype is _BF16,
+            _vector(workspace, torch.uint8, dev, 0, "workspace"),
+            workspace.numel(), s), "bw_attn_paged_decode")
     return out
 
 
@@ -669,27 +661,24 @@ def bw_attn_paged_prefill(q: torch.Tensor, k_pages: torch.Tensor,
     last positions; rows of no sequence are left as they are (zeros in an out
     made here).  window, sinks, scale, workspace as for bw_attn_paged_decode
     (bw_attn_paged_prefill_workspace_bytes)."""
-    kv = _paged_kv(k_pages, v_pages, page_table, kv_len)
-    dev, D = k_pages.device, kv.head_dim
+    kv, dev, n_seqs, hkv, D = _paged_kv(k_pages, v_pages, page_table, kv_len)
     if not isinstance(q, torch.Tensor) or q.dim() != 3:
-        raise ValueError("q must be [n_tokens][H][D]")
+        _refuse(q, (_BF16,), dev, "q must be [n_tokens][H][D]")
     n, H = q.shape[0], q.shape[1]
-    ptr, ld = _rows(q, (torch.bfloat16,), n, H, D, "q")
-    starts = _dev(q_start, torch.int32, "q_start")
-    _need(q_start, kv.n_seqs + 1, "q_start")
-    _same_device(dev, q, q_start, out, workspace)
-    with _OnDevice(dev, stream) as s:
+    ptr, ld = _rows(q, (_BF16,), dev, n, H, D, "q")
+    starts = _vector(q_start, _I32, dev, n_seqs + 1, "q_start")
+    context, s = _where(dev, stream)
+    with context:
         if out is None:
-            out = torch.zeros((n, H, D), dtype=torch.bfloat16, device=dev)
+            out = torch.zeros((n, H, D), dtype=_BF16, device=q.device)
         if workspace is None:
             workspace = torch.zeros((max(16, bw_attn_paged_prefill_workspace_bytes(
-                n, kv.n_seqs, H, kv.n_kv_heads, D)),), dtype=torch.uint8,
-                device=dev)
-        o, out_ld = _rows(out, (torch.bfloat16,), n, H, D, "out")
+                n, n_seqs, H, hkv, D)),), dtype=torch.uint8, device=q.device)
+        o, out_ld = _rows(out, (_BF16,), dev, n, H, D, "out")
         _check(_lib.bw_attn_paged_prefill(
-            ptr, ld, n, starts, H, ctypes.byref(kv),
-            1.0 / D ** 0.5 if scale is None else scale, window, sinks, o,
-            out_ld, _dev(workspace, torch.uint8, "workspace"),
+            ptr, ld, n, starts, H, kv, 1.0 / D ** 0.5 if scale is None else scale,
+            window, sinks, o, out_ld,
+            _vector(workspace, torch.uint8, dev, 0, "workspace"),
             workspace.numel(), s), "bw_attn_paged_prefill")
     return out
 
