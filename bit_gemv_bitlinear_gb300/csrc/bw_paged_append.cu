@@ -195,11 +195,21 @@ cudaError_t launch_paged_append(const PagedView &v, const AppendLaunch &l,
   a.n_tokens = l.n_tokens;
   a.H = l.H;
   a.eps = l.eps;
-  constexpr double kInv2Pi = 0.15915494309189533576888376337251;
-  for (int i = 0; i < l.D / 2; ++i) {
-    const double f = pow(double(l.theta), -2.0 * i / double(l.D)) * kInv2Pi;
-    a.turn[i] = uint64_t(ldexp(f, 64));  // f < 1: theta >= 1
+  // A table of constants by (theta, D), kept by each calling thread: 64 powers
+  // in fp64 cost more than the launch.
+  thread_local double table_theta = 0.0;
+  thread_local int table_dim = 0;
+  thread_local uint64_t table[kApMaxPairs];
+  if (table_theta != double(l.theta) || table_dim != l.D) {
+    constexpr double kInv2Pi = 0.15915494309189533576888376337251;
+    for (int i = 0; i < l.D / 2; ++i) {
+      const double f = pow(double(l.theta), -2.0 * i / double(l.D)) * kInv2Pi;
+      table[i] = uint64_t(ldexp(f, 64));  // f < 1: theta >= 1
+    }
+    table_theta = l.theta;
+    table_dim = l.D;
   }
+  for (int i = 0; i < l.D / 2; ++i) a.turn[i] = table[i];
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(l.n_tokens));
   cfg.blockDim = dim3(kApThreads);

@@ -12,13 +12,17 @@
 // o / l.
 //
 // Bound by the bytes of the visible keys and values.  Layout:
-//  * Work is cut into tiles of 64 positions of one (sequence, head); all
-//    tiles in order are dealt to the CTAs in equal contiguous shares, found
-//    on the device from the lengths, so ragged batches and long single
-//    sequences balance alike and one launch serves every step of a graph.
+//  * Work is cut into tiles of 64 positions of one (sequence, head), all tiles
+//    in one order, found on the device from the lengths, so ragged batches
+//    and long single sequences balance alike and one launch serves every step
+//    of a graph.  The first 70 % of a long call are dealt to the CTAs in equal
+//    contiguous shares, the rest in small units that a CTA claims when it is
+//    about to run out: SMs stream at unlike rates (equal shares of 50 us took
+//    42 to 61), and every piece ends in a part to be joined.
 //  * A producer warp looks up the pages and brings a tile's keys and values
 //    into a ring of shared-memory stages with tiled copies (128-byte
-//    swizzle), a lane per box; positions nobody sees are not read.
+//    swizzle), a lane per box; positions nobody sees are not read.  Next to
+//    the stage it leaves what the tile is.
 //  * Four warps take 16 positions each: scores K Q^T with the heads as the 8
 //    columns of an mma.sync, a running softmax in registers, and V^T P^T with
 //    the weights transposed in registers (movmatrix).  mma.sync and not
@@ -27,10 +31,10 @@
 //    heads as the 16 rows.  The weights enter as a sum of two (bf16 output)
 //    or three (fp32 output) bf16 values, so an fp32 result keeps fp32
 //    precision.
-//  * At the end of a share's part of a (sequence, head) the warps join in
+//  * At the end of a piece's part of a (sequence, head) the warps join in
 //    shared memory.  A part that is the whole goes straight to the output;
-//    others go to the workspace, and the CTA that finishes last (a fence and
-//    a counter; nothing waits) joins them in order and sets the counter back.
+//    others go to the workspace, and a second kernel, launched along with the
+//    first and waiting for its end, joins them.
 #include "bw_paged_tc.cuh"
 
 namespace bw {
@@ -40,6 +44,15 @@ constexpr int kDcWarps = 4;                      // consumers
 constexpr int kDcThreads = (kDcWarps + 1) * 32;  // and the producer
 constexpr int kDcTile = 64;
 constexpr int kDcMaxCtas = 320;
+constexpr int kDcMaxUnits = 4 * kDcMaxCtas + 1;  // shares and claimed units
+constexpr int kDcJoinThreads = 256;
+
+// What the workspace keeps of a (sequence, head): its parts are those of units
+// unit0 .. unit0 + parts - 1 (parts 1: the output is written already, 0: zeros
+// are).
+struct DcParts {
+  int unit0, parts;
+};
 
 struct DecodeArgs {
   PagedView v;
@@ -47,13 +60,25 @@ struct DecodeArgs {
   int64_t q_ld;
   void *out;
   int64_t out_ld;
-  float *part;          // [2 kDcMaxCtas][part_floats(G, D)]
-  unsigned int *count;  // [n_seqs][Hkv]
+  float *part;          // [2 kDcMaxUnits][part_floats(G, D)]
+  DcParts *parts;       // [n_seqs][Hkv]
+  unsigned int *claim;  // units claimed so far; zero between calls
   int H, G;
   float scale2;         // scale log2(e)
   int window, sinks;
   int box_rows;
   int min_tiles;
+};
+
+// A tile as the producer leaves it next to its stage.
+struct DcTileInfo {
+  int unit;           // -1: no more tiles
+  int b, g, len;      // sequence, key-value head, length
+  int pos;            // first position
+  int index, n;       // tile of the item's n
+  int s1, lo;         // seen: [0, s1) and [lo, len)
+  int pad;
+  int64_t first;      // first tile of the item
 };
 
 template <int D, int GH>
@@ -66,18 +91,13 @@ struct DcCfg {
   static constexpr int kStages = (D == 128 ? 3 : 6) * GH;
   static constexpr int kCtas = GH == 1 ? 2 : 1;
   static constexpr int kPad = D + 4;                       // floats a row
-  // the warps' sums [2][8 GH][kPad]; the last CTA's (m, l) and lanes' sums
-  static constexpr int kMlMax = 512 * GH;
+  // the warps' sums [3][8 GH][kPad] and (m, l)
   static constexpr uint32_t kDump = kStages * kStage;
-  static constexpr uint32_t kSums = kDump + kMlMax * 8;
-  static constexpr uint32_t kSumsBytes = kDcWarps * 32 * 20;
-  static constexpr uint32_t kDumpBytes =
-      2u * 8 * GH * kPad * 4 > kMlMax * 8 + kSumsBytes
-          ? 2u * 8 * GH * kPad * 4
-          : kMlMax * 8 + kSumsBytes;
-  static constexpr uint32_t kMl = kDump + kDumpBytes;      // [4][8 GH] float2
-  static constexpr uint32_t kBars = kMl + kDcWarps * 8 * GH * 8;
-  static constexpr uint32_t kTotal = kBars + 2 * kStages * 8;
+  static constexpr uint32_t kMl = kDump + 3u * 8 * GH * kPad * 4;
+  static constexpr uint32_t kInfo = kMl + kDcWarps * 8 * GH * 8;
+  static constexpr uint32_t kBefore = kInfo + kStages * sizeof(DcTileInfo);
+  static constexpr uint32_t kBars = kBefore + kDcThreads * 8;
+  static constexpr uint32_t kTotal = kBars + (2 * kStages + 1) * 8;
   static constexpr uint32_t kSmem = kTotal + 1024;
 };
 
@@ -116,9 +136,6 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t a) {
                : "r"(a));
   return d;
 }
-__device__ __forceinline__ void consumers_sync() {
-  asm volatile("bar.sync 1, %0;" ::"n"(kDcWarps * 32) : "memory");
-}
 // (a, b) as a bf16 pair; what the rounding leaves goes back into a and b.
 __device__ __forceinline__ uint32_t take_bf16(float &a, float &b) {
   const __nv_bfloat162 t = __floats2bfloat162_rn(a, b);
@@ -133,14 +150,41 @@ __device__ __forceinline__ TilePlan seq_plan(int len, int window, int sinks) {
   return tile_plan(len - 1, len - 1, window, sinks, kDcTile);
 }
 
-// A CTA's share, tiles [begin, end) of `total`, and where it starts.
-struct Share {
-  int64_t begin, end, total, item0;  // item0: first tile of sequence b
-  int b, n_ctas;
-  int len;  // sequence b's
+// How a call's tiles are dealt: [0, dealt) in equal shares to n_ctas CTAs
+// (units 0 .. n_ctas - 1), the rest in units of `unit` tiles.
+struct Dealing {
+  int64_t total, dealt;
+  int n_ctas, unit;
 };
+__device__ __forceinline__ Dealing deal(int64_t total, int min_tiles, int grid) {
+  Dealing d{total, total, 0, 1};
+  const int64_t n = (total + min_tiles - 1) / min_tiles;
+  d.n_ctas = n < grid ? int(n) : grid;
+  if (total >= 16 * int64_t(d.n_ctas)) {
+    const int64_t rest = total * 3 / 10;
+    d.dealt = total - rest;
+    // at most 3 units a CTA, of 4 tiles at least
+    const int64_t u = (rest + 3 * d.n_ctas - 1) / (3 * d.n_ctas);
+    d.unit = u < 4 ? 4 : int(u);
+  }
+  return d;
+}
+__device__ __forceinline__ int unit_of(const Dealing &d, int64_t tile) {
+  return tile < d.dealt ? int(((tile + 1) * d.n_ctas - 1) / d.dealt)
+                        : d.n_ctas + int((tile - d.dealt) / d.unit);
+}
+__device__ __forceinline__ void unit_range(const Dealing &d, int unit,
+                                           int64_t *lo, int64_t *hi) {
+  if (unit < d.n_ctas) {
+    *lo = unit * d.dealt / d.n_ctas;
+    *hi = (unit + 1) * d.dealt / d.n_ctas;
+  } else {
+    *lo = d.dealt + int64_t(unit - d.n_ctas) * d.unit;
+    *hi = *lo + d.unit < d.total ? *lo + d.unit : d.total;
+  }
+}
 
-// The (sequence, head) items of a share, in order.
+// A (sequence, head) and its tiles.
 struct Item {
   int b, g, len;
   TilePlan plan;
@@ -149,20 +193,25 @@ struct Item {
 
 // Both return false past the last sequence, which only lengths that change
 // under the call can bring about.
-__device__ __forceinline__ bool item_start(const DecodeArgs &a, const Share &s,
-                                           int64_t at, Item &it) {
-  // at: a tile of the share within sequence s.b or a later one
-  int64_t base = s.item0;
-  for (it.b = s.b; it.b < a.v.n_seqs; ++it.b) {
-    it.len = it.b == s.b ? s.len : seq_len(a.v, it.b);
+// The item of tile `at`; before[t]: the first tile of sequences t per and on.
+__device__ __forceinline__ bool item_at(const DecodeArgs &a,
+                                        const long long *before, int per,
+                                        int64_t at, Item &it) {
+  int n = 0;
+  for (int t = threadIdx.x & 31; t < kDcThreads; t += 32) n += before[t] <= at;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+  int64_t base = before[n - 1];
+  for (it.b = (n - 1) * per; it.b < a.v.n_seqs; ++it.b) {
+    it.len = seq_len(a.v, it.b);
     it.plan = seq_plan(it.len, a.window, a.sinks);
-    const int64_t n = int64_t(it.plan.n) * a.v.hkv;
-    if (at < base + n) {
-      it.g = int((at - base) / it.plan.n);
+    const int64_t tiles = int64_t(it.plan.n) * a.v.hkv;
+    if (at < base + tiles) {
+      it.g = int(at - base) / it.plan.n;  // below 2^24
       it.first = base + int64_t(it.g) * it.plan.n;
       return true;
     }
-    base += n;
+    base += tiles;
   }
   return false;
 }
@@ -183,10 +232,6 @@ __host__ __device__ constexpr int part_floats(int G, int D) {
   return (G * (D + 2) + 3) / 4 * 4;
 }
 
-__device__ __forceinline__ int owner_of(const Share &s, int64_t tile) {
-  return int(((tile + 1) * s.n_ctas - 1) / s.total);
-}
-
 template <int D, int GH, bool BF16>
 __global__ void __launch_bounds__(kDcThreads, (DcCfg<D, GH>::kCtas))
 decode_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap kmap,
@@ -196,9 +241,10 @@ decode_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap kmap,
   uint8_t *smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
   uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::kBars);
   uint64_t *empty = full + C::kStages;
-  __shared__ Share s_share;
+  uint64_t *joined = empty + C::kStages;  // the four warps
+  DcTileInfo *info = reinterpret_cast<DcTileInfo *>(smem + C::kInfo);
+  long long *s_before = reinterpret_cast<long long *>(smem + C::kBefore);
   __shared__ long long s_sum[kDcThreads / 32];
-  __shared__ int s_last;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
     prefetch_map(&kmap);
@@ -207,25 +253,25 @@ decode_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap kmap,
       mbar_init(&full[i], 1);
       mbar_init(&empty[i], kDcWarps);
     }
+    mbar_init(joined, kDcWarps);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    s_share.b = -1;
   }
   pdl_wait();
   pdl_trigger();
 
-  // ---- every CTA finds its share: thread t counts the tiles of sequences
-  // [t per, (t + 1) per), a scan over the CTA gives their first tiles ----
+  // ---- thread t counts the tiles of sequences [t per, (t + 1) per), a scan
+  // over the CTA gives their first tiles ----
   const int per = (a.v.n_seqs + kDcThreads - 1) / kDcThreads;
   const int b_lo = min(tid * per, a.v.n_seqs);
   const int b_hi = min(b_lo + per, a.v.n_seqs);
   long long mine = 0;
-  int len0 = 0;
   for (int b = b_lo; b < b_hi; ++b) {
     const int len = seq_len(a.v, b);
-    if (b == b_lo) len0 = len;
     mine += int64_t(seq_plan(len, a.window, a.sinks).n) * a.v.hkv;
     if (len <= 0 && b % int(gridDim.x) == int(blockIdx.x)) {
       // an empty sequence: zeros
+      for (int g = 0; g < a.v.hkv; ++g)
+        a.parts[int64_t(b) * a.v.hkv + g] = DcParts{0, 0};
       for (int e = 0; e < a.H * D; e += 8) {
         const int64_t at = int64_t(b) * a.out_ld + e;
         const uint4 z = make_uint4(0u, 0u, 0u, 0u);
@@ -252,16 +298,10 @@ decode_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap kmap,
     if (w < warp) before += s_sum[w];
     total += s_sum[w];
   }
-  long long n_ctas = (total + a.min_tiles - 1) / a.min_tiles;
-  if (n_ctas > gridDim.x) n_ctas = gridDim.x;
-  if (blockIdx.x >= n_ctas) return;  // the whole CTA, also without any tile
-  const long long begin = blockIdx.x * total / n_ctas;
-  const long long end = (blockIdx.x + 1) * total / n_ctas;
-  if (begin >= before && begin < before + mine)
-    s_share = Share{begin, end, total, before, b_lo, int(n_ctas), len0};
+  s_before[tid] = before;
+  const Dealing dl = deal(total, a.min_tiles, int(gridDim.x));
+  if (int(blockIdx.x) >= dl.n_ctas) return;  // the whole CTA
   __syncthreads();
-  const Share sh = s_share;
-  if (sh.b < 0) return;  // lengths that changed under the call
 
   if (warp == kDcWarps) {
     // ---- producer ----
@@ -275,40 +315,65 @@ decode_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap kmap,
     const int half = j % (D / 64), r0 = j / (D / 64) * a.box_rows;
     const uint32_t dst = (is_v ? C::kKBytes : 0u) + half * C::kHalf + r0 * 128;
     const bool mine_box = lane < 2 * per_kv;
+    // Keys and values are read once: they should not push the parts out of L2.
+    uint64_t once;
+    asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(once));
     Item it;
-    int stage = 0;
+    int stage = 0, unit = int(blockIdx.x);
     uint32_t round = 0;
-    bool ok = item_start(a, sh, sh.begin, it);
-    int64_t t = sh.begin;
-    int pos = 0, page = 0;
-    auto look_up = [&] {
-      pos = tile_pos(it.plan, int(t - it.first), kDcTile) + r0;
-      page = mine_box ? box_page(a.v, it.b, pos, a.box_rows, it.plan.s1,
-                                 it.plan.lo, it.len)
-                      : 0;
+    bool ok = true;
+    auto stage_free = [&] {
+      return round == 0 || warp_wait(&empty[stage], (round - 1) & 1u);
     };
-    if (ok) look_up();
-    while (ok && t < sh.end) {
-      if (round > 0 && !warp_wait(&empty[stage], (round - 1) & 1u)) {
-        ok = false;
-        break;
+    while (ok) {
+      int64_t t, end;
+      unit_range(dl, unit, &t, &end);
+      // the next unit is claimed shortly before this one is copied
+      unsigned int claimed = 0;
+      const bool dynamic = dl.dealt < dl.total;
+      const int64_t claim_at = end - t > 2 ? end - 2 : t;
+      ok = item_at(a, s_before, per, t, it);
+      int pos = 0, page = 0;
+      auto look_up = [&] {
+        pos = tile_pos(it.plan, int(t - it.first), kDcTile);
+        page = mine_box ? box_page(a.v, it.b, pos + r0, a.box_rows, it.plan.s1,
+                                   it.plan.lo, it.len)
+                        : 0;
+      };
+      if (ok) look_up();
+      while (ok) {
+        if (dynamic && t == claim_at && lane == 0) claimed = atomicAdd(a.claim, 1u);
+        ok = stage_free();
+        if (!ok) break;
+        if (lane == 0) {
+          info[stage] = DcTileInfo{unit, it.b, it.g, it.len, pos,
+                                   int(t - it.first), it.plan.n, it.plan.s1,
+                                   it.plan.lo, 0, it.first};
+          mbar_arrive_expect_tx(&full[stage], C::kStage);
+        }
+        __syncwarp();
+        if (mine_box)
+          tma_load_4d_once(smem + stage * C::kStage + dst, is_v ? &vmap : &kmap,
+                           half * 64, (pos + r0) & ((1 << a.v.page_shift) - 1),
+                           it.g, page, &full[stage], once);
+        if (++stage == C::kStages) {
+          stage = 0;
+          ++round;
+        }
+        if (++t == end) break;
+        if (t >= it.first + it.plan.n) ok = item_next(a, it);
+        if (ok) look_up();
       }
-      if (lane == 0) mbar_arrive_expect_tx(&full[stage], C::kStage);
-      __syncwarp();
-      if (mine_box)
-        tma_load_4d(smem + stage * C::kStage + dst, is_v ? &vmap : &kmap,
-                    half * 64, pos & ((1 << a.v.page_shift) - 1), it.g, page,
-                    &full[stage]);
-      if (++stage == C::kStages) {
-        stage = 0;
-        ++round;
-      }
-      if (++t == sh.end) break;
-      if (t >= it.first + it.plan.n && !item_next(a, it)) {
-        ok = false;
-        break;
-      }
-      look_up();
+      if (!ok || !dynamic) break;
+      claimed = __shfl_sync(0xffffffffu, claimed, 0);
+      if (int64_t(claimed) * dl.unit >= dl.total - dl.dealt) break;
+      unit = dl.n_ctas + int(claimed);
+    }
+    // no more tiles (also after a wait that ran out)
+    if (ok) ok = stage_free();
+    if (ok && lane == 0) {
+      info[stage].unit = -1;
+      mbar_arrive(&full[stage]);
     }
     // The stages in flight land before the CTA may leave (only after a
     // time-out are they not consumed first).
@@ -328,18 +393,34 @@ decode_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap kmap,
   const int G = a.G;
   float *dump = reinterpret_cast<float *>(smem + C::kDump);
   float2 *ml = reinterpret_cast<float2 *>(smem + C::kMl);
-  Item it;
   int stage = 0;
   uint32_t round = 0;
-  int64_t t = sh.begin;
-  // After a wait that ran out (never expected; reported, the result is lost)
-  // a warp goes through the rest without waiting, so that no barrier of the
-  // CTA and no counter is left short.
-  bool ok = true;
-  bool more = item_start(a, sh, sh.begin, it);
-  while (more && t < sh.end) {
-    const int64_t part_end = min(sh.end, it.first + it.plan.n);
-    const bool from_start = t == it.first;
+  // After a wait that runs out (never expected; reported, the result is lost)
+  // a warp takes it that there are no more tiles, and waits for nobody.
+  uint32_t joins = 0;
+  bool alone = false;
+  auto consumers_sync = [&] {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(joined);
+    if (!alone && !warp_wait(joined, joins & 1u)) {
+      if (lane == 0) atomicOr(a.v.err, 4u);
+      alone = true;
+    }
+    ++joins;
+  };
+  auto next_tile = [&](DcTileInfo &t) {
+    if (!warp_wait(&full[stage], round & 1u)) {
+      if (lane == 0) atomicOr(a.v.err, 4u);
+      t.unit = -1;
+      alone = true;
+    } else {
+      t = info[stage];
+    }
+  };
+  DcTileInfo t;
+  next_tile(t);
+  while (t.unit >= 0) {
+    const DcTileInfo it = t;  // the part's first tile
     // the queries of this head group as B fragments (columns past G: zero)
     uint32_t qf[GH][D / 16][2];
     {
@@ -366,19 +447,15 @@ decode_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap kmap,
       m[nt][0] = m[nt][1] = -INFINITY;
       l[nt][0] = l[nt][1] = 0.0f;
     }
-    for (; t < part_end; ++t) {
-      const int pos = tile_pos(it.plan, int(t - it.first), kDcTile) + 16 * warp;
-      if (ok && !warp_wait(&full[stage], round & 1u)) {
-        if (lane == 0) atomicOr(a.v.err, 4u);
-        ok = false;
-      }
-      const int s1 = it.plan.s1, lo = it.plan.lo, hi = it.len;
+    while (t.unit == it.unit && t.first == it.first) {
+      const int pos = t.pos + 16 * warp;
+      const int s1 = it.s1, lo = it.lo, hi = it.len;
       auto sees = [&](int j) { return j < hi && (j >= lo || j < s1); };
       const bool all = pos >= lo && pos + 16 <= hi;
       const bool none = pos >= hi || (pos >= s1 && pos + 16 <= lo);
       uint8_t *ks = smem + stage * C::kStage;
       uint8_t *vs = ks + C::kKBytes;
-      if (!none && ok) {
+      if (!none) {
         float c[GH][2][4] = {};  // even and odd steps: shorter chains
         const int krow = 16 * warp + (lane & 15);
 #pragma unroll
@@ -487,9 +564,10 @@ decode_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap kmap,
         stage = 0;
         ++round;
       }
+      next_tile(t);
     }
 
-    // ---- the four warps join: weights for each, then the sums in pairs ----
+    // ---- the four warps join: weights for each, then warp 0 sums ----
 #pragma unroll
     for (int nt = 0; nt < GH; ++nt)
 #pragma unroll
@@ -529,20 +607,20 @@ decode_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap kmap,
     auto at = [&](int nt, int i, int u) {
       return (8 * nt + fc + (u & 1)) * C::kPad + 16 * i + fr + 8 * (u >> 1);
     };
+    if (warp > 0) {
+      float *to = dump + (warp - 1) * 8 * GH * C::kPad;
 #pragma unroll
-    for (int step = 2; step > 0; step >>= 1) {
-      if (warp >= step && warp < 2 * step) {
-        float *to = dump + (warp - step) * 8 * GH * C::kPad;
+      for (int nt = 0; nt < GH; ++nt)
 #pragma unroll
-        for (int nt = 0; nt < GH; ++nt)
+        for (int i = 0; i < D / 16; ++i)
 #pragma unroll
-          for (int i = 0; i < D / 16; ++i)
+          for (int u = 0; u < 4; ++u) to[at(nt, i, u)] = o[nt][i][u];
+    }
+    consumers_sync();
+    if (warp == 0) {
 #pragma unroll
-            for (int u = 0; u < 4; ++u) to[at(nt, i, u)] = o[nt][i][u];
-      }
-      consumers_sync();
-      if (warp < step) {
-        const float *from = dump + warp * 8 * GH * C::kPad;
+      for (int k = 0; k < kDcWarps - 1; ++k) {
+        const float *from = dump + k * 8 * GH * C::kPad;
 #pragma unroll
         for (int nt = 0; nt < GH; ++nt)
 #pragma unroll
@@ -550,16 +628,21 @@ decode_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap kmap,
 #pragma unroll
             for (int u = 0; u < 4; ++u) o[nt][i][u] += from[at(nt, i, u)];
       }
-      consumers_sync();
     }
+    // (Warp 0 is done with the sums, and every warp with the (m, l), before it
+    // joins again: nothing else keeps the next part's from theirs.)
 
     // ---- out, or to the workspace ----
-    const int c0 = owner_of(sh, it.first);
-    const int parts = owner_of(sh, it.first + it.plan.n - 1) - c0 + 1;
+    const int unit0 = unit_of(dl, it.first);
+    const int parts = unit_of(dl, it.first + it.n - 1) - unit0 + 1;
     const int64_t row = int64_t(it.b) * a.out_ld + int64_t(it.g) * G * D;
     const int stride = part_floats(G, D);
     if (warp == 0) {
-      float *p = a.part + int64_t(2 * blockIdx.x + (from_start ? 1 : 0)) * stride;
+      // slot 2 unit + 1 for a part that begins its item, else 2 unit: a unit
+      // has at most one of each
+      float *p = a.part + int64_t(2 * it.unit + (it.index == 0 ? 1 : 0)) * stride;
+      if (it.index == 0 && lane == 0)
+        a.parts[int64_t(it.b) * a.v.hkv + it.g] = DcParts{unit0, parts};
 #pragma unroll
       for (int nt = 0; nt < GH; ++nt)
 #pragma unroll
@@ -587,121 +670,147 @@ decode_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap kmap,
           }
         }
     }
-    if (parts > 1) {
-      if (warp == 0) {
-        __threadfence();
-        __syncwarp();
-        if (lane == 0) {
-          unsigned int *cnt = a.count + int64_t(it.b) * a.v.hkv + it.g;
-          const bool last = atomicAdd(cnt, 1u) == unsigned(parts) - 1u;
-          if (last) *cnt = 0u;
-          s_last = last;
+  }
+}
+
+// Joins the parts of the query heads: block x takes heads x, x + grid, ... of
+// all (sequence, query head) in order.  A warp joins a head of few parts by
+// itself (most heads of a batch); the block does one of many parts together:
+// thread (lane, vector v) sums parts lane, lane + lanes, ... of four outputs.
+// 8 loads are in flight in both, the first before the maximum is known.
+constexpr int kDcFewParts = 16;
+template <int D, bool BF16>
+__global__ void __launch_bounds__(kDcJoinThreads)
+decode_join_kernel(const DecodeArgs a, int heads) {
+  __shared__ float s_max[kDcJoinThreads / 32];
+  __shared__ float4 s_acc[kDcJoinThreads];
+  __shared__ float s_sum[kDcJoinThreads / (D / 4)];
+  pdl_wait();
+  pdl_trigger();
+  if (blockIdx.x == 0 && threadIdx.x == 0) *a.claim = 0u;  // for the next call
+  const int stride = part_floats(a.G, D);
+  const int n = a.v.n_seqs * a.H;
+
+  // One head by `threads` threads (this one is `tid`): a warp or the block.
+  auto join = [&](int head, const DcParts &ps, int tid, auto whole) {
+    constexpr bool kBlock = decltype(whole)::value;
+    constexpr int kThreads = kBlock ? kDcJoinThreads : 32;
+    constexpr int kVec = D / 4;
+    constexpr int kLanes = kThreads / kVec;  // 1 or 2 of a warp
+    const int v = tid % kVec, lane = tid / kVec;
+    const int item = head / a.G, h = head - item * a.G;
+    const float *base = a.part + int64_t(2 * ps.unit0) * stride;
+    auto slot = [&](int i) {
+      return base + int64_t(2 * i + (i == 0 ? 1 : 0)) * stride;
+    };
+    auto ml = [&](int i) {
+      return __ldcg(reinterpret_cast<const float2 *>(slot(i) + a.G * D) + h);
+    };
+    constexpr int kAhead = 8;
+    float4 x[kAhead];
+    float2 y[kAhead];
+    auto load = [&](int i0) {
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        const int i = i0 + u * kLanes;
+        if (i < ps.parts) {
+          x[u] = __ldcg(reinterpret_cast<const float4 *>(slot(i) + h * D) + v);
+          y[u] = ml(i);
         }
       }
-      consumers_sync();
-      if (s_last) {
-        // The first part's slot is 2 c0 + 1, the others' 2 c.  Thread (vector
-        // v, lane gi) sums the parts gi, gi + ng, ... of four outputs; (m, l)
-        // of up to kMlMax / G parts at a time lie in shared memory, and 16
-        // outputs' loads are in flight at once (the first before the maximum
-        // is known).
-        __threadfence();
-        const int nv = G * D / 4, ng = nv >= kDcWarps * 32 ? 1 : kDcWarps * 32 / nv;
-        const int chunk = C::kMlMax / G;
-        float2 *mlc = reinterpret_cast<float2 *>(dump);
-        float4 *sums = reinterpret_cast<float4 *>(smem + C::kSums);
-        float *sums_l = reinterpret_cast<float *>(sums + kDcWarps * 32);
-        auto slot = [&](int i) {
-          return a.part + int64_t(2 * (c0 + i) + (i == 0 ? 1 : 0)) * stride;
-        };
-        for (int v0 = 0; v0 < nv; v0 += kDcWarps * 32) {
-          const int gi = tid / nv, v = v0 + tid - gi * nv;
-          const bool on = v < nv && gi < ng;
-          const int h = on ? v / (D / 4) : 0;
-          float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-          float sum = 0.0f, mx = -INFINITY;
-          for (int p0 = 0; p0 < parts; p0 += chunk) {
-            const int n = min(chunk, parts - p0);
-            float4 x[16];
-            auto load = [&](int i0) {
+    };
+    load(lane);
+    float mx = -INFINITY;
+    for (int i = tid; i < ps.parts; i += kThreads) mx = fmaxf(mx, ml(i).x);
 #pragma unroll
-              for (int u = 0; u < 16; ++u)
-                if (on && i0 + u * ng < n)
-                  x[u] = __ldcg(reinterpret_cast<const float4 *>(
-                                    slot(p0 + i0 + u * ng)) + v);
-            };
-            load(gi);
-            for (int e = tid; e < n * G; e += kDcWarps * 32)
-              mlc[e] = __ldcg(reinterpret_cast<const float2 *>(
-                                  slot(p0 + e / G) + G * D) + e % G);
-            consumers_sync();
-            const float m_old = mx;
-#pragma unroll 8
-            for (int i = 0; i < n; ++i) mx = fmaxf(mx, mlc[i * G + h].x);
-            const float f = m_old == -INFINITY ? 0.0f : ex2(m_old - mx);
-            sum *= f;
-            acc.x *= f;
-            acc.y *= f;
-            acc.z *= f;
-            acc.w *= f;
-            for (int i0 = gi; i0 < n; i0 += 16 * ng) {
-              if (i0 != gi) load(i0);
+    for (int o = 16; o > 0; o >>= 1)
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    if (kBlock) {
+      if ((tid & 31) == 0) s_max[tid >> 5] = mx;
+      __syncthreads();
 #pragma unroll
-              for (int u = 0; u < 16; ++u) {
-                const int i = i0 + u * ng;
-                if (i >= n) break;
-                const float2 y = mlc[i * G + h];
-                const float w = y.x == -INFINITY ? 0.0f : ex2(y.x - mx);
-                sum = fmaf(w, y.y, sum);
-                acc.x = fmaf(w, x[u].x, acc.x);
-                acc.y = fmaf(w, x[u].y, acc.y);
-                acc.z = fmaf(w, x[u].z, acc.z);
-                acc.w = fmaf(w, x[u].w, acc.w);
-              }
-            }
-            consumers_sync();
-          }
-          if (ng > 1) {
-            sums[tid] = acc;
-            sums_l[tid] = sum;
-            consumers_sync();
-            if (gi == 0)
-              for (int k = 1; k < ng; ++k) {
-                const float4 y = sums[k * nv + v];
-                acc.x += y.x;
-                acc.y += y.y;
-                acc.z += y.z;
-                acc.w += y.w;
-                sum += sums_l[k * nv + v];
-              }
-          }
-          if (on && gi == 0) {
-            const float inv = 1.0f / sum;
-            const int64_t e = row + 4 * v;
-            if (BF16) {
-              const __nv_bfloat162 y0 = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
-              const __nv_bfloat162 y1 = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
-              uint2 w;
-              w.x = *reinterpret_cast<const uint32_t *>(&y0);
-              w.y = *reinterpret_cast<const uint32_t *>(&y1);
-              *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.out) + e) = w;
-            } else {
-              *reinterpret_cast<float4 *>(static_cast<float *>(a.out) + e) =
-                  make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
-            }
-          }
-        }
-      }
-      consumers_sync();  // s_last is read before it is written again
+      for (int w = 0; w < kDcJoinThreads / 32; ++w) mx = fmaxf(mx, s_max[w]);
     }
-    if (t < sh.end) more = item_next(a, it);
+    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    float sum = 0.0f;
+    for (int i0 = lane; i0 < ps.parts; i0 += kAhead * kLanes) {
+      if (i0 != lane) load(i0);
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u)
+        if (i0 + u * kLanes < ps.parts) {
+          const float w = y[u].x == -INFINITY ? 0.0f : ex2(y[u].x - mx);
+          sum = fmaf(w, y[u].y, sum);
+          acc.x = fmaf(w, x[u].x, acc.x);
+          acc.y = fmaf(w, x[u].y, acc.y);
+          acc.z = fmaf(w, x[u].z, acc.z);
+          acc.w = fmaf(w, x[u].w, acc.w);
+        }
+    }
+    if (kBlock) {
+      s_acc[tid] = acc;
+      if (v == 0) s_sum[lane] = sum;
+      __syncthreads();
+#pragma unroll
+      for (int k = 1; k < kLanes; ++k) {
+        const float4 z = s_acc[(k * kVec + v)];
+        acc.x += z.x;
+        acc.y += z.y;
+        acc.z += z.z;
+        acc.w += z.w;
+        sum += s_sum[k];
+      }
+    } else if (kLanes == 2) {
+      acc.x += __shfl_down_sync(0xffffffffu, acc.x, 16);
+      acc.y += __shfl_down_sync(0xffffffffu, acc.y, 16);
+      acc.z += __shfl_down_sync(0xffffffffu, acc.z, 16);
+      acc.w += __shfl_down_sync(0xffffffffu, acc.w, 16);
+      sum += __shfl_down_sync(0xffffffffu, sum, 16);
+    }
+    if (lane == 0) {
+      const float inv = 1.0f / sum;
+      const int b = head / a.H, hh = head - b * a.H;
+      const int64_t e = int64_t(b) * a.out_ld + int64_t(hh) * D + 4 * v;
+      if (BF16) {
+        const __nv_bfloat162 y0 = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
+        const __nv_bfloat162 y1 = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
+        uint2 w;
+        w.x = *reinterpret_cast<const uint32_t *>(&y0);
+        w.y = *reinterpret_cast<const uint32_t *>(&y1);
+        *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.out) + e) = w;
+      } else {
+        *reinterpret_cast<float4 *>(static_cast<float *>(a.out) + e) =
+            make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+      }
+    }
+    if (kBlock) __syncthreads();  // the shared sums serve again
+  };
+  // (a workspace that holds something else than the kernel before left there
+  // is not followed)
+  auto parts_of = [&](int head) {
+    DcParts ps = a.parts[head / a.G];
+    if (ps.unit0 < 0 || ps.parts > kDcMaxUnits || ps.unit0 > kDcMaxUnits - ps.parts)
+      ps.parts = 0;
+    return ps;
+  };
+  const int first = blockIdx.x, step = gridDim.x;
+  const int warp = threadIdx.x >> 5, few = heads > 1 ? kDcFewParts : 1;
+  if (warp < heads && first + warp * step < n) {
+    const int head = first + warp * step;
+    const DcParts ps = parts_of(head);
+    if (ps.parts > 1 && ps.parts <= few)
+      join(head, ps, threadIdx.x & 31, std::false_type{});
+  }
+  for (int k = 0; k < heads && first + k * step < n; ++k) {
+    const int head = first + k * step;
+    const DcParts ps = parts_of(head);
+    if (ps.parts > few) join(head, ps, threadIdx.x, std::true_type{});
   }
 }
 
 size_t align256(size_t b) { return (b + 255) / 256 * 256; }
 
 size_t part_bytes(int G, int D) {
-  return align256(size_t(2) * kDcMaxCtas * part_floats(G, D) * sizeof(float));
+  return align256(size_t(2) * kDcMaxUnits * part_floats(G, D) * sizeof(float));
 }
 
 template <int D, int GH, bool BF16>
@@ -709,7 +818,7 @@ cudaError_t launch_t(const DecodeArgs &a, const CUtensorMap &kmap,
                      const CUtensorMap &vmap, cudaStream_t stream) {
   static std::atomic<int> cached[64];
   int resident = 0;
-  const cudaError_t e =
+  cudaError_t e =
       paged_resident(decode_kernel<D, GH, BF16>, cached, kDcThreads,
                      DcCfg<D, GH>::kSmem, &resident);
   if (e != cudaSuccess) return e;
@@ -730,7 +839,16 @@ cudaError_t launch_t(const DecodeArgs &a, const CUtensorMap &kmap,
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, decode_kernel<D, GH, BF16>, a, kmap, vmap);
+  e = cudaLaunchKernelEx(&cfg, decode_kernel<D, GH, BF16>, a, kmap, vmap);
+  if (e != cudaSuccess) return e;
+  // A block for each head while the blocks fit on the device at once (few
+  // heads, so likely many parts each), else one for 8 heads.
+  const unsigned n = unsigned(a.v.n_seqs) * unsigned(a.H);
+  const int heads = n <= 2u * unsigned(device_sm_count()) ? 1 : 8;
+  cfg.gridDim = dim3((n + heads - 1) / heads);
+  cfg.blockDim = dim3(kDcJoinThreads);
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&cfg, decode_join_kernel<D, BF16>, a, heads);
 }
 
 template <int D>
@@ -747,7 +865,7 @@ cudaError_t launch_d(const DecodeArgs &a, const CUtensorMap &kmap,
 
 size_t paged_decode_workspace_bytes(int n_seqs, int H, int Hkv, int D) {
   return part_bytes(H / Hkv, D) +
-         align256(size_t(n_seqs) * Hkv * sizeof(unsigned int));
+         align256(size_t(n_seqs) * Hkv * sizeof(DcParts)) + 256;
 }
 
 cudaError_t launch_paged_decode(const PagedView &v, const PagedAttnLaunch &l,
@@ -761,8 +879,9 @@ cudaError_t launch_paged_decode(const PagedView &v, const PagedAttnLaunch &l,
   a.H = l.H;
   a.G = l.H / v.hkv;
   a.part = static_cast<float *>(l.workspace);
-  a.count = reinterpret_cast<unsigned int *>(
-      static_cast<uint8_t *>(l.workspace) + part_bytes(a.G, l.D));
+  uint8_t *rest = static_cast<uint8_t *>(l.workspace) + part_bytes(a.G, l.D);
+  a.claim = reinterpret_cast<unsigned int *>(rest);
+  a.parts = reinterpret_cast<DcParts *>(rest + 256);
   a.scale2 = l.scale * kLog2e;
   a.window = l.window;
   a.sinks = l.sinks;
