@@ -44,8 +44,7 @@ constexpr int kDcWarps = 4;                      // consumers
 constexpr int kDcThreads = (kDcWarps + 1) * 32;  // and the producer
 constexpr int kDcTile = 64;
 constexpr int kDcMaxCtas = 320;
-constexpr int kDcMaxUnits = 4 * kDcMaxCtas + 1;  // shares and claimed units
-constexpr int kDcJoinThreads = 256;
+constexpr int kDcMaxUnits = 5 * kDcMaxCtas;      // shares and claimed units
 
 // What the workspace keeps of a (sequence, head): its parts are those of units
 // unit0 .. unit0 + parts - 1 (parts 1: the output is written already, 0: zeros
@@ -75,10 +74,10 @@ struct DcTileInfo {
   int unit;           // -1: no more tiles
   int b, g, len;      // sequence, key-value head, length
   int pos;            // first position
-  int index, n;       // tile of the item's n
+  int starts;         // the item's first tile
   int s1, lo;         // seen: [0, s1) and [lo, len)
-  int pad;
-  int64_t first;      // first tile of the item
+  int unit0, parts;   // of the item
+  int pad[2];
 };
 
 template <int D, int GH>
@@ -96,8 +95,9 @@ struct DcCfg {
   static constexpr uint32_t kMl = kDump + 3u * 8 * GH * kPad * 4;
   static constexpr uint32_t kInfo = kMl + kDcWarps * 8 * GH * 8;
   static constexpr uint32_t kBefore = kInfo + kStages * sizeof(DcTileInfo);
-  static constexpr uint32_t kBars = kBefore + kDcThreads * 8;
-  static constexpr uint32_t kTotal = kBars + (2 * kStages + 1) * 8;
+  static constexpr uint32_t kLen0 = kBefore + kDcThreads * 8;
+  static constexpr uint32_t kBars = kLen0 + kDcThreads * 4;
+  static constexpr uint32_t kTotal = kBars + (2 * kStages + 2) * 8;
   static constexpr uint32_t kSmem = kTotal + 1024;
 };
 
@@ -151,36 +151,47 @@ __device__ __forceinline__ TilePlan seq_plan(int len, int window, int sinks) {
 }
 
 // How a call's tiles are dealt: [0, dealt) in equal shares to n_ctas CTAs
-// (units 0 .. n_ctas - 1), the rest in units of `unit` tiles.
+// (units 0 .. n_ctas - 1); [dealt, late) in units of unit_a tiles, the rest in
+// units of unit_b, both claimed.  Few tiles are all dealt.
 struct Dealing {
-  int64_t total, dealt;
-  int n_ctas, unit;
+  int64_t total, dealt, late;
+  int n_ctas, n_a, unit_a, unit_b;
 };
 __device__ __forceinline__ Dealing deal(int64_t total, int min_tiles, int grid) {
-  Dealing d{total, total, 0, 1};
+  Dealing d{total, total, total, 0, 0, 1, 1};
   const int64_t n = (total + min_tiles - 1) / min_tiles;
   d.n_ctas = n < grid ? int(n) : grid;
   if (total >= 16 * int64_t(d.n_ctas)) {
-    const int64_t rest = total * 3 / 10;
-    d.dealt = total - rest;
-    // at most 3 units a CTA, of 4 tiles at least
-    const int64_t u = (rest + 3 * d.n_ctas - 1) / (3 * d.n_ctas);
-    d.unit = u < 4 ? 4 : int(u);
+    // 20 % in at most 1.5 units a CTA, 10 % in at most 2: the shorter the
+    // unit, the less the last one keeps the call waiting, and the more parts
+    // there are to join.
+    d.late = total - total / 10;
+    d.dealt = d.late - total / 5;
+    const int64_t ua = (2 * (d.late - d.dealt) + 3 * d.n_ctas - 1) / (3 * d.n_ctas);
+    const int64_t ub = (total - d.late + 2 * d.n_ctas - 1) / (2 * d.n_ctas);
+    d.unit_a = ua < 4 ? 4 : int(ua);
+    d.unit_b = ub < 2 ? 2 : int(ub);
+    d.n_a = int((d.late - d.dealt + d.unit_a - 1) / d.unit_a);
   }
   return d;
 }
 __device__ __forceinline__ int unit_of(const Dealing &d, int64_t tile) {
-  return tile < d.dealt ? int(((tile + 1) * d.n_ctas - 1) / d.dealt)
-                        : d.n_ctas + int((tile - d.dealt) / d.unit);
+  if (tile < d.dealt) return int(((tile + 1) * d.n_ctas - 1) / d.dealt);
+  if (tile < d.late) return d.n_ctas + int((tile - d.dealt) / d.unit_a);
+  return d.n_ctas + d.n_a + int((tile - d.late) / d.unit_b);
 }
+// The tiles of a unit (none past the last unit).
 __device__ __forceinline__ void unit_range(const Dealing &d, int unit,
                                            int64_t *lo, int64_t *hi) {
   if (unit < d.n_ctas) {
     *lo = unit * d.dealt / d.n_ctas;
     *hi = (unit + 1) * d.dealt / d.n_ctas;
+  } else if (unit < d.n_ctas + d.n_a) {
+    *lo = d.dealt + int64_t(unit - d.n_ctas) * d.unit_a;
+    *hi = *lo + d.unit_a < d.late ? *lo + d.unit_a : d.late;
   } else {
-    *lo = d.dealt + int64_t(unit - d.n_ctas) * d.unit;
-    *hi = *lo + d.unit < d.total ? *lo + d.unit : d.total;
+    *lo = d.late + int64_t(unit - d.n_ctas - d.n_a) * d.unit_b;
+    *hi = *lo + d.unit_b < d.total ? *lo + d.unit_b : d.total;
   }
 }
 
@@ -193,17 +204,20 @@ struct Item {
 
 // Both return false past the last sequence, which only lengths that change
 // under the call can bring about.
-// The item of tile `at`; before[t]: the first tile of sequences t per and on.
+// The item of tile `at`; before[t]: the first tile of sequences t per and on,
+// len0[t]: the first one's length.
 __device__ __forceinline__ bool item_at(const DecodeArgs &a,
-                                        const long long *before, int per,
-                                        int64_t at, Item &it) {
+                                        const long long *before,
+                                        const int *len0, int per, int64_t at,
+                                        Item &it) {
   int n = 0;
   for (int t = threadIdx.x & 31; t < kDcThreads; t += 32) n += before[t] <= at;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
   int64_t base = before[n - 1];
-  for (it.b = (n - 1) * per; it.b < a.v.n_seqs; ++it.b) {
-    it.len = seq_len(a.v, it.b);
+  const int b0 = (n - 1) * per;
+  for (it.b = b0; it.b < a.v.n_seqs; ++it.b) {
+    it.len = it.b == b0 ? len0[n - 1] : seq_len(a.v, it.b);
     it.plan = seq_plan(it.len, a.window, a.sinks);
     const int64_t tiles = int64_t(it.plan.n) * a.v.hkv;
     if (at < base + tiles) {
@@ -241,9 +255,11 @@ decode_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap kmap,
   uint8_t *smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
   uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::kBars);
   uint64_t *empty = full + C::kStages;
-  uint64_t *joined = empty + C::kStages;  // the four warps
+  uint64_t *joined = empty + C::kStages;  // three warps' sums are there
+  uint64_t *taken = joined + 1;           // and have been added up
   DcTileInfo *info = reinterpret_cast<DcTileInfo *>(smem + C::kInfo);
   long long *s_before = reinterpret_cast<long long *>(smem + C::kBefore);
+  int *s_len0 = reinterpret_cast<int *>(smem + C::kLen0);
   __shared__ long long s_sum[kDcThreads / 32];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
@@ -253,7 +269,8 @@ decode_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap kmap,
       mbar_init(&full[i], 1);
       mbar_init(&empty[i], kDcWarps);
     }
-    mbar_init(joined, kDcWarps);
+    mbar_init(joined, kDcWarps - 1);
+    mbar_init(taken, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   pdl_wait();
@@ -267,6 +284,7 @@ decode_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap kmap,
   long long mine = 0;
   for (int b = b_lo; b < b_hi; ++b) {
     const int len = seq_len(a.v, b);
+    if (b == b_lo) s_len0[tid] = len;
     mine += int64_t(seq_plan(len, a.window, a.sinks).n) * a.v.hkv;
     if (len <= 0 && b % int(gridDim.x) == int(blockIdx.x)) {
       // an empty sequence: zeros
@@ -332,7 +350,13 @@ decode_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap kmap,
       unsigned int claimed = 0;
       const bool dynamic = dl.dealt < dl.total;
       const int64_t claim_at = end - t > 2 ? end - 2 : t;
-      ok = item_at(a, s_before, per, t, it);
+      ok = item_at(a, s_before, s_len0, per, t, it);
+      int unit0 = 0, parts = 0;  // of the item
+      auto count_parts = [&] {
+        unit0 = unit_of(dl, it.first);
+        parts = unit_of(dl, it.first + it.plan.n - 1) - unit0 + 1;
+      };
+      if (ok) count_parts();
       int pos = 0, page = 0;
       auto look_up = [&] {
         pos = tile_pos(it.plan, int(t - it.first), kDcTile);
@@ -346,9 +370,8 @@ decode_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap kmap,
         ok = stage_free();
         if (!ok) break;
         if (lane == 0) {
-          info[stage] = DcTileInfo{unit, it.b, it.g, it.len, pos,
-                                   int(t - it.first), it.plan.n, it.plan.s1,
-                                   it.plan.lo, 0, it.first};
+          info[stage] = DcTileInfo{unit, it.b, it.g, it.len, pos, t == it.first,
+                                   it.plan.s1, it.plan.lo, unit0, parts, {}};
           mbar_arrive_expect_tx(&full[stage], C::kStage);
         }
         __syncwarp();
@@ -361,13 +384,18 @@ decode_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap kmap,
           ++round;
         }
         if (++t == end) break;
-        if (t >= it.first + it.plan.n) ok = item_next(a, it);
+        if (t >= it.first + it.plan.n) {
+          ok = item_next(a, it);
+          if (ok) count_parts();
+        }
         if (ok) look_up();
       }
       if (!ok || !dynamic) break;
       claimed = __shfl_sync(0xffffffffu, claimed, 0);
-      if (int64_t(claimed) * dl.unit >= dl.total - dl.dealt) break;
+      // (at most 3.5 units and one claim too many a CTA)
       unit = dl.n_ctas + int(claimed);
+      unit_range(dl, unit, &t, &end);
+      if (t >= dl.total) break;
     }
     // no more tiles (also after a wait that ran out)
     if (ok) ok = stage_free();
@@ -399,14 +427,11 @@ decode_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap kmap,
   // a warp takes it that there are no more tiles, and waits for nobody.
   uint32_t joins = 0;
   bool alone = false;
-  auto consumers_sync = [&] {
-    __syncwarp();
-    if (lane == 0) mbar_arrive(joined);
-    if (!alone && !warp_wait(joined, joins & 1u)) {
+  auto wait_for = [&](uint64_t *b, uint32_t phase) {
+    if (!alone && !warp_wait(b, phase & 1u)) {
       if (lane == 0) atomicOr(a.v.err, 4u);
       alone = true;
     }
-    ++joins;
   };
   auto next_tile = [&](DcTileInfo &t) {
     if (!warp_wait(&full[stage], round & 1u)) {
@@ -417,27 +442,39 @@ decode_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap kmap,
       t = info[stage];
     }
   };
+  // The queries of a head group as B fragments (columns past G: zero); the
+  // first part's are loaded while its first tile is copied.
+  uint32_t qf[GH][D / 16][2];
+  auto load_q = [&](int b, int g) {
+    const __nv_bfloat16 *q0 = a.q + int64_t(b) * a.q_ld + int64_t(g) * G * D;
+#pragma unroll
+    for (int nt = 0; nt < GH; ++nt)
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk)
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+          qf[nt][kk][u] =
+              8 * nt + fr < G
+                  ? __ldcg(reinterpret_cast<const unsigned int *>(
+                        q0 + (8 * nt + fr) * D + 16 * kk + fc + 8 * u))
+                  : 0u;
+  };
+  bool first_part = false;
+  {
+    int64_t lo, hi;
+    Item it;
+    unit_range(dl, int(blockIdx.x), &lo, &hi);
+    if (item_at(a, s_before, s_len0, per, lo, it)) {
+      load_q(it.b, it.g);
+      first_part = true;
+    }
+  }
   DcTileInfo t;
   next_tile(t);
   while (t.unit >= 0) {
     const DcTileInfo it = t;  // the part's first tile
-    // the queries of this head group as B fragments (columns past G: zero)
-    uint32_t qf[GH][D / 16][2];
-    {
-      const __nv_bfloat16 *q0 =
-          a.q + int64_t(it.b) * a.q_ld + int64_t(it.g) * G * D;
-#pragma unroll
-      for (int nt = 0; nt < GH; ++nt)
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk)
-#pragma unroll
-          for (int u = 0; u < 2; ++u)
-            qf[nt][kk][u] =
-                8 * nt + fr < G
-                    ? __ldcg(reinterpret_cast<const unsigned int *>(
-                          q0 + (8 * nt + fr) * D + 16 * kk + fc + 8 * u))
-                    : 0u;
-    }
+    if (!first_part) load_q(it.b, it.g);
+    first_part = false;
     // Output^T: rows dims 16 i + fr (+ 8), columns heads 8 nt + fc (+ 1);
     // maximum and sum of those two heads.
     float o[GH][D / 16][4] = {};
@@ -447,7 +484,7 @@ decode_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap kmap,
       m[nt][0] = m[nt][1] = -INFINITY;
       l[nt][0] = l[nt][1] = 0.0f;
     }
-    while (t.unit == it.unit && t.first == it.first) {
+    while (t.unit == it.unit && t.b == it.b && t.g == it.g) {
       const int pos = t.pos + 16 * warp;
       const int s1 = it.s1, lo = it.lo, hi = it.len;
       auto sees = [&](int j) { return j < hi && (j >= lo || j < s1); };
@@ -567,109 +604,101 @@ decode_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap kmap,
       next_tile(t);
     }
 
-    // ---- the four warps join: weights for each, then warp 0 sums ----
+    // ---- the four warps join: three leave their sums in shared memory and go
+    // on, warp 0 adds them up and stores ----
 #pragma unroll
     for (int nt = 0; nt < GH; ++nt)
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
+      for (int u = 0; u < 2; ++u)
 #pragma unroll
         for (int off = 4; off < 32; off <<= 1)
           l[nt][u] += __shfl_xor_sync(0xffffffffu, l[nt][u], off);
-        if (fr == 0)
-          ml[(warp * GH + nt) * 8 + fc + u] = make_float2(m[nt][u], l[nt][u]);
-      }
-    consumers_sync();
-    float M[GH][2], L[GH][2];
-#pragma unroll
-    for (int nt = 0; nt < GH; ++nt)
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        float2 x[kDcWarps];
-        M[nt][u] = -INFINITY;
-        L[nt][u] = 0.0f;
-#pragma unroll
-        for (int w = 0; w < kDcWarps; ++w) {
-          x[w] = ml[(w * GH + nt) * 8 + fc + u];
-          M[nt][u] = fmaxf(M[nt][u], x[w].x);
-        }
-#pragma unroll
-        for (int w = 0; w < kDcWarps; ++w)
-          if (x[w].x != -INFINITY)
-            L[nt][u] = fmaf(ex2(x[w].x - M[nt][u]), x[w].y, L[nt][u]);
-        const float f = m[nt][u] == -INFINITY ? 0.0f : ex2(m[nt][u] - M[nt][u]);
-#pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
-          o[nt][i][u] *= f;
-          o[nt][i][2 + u] *= f;
-        }
-      }
     // where element u of o[nt][i] lies in a [8 GH][kPad] block
     auto at = [&](int nt, int i, int u) {
       return (8 * nt + fc + (u & 1)) * C::kPad + 16 * i + fr + 8 * (u >> 1);
     };
     if (warp > 0) {
+      if (joins > 0) wait_for(taken, joins - 1);  // the part's before
       float *to = dump + (warp - 1) * 8 * GH * C::kPad;
 #pragma unroll
-      for (int nt = 0; nt < GH; ++nt)
+      for (int nt = 0; nt < GH; ++nt) {
 #pragma unroll
         for (int i = 0; i < D / 16; ++i)
 #pragma unroll
           for (int u = 0; u < 4; ++u) to[at(nt, i, u)] = o[nt][i][u];
-    }
-    consumers_sync();
-    if (warp == 0) {
+        if (fr == 0)
 #pragma unroll
-      for (int k = 0; k < kDcWarps - 1; ++k) {
-        const float *from = dump + k * 8 * GH * C::kPad;
-#pragma unroll
-        for (int nt = 0; nt < GH; ++nt)
-#pragma unroll
-          for (int i = 0; i < D / 16; ++i)
-#pragma unroll
-            for (int u = 0; u < 4; ++u) o[nt][i][u] += from[at(nt, i, u)];
+          for (int u = 0; u < 2; ++u)
+            ml[(warp * GH + nt) * 8 + fc + u] = make_float2(m[nt][u], l[nt][u]);
       }
-    }
-    // (Warp 0 is done with the sums, and every warp with the (m, l), before it
-    // joins again: nothing else keeps the next part's from theirs.)
-
-    // ---- out, or to the workspace ----
-    const int unit0 = unit_of(dl, it.first);
-    const int parts = unit_of(dl, it.first + it.n - 1) - unit0 + 1;
-    const int64_t row = int64_t(it.b) * a.out_ld + int64_t(it.g) * G * D;
-    const int stride = part_floats(G, D);
-    if (warp == 0) {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(joined);
+    } else {
+      wait_for(joined, joins);
       // slot 2 unit + 1 for a part that begins its item, else 2 unit: a unit
       // has at most one of each
-      float *p = a.part + int64_t(2 * it.unit + (it.index == 0 ? 1 : 0)) * stride;
-      if (it.index == 0 && lane == 0)
-        a.parts[int64_t(it.b) * a.v.hkv + it.g] = DcParts{unit0, parts};
+      const bool whole = it.parts == 1;
+      float *p = a.part + int64_t(2 * it.unit + it.starts) * part_floats(G, D);
+      if (it.starts && lane == 0)
+        a.parts[int64_t(it.b) * a.v.hkv + it.g] = DcParts{it.unit0, it.parts};
 #pragma unroll
       for (int nt = 0; nt < GH; ++nt)
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          const int h = 8 * nt + fc + u;
-          if (h >= G) continue;
-          if (parts == 1) {
-            const float inv = 1.0f / L[nt][u];
+          float2 x[kDcWarps] = {make_float2(m[nt][u], l[nt][u])};
+          float M = m[nt][u];
 #pragma unroll
-            for (int i = 0; i < 2 * (D / 16); ++i) {
-              const int64_t e = row + h * D + 8 * i + fr;
-              const float y = o[nt][i >> 1][2 * (i & 1) + u] * inv;
-              if (BF16)
-                static_cast<__nv_bfloat16 *>(a.out)[e] = __float2bfloat16_rn(y);
-              else
-                static_cast<float *>(a.out)[e] = y;
-            }
-          } else {
+          for (int w = 1; w < kDcWarps; ++w) {
+            x[w] = ml[(w * GH + nt) * 8 + fc + u];
+            M = fmaxf(M, x[w].x);
+          }
+          float f[kDcWarps], L = 0.0f;
 #pragma unroll
-            for (int i = 0; i < 2 * (D / 16); ++i)
-              p[h * D + 8 * i + fr] = o[nt][i >> 1][2 * (i & 1) + u];
-            if (fr == 0)
-              *reinterpret_cast<float2 *>(p + G * D + 2 * h) =
-                  make_float2(M[nt][u], L[nt][u]);
+          for (int w = 0; w < kDcWarps; ++w) {
+            f[w] = x[w].x == -INFINITY ? 0.0f : ex2(x[w].x - M);
+            L = fmaf(f[w], x[w].y, L);
+          }
+          if (whole) {
+            const float inv = 1.0f / L;
+#pragma unroll
+            for (int w = 0; w < kDcWarps; ++w) f[w] *= inv;
+          } else if (fr == 0 && 8 * nt + fc + u < G) {
+            *reinterpret_cast<float2 *>(p + G * D + 2 * (8 * nt + fc + u)) =
+                make_float2(M, L);
+          }
+          // (a lane reads and writes its own places of the first block)
+#pragma unroll
+          for (int i = 0; i < 2 * (D / 16); ++i) {
+            const int e = at(nt, i >> 1, 2 * (i & 1) + u);
+            float y = f[0] * o[nt][i >> 1][2 * (i & 1) + u];
+#pragma unroll
+            for (int w = 1; w < kDcWarps; ++w)
+              y = fmaf(f[w], dump[(w - 1) * 8 * GH * C::kPad + e], y);
+            dump[e] = y;
           }
         }
+      __syncwarp();
+      const int64_t row = int64_t(it.b) * a.out_ld + int64_t(it.g) * G * D;
+      for (int e = lane; e < G * (D / 4); e += 32) {
+        const int h = e / (D / 4), v = e % (D / 4);
+        const float4 y = *reinterpret_cast<const float4 *>(dump + h * C::kPad + 4 * v);
+        if (!whole) {
+          *reinterpret_cast<float4 *>(p + 4 * e) = y;
+        } else if (BF16) {
+          const __nv_bfloat162 y0 = __floats2bfloat162_rn(y.x, y.y);
+          const __nv_bfloat162 y1 = __floats2bfloat162_rn(y.z, y.w);
+          uint2 w;
+          w.x = *reinterpret_cast<const uint32_t *>(&y0);
+          w.y = *reinterpret_cast<const uint32_t *>(&y1);
+          *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.out) + row + 4 * e) = w;
+        } else {
+          *reinterpret_cast<float4 *>(static_cast<float *>(a.out) + row + 4 * e) = y;
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(taken);
     }
+    ++joins;
   }
 }
 
@@ -679,12 +708,14 @@ decode_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap kmap,
 // thread (lane, vector v) sums parts lane, lane + lanes, ... of four outputs.
 // 8 loads are in flight in both, the first before the maximum is known.
 constexpr int kDcFewParts = 16;
-template <int D, bool BF16>
-__global__ void __launch_bounds__(kDcJoinThreads)
-decode_join_kernel(const DecodeArgs a, int heads) {
-  __shared__ float s_max[kDcJoinThreads / 32];
-  __shared__ float4 s_acc[kDcJoinThreads];
-  __shared__ float s_sum[kDcJoinThreads / (D / 4)];
+template <int D, bool BF16, int kThreads, int kHeads>
+__global__ void __launch_bounds__(kThreads)
+decode_join_kernel(const DecodeArgs a) {
+  static_assert(kHeads <= kThreads / 32, "a warp per head");
+  __shared__ float s_max[kThreads / 32];
+  __shared__ float4 s_acc[kThreads];
+  __shared__ float s_sum[kThreads / (D / 4)];
+  __shared__ DcParts s_parts[kHeads];
   pdl_wait();
   pdl_trigger();
   if (blockIdx.x == 0 && threadIdx.x == 0) *a.claim = 0u;  // for the next call
@@ -694,9 +725,9 @@ decode_join_kernel(const DecodeArgs a, int heads) {
   // One head by `threads` threads (this one is `tid`): a warp or the block.
   auto join = [&](int head, const DcParts &ps, int tid, auto whole) {
     constexpr bool kBlock = decltype(whole)::value;
-    constexpr int kThreads = kBlock ? kDcJoinThreads : 32;
+    constexpr int kMine = kBlock ? kThreads : 32;
     constexpr int kVec = D / 4;
-    constexpr int kLanes = kThreads / kVec;  // 1 or 2 of a warp
+    constexpr int kLanes = kMine / kVec;  // 1 or 2 of a warp
     const int v = tid % kVec, lane = tid / kVec;
     const int item = head / a.G, h = head - item * a.G;
     const float *base = a.part + int64_t(2 * ps.unit0) * stride;
@@ -721,7 +752,7 @@ decode_join_kernel(const DecodeArgs a, int heads) {
     };
     load(lane);
     float mx = -INFINITY;
-    for (int i = tid; i < ps.parts; i += kThreads) mx = fmaxf(mx, ml(i).x);
+    for (int i = tid; i < ps.parts; i += kMine) mx = fmaxf(mx, ml(i).x);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1)
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
@@ -729,7 +760,7 @@ decode_join_kernel(const DecodeArgs a, int heads) {
       if ((tid & 31) == 0) s_max[tid >> 5] = mx;
       __syncthreads();
 #pragma unroll
-      for (int w = 0; w < kDcJoinThreads / 32; ++w) mx = fmaxf(mx, s_max[w]);
+      for (int w = 0; w < kThreads / 32; ++w) mx = fmaxf(mx, s_max[w]);
     }
     float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     float sum = 0.0f;
@@ -793,17 +824,21 @@ decode_join_kernel(const DecodeArgs a, int heads) {
     return ps;
   };
   const int first = blockIdx.x, step = gridDim.x;
-  const int warp = threadIdx.x >> 5, few = heads > 1 ? kDcFewParts : 1;
-  if (warp < heads && first + warp * step < n) {
+  const int warp = threadIdx.x >> 5;
+  constexpr int kFew = kHeads > 1 ? kDcFewParts : 1;
+  if (warp < kHeads) {
     const int head = first + warp * step;
-    const DcParts ps = parts_of(head);
-    if (ps.parts > 1 && ps.parts <= few)
+    DcParts ps{0, 0};
+    if (head < n) ps = parts_of(head);
+    if ((threadIdx.x & 31) == 0) s_parts[warp] = ps;
+    if (ps.parts > 1 && ps.parts <= kFew)
       join(head, ps, threadIdx.x & 31, std::false_type{});
   }
-  for (int k = 0; k < heads && first + k * step < n; ++k) {
-    const int head = first + k * step;
-    const DcParts ps = parts_of(head);
-    if (ps.parts > few) join(head, ps, threadIdx.x, std::true_type{});
+  __syncthreads();
+#pragma unroll 1
+  for (int k = 0; k < kHeads; ++k) {
+    const DcParts ps = s_parts[k];
+    if (ps.parts > kFew) join(first + k * step, ps, threadIdx.x, std::true_type{});
   }
 }
 
@@ -841,14 +876,18 @@ cudaError_t launch_t(const DecodeArgs &a, const CUtensorMap &kmap,
   cfg.numAttrs = 1;
   e = cudaLaunchKernelEx(&cfg, decode_kernel<D, GH, BF16>, a, kmap, vmap);
   if (e != cudaSuccess) return e;
-  // A block for each head while the blocks fit on the device at once (few
-  // heads, so likely many parts each), else one for 8 heads.
+  // Few heads (so likely many parts each): a large block for each; else a
+  // small block for 8.
   const unsigned n = unsigned(a.v.n_seqs) * unsigned(a.H);
-  const int heads = n <= 2u * unsigned(device_sm_count()) ? 1 : 8;
-  cfg.gridDim = dim3((n + heads - 1) / heads);
-  cfg.blockDim = dim3(kDcJoinThreads);
   cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, decode_join_kernel<D, BF16>, a, heads);
+  if (n <= unsigned(device_sm_count())) {
+    cfg.gridDim = dim3(n);
+    cfg.blockDim = dim3(512);
+    return cudaLaunchKernelEx(&cfg, decode_join_kernel<D, BF16, 512, 1>, a);
+  }
+  cfg.gridDim = dim3((n + 7) / 8);
+  cfg.blockDim = dim3(256);
+  return cudaLaunchKernelEx(&cfg, decode_join_kernel<D, BF16, 256, 8>, a);
 }
 
 template <int D>
