@@ -43,8 +43,17 @@ namespace {
 constexpr int kDcWarps = 4;                      // consumers
 constexpr int kDcThreads = (kDcWarps + 1) * 32;  // and the producer
 constexpr int kDcTile = 64;
-constexpr int kDcMaxCtas = 320;
-constexpr int kDcMaxUnits = 5 * kDcMaxCtas;      // shares and claimed units
+constexpr int kDcMaxSms = 160;
+// CTAs an SM: a tile takes a CTA's warps about 0.9 us from end to end, so it
+// takes several CTAs to keep up with the copies (the smaller the rows, the
+// more); what their stages and sums leave room for.
+__host__ __device__ constexpr int dc_ctas(int D, int GH) {
+  return GH == 1 && D == 64 ? 3 : 2;
+}
+// Shares and claimed units, at most.
+__host__ __device__ constexpr int dc_max_units(int D, int G) {
+  return 5 * dc_ctas(D, G > 8 ? 2 : 1) * kDcMaxSms;
+}
 
 // What the workspace keeps of a (sequence, head): its parts are those of units
 // unit0 .. unit0 + parts - 1 (parts 1: the output is written already, 0: zeros
@@ -59,7 +68,7 @@ struct DecodeArgs {
   int64_t q_ld;
   void *out;
   int64_t out_ld;
-  float *part;          // [2 kDcMaxUnits][part_floats(G, D)]
+  float *part;          // [2 dc_max_units][part_floats(G, D)]
   DcParts *parts;       // [n_seqs][Hkv]
   unsigned int *claim;  // units claimed so far; zero between calls
   int H, G;
@@ -85,19 +94,24 @@ struct DcCfg {
   static constexpr uint32_t kHalf = kDcTile * 128;        // 64 dims
   static constexpr uint32_t kKBytes = kHalf * (D / 64);
   static constexpr uint32_t kStage = 2 * kKBytes;
-  // about 100 KB of stages a CTA and two CTAs an SM; with 16 heads' partial
-  // sums one CTA of twice the stages
-  static constexpr int kStages = (D == 128 ? 3 : 6) * GH;
-  static constexpr int kCtas = GH == 1 ? 2 : 1;
+  static constexpr int kCtas = dc_ctas(D, GH);
+  // 128 to 192 KB of stages an SM
+  static constexpr int kStages = GH == 1 ? (D == 128 ? 3 : 4) : (D == 128 ? 2 : 4);
   static constexpr int kPad = D + 4;                       // floats a row
   // the warps' sums [3][8 GH][kPad] and (m, l)
   static constexpr uint32_t kDump = kStages * kStage;
   static constexpr uint32_t kMl = kDump + 3u * 8 * GH * kPad * 4;
   static constexpr uint32_t kInfo = kMl + kDcWarps * 8 * GH * 8;
-  static constexpr uint32_t kBefore = kInfo + kStages * sizeof(DcTileInfo);
+  static constexpr uint32_t kQ = kInfo + kStages * sizeof(DcTileInfo);
+  static constexpr uint32_t kQBytes = 8 * GH * D * 2;
+  static constexpr uint32_t kBars = kQ + kQBytes;
+  static constexpr uint32_t kTotal = kBars + (2 * kStages + 3) * 8;
+  // at the start, where the sums come later
+  static constexpr uint32_t kBefore = kDump;
   static constexpr uint32_t kLen0 = kBefore + kDcThreads * 8;
-  static constexpr uint32_t kBars = kLen0 + kDcThreads * 4;
-  static constexpr uint32_t kTotal = kBars + (2 * kStages + 2) * 8;
+  static constexpr uint32_t kWarpSum = kLen0 + kDcThreads * 4;
+  static_assert(kWarpSum + kDcThreads / 32 * 8 <= kMl, "scratch");
+  static_assert(kInfo % 16 == 0, "16-byte aligned info and queries");
   static constexpr uint32_t kSmem = kTotal + 1024;
 };
 
@@ -161,7 +175,7 @@ __device__ __forceinline__ Dealing deal(int64_t total, int min_tiles, int grid) 
   Dealing d{total, total, total, 0, 0, 1, 1};
   const int64_t n = (total + min_tiles - 1) / min_tiles;
   d.n_ctas = n < grid ? int(n) : grid;
-  if (total >= 16 * int64_t(d.n_ctas)) {
+  if (total >= 64 * int64_t(d.n_ctas)) {
     // 20 % in at most 1.5 units a CTA, 10 % in at most 2: the shorter the
     // unit, the less the last one keeps the call waiting, and the more parts
     // there are to join.
@@ -204,20 +218,32 @@ struct Item {
 
 // Both return false past the last sequence, which only lengths that change
 // under the call can bring about.
-// The item of tile `at`; before[t]: the first tile of sequences t per and on,
-// len0[t]: the first one's length.
-__device__ __forceinline__ bool item_at(const DecodeArgs &a,
-                                        const long long *before,
-                                        const int *len0, int per, int64_t at,
-                                        Item &it) {
+// Where the sequences begin, for one warp: entry t = 32 k + lane is the first
+// tile of sequences t per and on, and the first one's length.
+struct Begins {
+  static constexpr int kPer = kDcThreads / 32;
+  long long before[kPer];
+  int len0[kPer];
+  int per;
+};
+// The item of tile `at` (by a whole warp).
+__device__ __forceinline__ bool item_at(const DecodeArgs &a, const Begins &bg,
+                                        int64_t at, Item &it) {
   int n = 0;
-  for (int t = threadIdx.x & 31; t < kDcThreads; t += 32) n += before[t] <= at;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
-  int64_t base = before[n - 1];
-  const int b0 = (n - 1) * per;
+  for (int k = 0; k < Begins::kPer; ++k)
+    n += __popc(__ballot_sync(0xffffffffu, bg.before[k] <= at));
+  const int b0 = (n - 1) * bg.per;
+  int64_t base = 0;
+  int len = 0;
+#pragma unroll
+  for (int k = 0; k < Begins::kPer; ++k)
+    if ((n - 1) / 32 == k) {
+      base = __shfl_sync(0xffffffffu, bg.before[k], (n - 1) & 31);
+      len = __shfl_sync(0xffffffffu, bg.len0[k], (n - 1) & 31);
+    }
   for (it.b = b0; it.b < a.v.n_seqs; ++it.b) {
-    it.len = it.b == b0 ? len0[n - 1] : seq_len(a.v, it.b);
+    it.len = it.b == b0 ? len : seq_len(a.v, it.b);
     it.plan = seq_plan(it.len, a.window, a.sinks);
     const int64_t tiles = int64_t(it.plan.n) * a.v.hkv;
     if (at < base + tiles) {
@@ -257,10 +283,11 @@ decode_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap kmap,
   uint64_t *empty = full + C::kStages;
   uint64_t *joined = empty + C::kStages;  // three warps' sums are there
   uint64_t *taken = joined + 1;           // and have been added up
+  uint64_t *q_read = taken + 1;           // a part's queries are in registers
   DcTileInfo *info = reinterpret_cast<DcTileInfo *>(smem + C::kInfo);
   long long *s_before = reinterpret_cast<long long *>(smem + C::kBefore);
   int *s_len0 = reinterpret_cast<int *>(smem + C::kLen0);
-  __shared__ long long s_sum[kDcThreads / 32];
+  long long *s_sum = reinterpret_cast<long long *>(smem + C::kWarpSum);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
     prefetch_map(&kmap);
@@ -271,6 +298,7 @@ decode_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap kmap,
     }
     mbar_init(joined, kDcWarps - 1);
     mbar_init(taken, 1);
+    mbar_init(q_read, kDcWarps);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   pdl_wait();
@@ -324,9 +352,9 @@ decode_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap kmap,
   if (warp == kDcWarps) {
     // ---- producer ----
     // Lane i copies box i of a tile (at most 16: 4 page parts, 2 halves, keys
-    // and values).  A tile's pages are looked up while the one before it
-    // waits for its stage: the lookup takes as long as a fifth of a stage's
-    // copy.
+    // and values).  32 entries of the page table are loaded at a time, and
+    // the next unit is claimed and found while this one's last tiles are
+    // copied: each lookup takes as long as a tile.
     const int per_kv = (kDcTile / a.box_rows) * (D / 64);
     const bool is_v = lane >= per_kv;
     const int j = is_v ? lane - per_kv : lane;
@@ -336,67 +364,125 @@ decode_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap kmap,
     // Keys and values are read once: they should not push the parts out of L2.
     uint64_t once;
     asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(once));
-    Item it;
-    int stage = 0, unit = int(blockIdx.x);
+    int stage = 0;
     uint32_t round = 0;
-    bool ok = true;
     auto stage_free = [&] {
       return round == 0 || warp_wait(&empty[stage], (round - 1) & 1u);
     };
-    while (ok) {
+    Begins bg;
+#pragma unroll
+    for (int k = 0; k < Begins::kPer; ++k) {
+      bg.before[k] = s_before[32 * k + lane];
+      bg.len0[k] = s_len0[32 * k + lane];
+    }
+    bg.per = per;
+    // Tiles [t, end) of a unit, the item of tile t, and entries pg0 .. pg0 + 31
+    // (one a lane) of sequence pg_b's row of the page table.
+    struct Work {
+      int unit;
       int64_t t, end;
-      unit_range(dl, unit, &t, &end);
-      // the next unit is claimed shortly before this one is copied
-      unsigned int claimed = 0;
+      Item it;
+      int pg, pg0, pg_b;
+    };
+    auto load_pages = [&](Work &w, int first) {
+      w.pg0 = first;
+      w.pg_b = w.it.b;
+      w.pg = first + lane < a.v.max_pages
+                 ? __ldcg(a.v.table + int64_t(w.it.b) * a.v.max_pages + first + lane)
+                 : -1;
+    };
+    // 1: found; 0: no such unit; -1: lengths that changed under the call
+    auto find = [&](Work &w, int unit) {
+      w.unit = unit;
+      unit_range(dl, unit, &w.t, &w.end);
+      if (w.t >= dl.total) return 0;
+      if (!item_at(a, bg, w.t, w.it)) return -1;
+      load_pages(w, tile_pos(w.it.plan, int(w.t - w.it.first), kDcTile) >>
+                        a.v.page_shift);
+      return 1;
+    };
+    Work w, next;
+    int found = find(w, int(blockIdx.x));
+    int part = 0;  // parts so far; their queries share one place
+    bool ok = true;
+    while (ok && found > 0) {
       const bool dynamic = dl.dealt < dl.total;
-      const int64_t claim_at = end - t > 2 ? end - 2 : t;
-      ok = item_at(a, s_before, s_len0, per, t, it);
+      const int64_t claim_at = w.end - w.t > 3 ? w.end - 3 : w.t;
+      unsigned int claimed = 0;
+      bool looked = false;
+      auto find_next = [&] {
+        looked = true;
+        // (at most 3.5 units and one claim too many a CTA)
+        found = find(next, dl.n_ctas + int(__shfl_sync(0xffffffffu, claimed, 0)));
+      };
       int unit0 = 0, parts = 0;  // of the item
       auto count_parts = [&] {
-        unit0 = unit_of(dl, it.first);
-        parts = unit_of(dl, it.first + it.plan.n - 1) - unit0 + 1;
+        unit0 = unit_of(dl, w.it.first);
+        parts = unit_of(dl, w.it.first + w.it.plan.n - 1) - unit0 + 1;
       };
-      if (ok) count_parts();
-      int pos = 0, page = 0;
-      auto look_up = [&] {
-        pos = tile_pos(it.plan, int(t - it.first), kDcTile);
-        page = mine_box ? box_page(a.v, it.b, pos + r0, a.box_rows, it.plan.s1,
-                                   it.plan.lo, it.len)
-                        : 0;
-      };
-      if (ok) look_up();
-      while (ok) {
-        if (dynamic && t == claim_at && lane == 0) claimed = atomicAdd(a.claim, 1u);
-        ok = stage_free();
+      count_parts();
+      bool new_part = true;
+      for (;;) {
+        if (dynamic && w.t == claim_at && lane == 0) claimed = atomicAdd(a.claim, 1u);
+        const int pos = tile_pos(w.it.plan, int(w.t - w.it.first), kDcTile);
+        const int p0 = pos >> a.v.page_shift;
+        if (w.pg_b != w.it.b || p0 < w.pg0 ||
+            ((pos + kDcTile - 1) >> a.v.page_shift) >= w.pg0 + 32)
+          load_pages(w, p0);
+        // A box that nobody sees and a bad page read as zeros (a page past the
+        // pool); only an entry that is used is looked at.
+        int page = __shfl_sync(0xffffffffu, w.pg,
+                               ((pos + r0) >> a.v.page_shift) - w.pg0);
+        const bool used = pos + r0 < w.it.plan.s1 ||
+                          (pos + r0 < w.it.len && pos + r0 + a.box_rows > w.it.plan.lo);
+        if (page < 0 || page >= a.v.n_pages || !used) {
+          if (used && mine_box) atomicOr(a.v.err, kPagedErr);
+          page = a.v.n_pages;
+        }
+        ok = stage_free() &&
+             (!new_part || part == 0 || warp_wait(q_read, uint32_t(part - 1) & 1u));
         if (!ok) break;
         if (lane == 0) {
-          info[stage] = DcTileInfo{unit, it.b, it.g, it.len, pos, t == it.first,
-                                   it.plan.s1, it.plan.lo, unit0, parts, {}};
-          mbar_arrive_expect_tx(&full[stage], C::kStage);
+          info[stage] = DcTileInfo{w.unit, w.it.b, w.it.g, w.it.len, pos,
+                                   w.t == w.it.first, w.it.plan.s1, w.it.plan.lo,
+                                   unit0, parts, {}};
+          const uint32_t q_bytes = new_part ? uint32_t(a.G) * D * 2 : 0u;
+          mbar_arrive_expect_tx(&full[stage], C::kStage + q_bytes);
+          // The queries come with the part's first tile, once for the CTA: read
+          // by every warp of every CTA, the one row of a long sequence was a
+          // hot spot that doubled the call's time.
+          if (new_part)
+            bulk_copy_g2s(smem + C::kQ,
+                          a.q + int64_t(w.it.b) * a.q_ld + int64_t(w.it.g) * a.G * D,
+                          q_bytes, &full[stage]);
         }
+        part += new_part;
+        new_part = false;
         __syncwarp();
         if (mine_box)
           tma_load_4d_once(smem + stage * C::kStage + dst, is_v ? &vmap : &kmap,
                            half * 64, (pos + r0) & ((1 << a.v.page_shift) - 1),
-                           it.g, page, &full[stage], once);
+                           w.it.g, page, &full[stage], once);
         if (++stage == C::kStages) {
           stage = 0;
           ++round;
         }
-        if (++t == end) break;
-        if (t >= it.first + it.plan.n) {
-          ok = item_next(a, it);
-          if (ok) count_parts();
+        if (dynamic && w.t == claim_at + 1) find_next();
+        if (++w.t == w.end) break;
+        if (w.t >= w.it.first + w.it.plan.n) {
+          if (!item_next(a, w.it)) {
+            ok = false;
+            break;
+          }
+          count_parts();
+          new_part = true;
         }
-        if (ok) look_up();
       }
       if (!ok || !dynamic) break;
-      claimed = __shfl_sync(0xffffffffu, claimed, 0);
-      // (at most 3.5 units and one claim too many a CTA)
-      unit = dl.n_ctas + int(claimed);
-      unit_range(dl, unit, &t, &end);
-      if (t >= dl.total) break;
+      if (!looked) find_next();
+      w = next;
     }
+    if (found < 0) ok = false;
     // no more tiles (also after a wait that ran out)
     if (ok) ok = stage_free();
     if (ok && lane == 0) {
@@ -442,11 +528,12 @@ decode_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap kmap,
       t = info[stage];
     }
   };
-  // The queries of a head group as B fragments (columns past G: zero); the
-  // first part's are loaded while its first tile is copied.
-  uint32_t qf[GH][D / 16][2];
-  auto load_q = [&](int b, int g) {
-    const __nv_bfloat16 *q0 = a.q + int64_t(b) * a.q_ld + int64_t(g) * G * D;
+  DcTileInfo t;
+  next_tile(t);
+  while (t.unit >= 0) {
+    const DcTileInfo it = t;  // the part's first tile
+    // the queries of this head group as B fragments (columns past G: zero)
+    uint32_t qf[GH][D / 16][2];
 #pragma unroll
     for (int nt = 0; nt < GH; ++nt)
 #pragma unroll
@@ -455,26 +542,13 @@ decode_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap kmap,
         for (int u = 0; u < 2; ++u)
           qf[nt][kk][u] =
               8 * nt + fr < G
-                  ? __ldcg(reinterpret_cast<const unsigned int *>(
-                        q0 + (8 * nt + fr) * D + 16 * kk + fc + 8 * u))
+                  ? *reinterpret_cast<const uint32_t *>(
+                        smem + C::kQ +
+                        ((8 * nt + fr) * D + 16 * kk + fc + 8 * u) * 2)
                   : 0u;
-  };
-  bool first_part = false;
-  {
-    int64_t lo, hi;
-    Item it;
-    unit_range(dl, int(blockIdx.x), &lo, &hi);
-    if (item_at(a, s_before, s_len0, per, lo, it)) {
-      load_q(it.b, it.g);
-      first_part = true;
-    }
-  }
-  DcTileInfo t;
-  next_tile(t);
-  while (t.unit >= 0) {
-    const DcTileInfo it = t;  // the part's first tile
-    if (!first_part) load_q(it.b, it.g);
-    first_part = false;
+    fence_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(q_read);
     // Output^T: rows dims 16 i + fr (+ 8), columns heads 8 nt + fc (+ 1);
     // maximum and sum of those two heads.
     float o[GH][D / 16][4] = {};
@@ -819,7 +893,8 @@ decode_join_kernel(const DecodeArgs a) {
   // is not followed)
   auto parts_of = [&](int head) {
     DcParts ps = a.parts[head / a.G];
-    if (ps.unit0 < 0 || ps.parts > kDcMaxUnits || ps.unit0 > kDcMaxUnits - ps.parts)
+    const int most = dc_max_units(D, a.G);
+    if (ps.unit0 < 0 || ps.parts > most || ps.unit0 > most - ps.parts)
       ps.parts = 0;
     return ps;
   };
@@ -845,7 +920,8 @@ decode_join_kernel(const DecodeArgs a) {
 size_t align256(size_t b) { return (b + 255) / 256 * 256; }
 
 size_t part_bytes(int G, int D) {
-  return align256(size_t(2) * kDcMaxUnits * part_floats(G, D) * sizeof(float));
+  return align256(size_t(2) * dc_max_units(D, G) * part_floats(G, D) *
+                  sizeof(float));
 }
 
 template <int D, int GH, bool BF16>
@@ -859,7 +935,8 @@ cudaError_t launch_t(const DecodeArgs &a, const CUtensorMap &kmap,
   if (e != cudaSuccess) return e;
   // Shares of at least min_tiles tiles: more CTAs than that have nothing to
   // do, however long the sequences may be.
-  int64_t ctas = resident < kDcMaxCtas ? resident : kDcMaxCtas;
+  constexpr int kMost = dc_ctas(D, GH) * kDcMaxSms;
+  int64_t ctas = resident < kMost ? resident : kMost;
   const int64_t most = int64_t(a.v.n_seqs) * a.v.hkv *
                        ((int64_t(a.v.max_pages) << a.v.page_shift) / kDcTile + 1);
   const int64_t useful = (most + a.min_tiles - 1) / a.min_tiles;
