@@ -16,11 +16,19 @@
 // turns.  Sine and cosine are the fast ones (absolute error about 2^-21 on
 // [-pi, pi]), far below the output's half step of 2^-9.
 //
-// Bound by the bytes of the rows: 2 bytes in and 2 out per value.  A CTA
-// takes one token; D / 8 lanes take a head, 8 values (one 16-byte load) a
-// lane, so a pair never leaves its lane and the norm is a shuffle sum over
-// the head's lanes.  A lane's loads of all its heads go out before the
-// position is known.
+// Bound by the bytes of the rows, 2 in and 2 out per value, once the
+// instructions per value are few: D / 8 lanes take a head, 8 values (one
+// 16-byte load) a lane, so a pair never leaves its lane and the norm is a
+// shuffle sum over the head's lanes; gains and rotation are multiplied once
+// per token.  One warp takes a token where there are tokens enough (the
+// rotation is made once per token and warp); 2 or 4 share it in shorter calls,
+// where latency counts.  The row is fetched into L2 as a whole at once (the
+// loads in flight alone are too few to cover the memory's latency), and the
+// first loads go out before the token's position is known.
+// 16381 tokens of 20 + 2 x 5 heads of 128: 49.0 us, 5.1 TB/s of its 252 MB;
+// without the fetch of whole rows 61.5 us; CTAs of 256 threads at 3 an SM
+// 50.9 us (a CTA leaves when its slowest warp does), persistent CTAs that
+// walk the tokens 66 us (each warp waits out its next token's loads).
 #include <cmath>
 
 #include "bw_paged.cuh"
@@ -28,7 +36,7 @@
 namespace bw {
 namespace {
 
-constexpr int kApThreads = 256;
+constexpr int kApThreads = 128;
 constexpr int kApWarps = kApThreads / 32;
 constexpr int kApMaxPairs = 64;
 
@@ -40,6 +48,7 @@ struct AppendArgs {
   __nv_bfloat16 *q_out;
   int64_t q_ld;
   int n_tokens, H;
+  int group;  // warps that share a token: 1, 2 or 4
   float eps;
   uint64_t turn[kApMaxPairs];  // F_i, fractions of 2^64
 };
@@ -49,76 +58,158 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
   return *reinterpret_cast<const uint32_t *>(&t);
 }
 
+// Gains times rotation of this lane's four pairs, for one kind of head:
+// (z0, z1) = (y0 a0 - y1 b1, y0 b0 + y1 a1), a = gamma c, b = gamma s.
+struct Turn {
+  float a0[4], a1[4], b0[4], b1[4];
+};
+__device__ __forceinline__ void make_turn(Turn &t, const float *gamma, int d0,
+                                          const float (&c)[4],
+                                          const float (&s)[4]) {
+  float g[8];
+  if (gamma) {
+    const float4 x = *reinterpret_cast<const float4 *>(gamma + d0);
+    const float4 y = *reinterpret_cast<const float4 *>(gamma + d0 + 4);
+    g[0] = x.x; g[1] = x.y; g[2] = x.z; g[3] = x.w;
+    g[4] = y.x; g[5] = y.y; g[6] = y.z; g[7] = y.w;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) g[i] = 1.0f;
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    t.a0[i] = g[2 * i] * c[i];
+    t.b0[i] = g[2 * i] * s[i];
+    t.a1[i] = g[2 * i + 1] * c[i];
+    t.b1[i] = g[2 * i + 1] * s[i];
+  }
+}
+
+// This lane's share of `count` heads of D at `in`: heads first, first + step,
+// ...; kAhead of them loaded at once.
+template <int D, int kAhead>
+__device__ __forceinline__ void load_heads(uint4 (&x)[kAhead],
+                                           const __nv_bfloat16 *in, int count,
+                                           int first, int step) {
+#pragma unroll
+  for (int u = 0; u < kAhead; ++u)
+    if (first + u * step < count)
+      x[u] = *reinterpret_cast<const uint4 *>(in + (first + u * step) * D);
+}
+
+// Norm (if any) and rotation of those heads, to `out`, heads out_step apart.
+// x: the first ones, loaded.
+template <int D, int kAhead>
+__device__ __forceinline__ void turn_heads(uint4 (&x)[kAhead],
+                                           const __nv_bfloat16 *in, int count,
+                                           __nv_bfloat16 *out, int64_t out_step,
+                                           const Turn &t, bool norm, float eps,
+                                           int first, int step) {
+  constexpr int kLanes = D / 8;
+  // the loop runs as long as the warp's first lanes have a head, so that the
+  // shuffles are the whole warp's
+  const int sub = (threadIdx.x & 31) / kLanes;
+  for (int h0 = first; h0 - sub < count; h0 += kAhead * step) {
+    if (h0 != first) load_heads<D, kAhead>(x, in, count, h0, step);
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int h = h0 + u * step;
+      if (h - sub >= count) break;  // warp-uniform
+      const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+      float y[8];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        y[2 * i] = __uint_as_float(w[i] << 16);
+        y[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+      }
+      float r = 1.0f;
+      if (norm) {
+        float ss = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) ss = fmaf(y[i], y[i], ss);
+#pragma unroll
+        for (int o = kLanes / 2; o > 0; o >>= 1)
+          ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        r = rsqrtf(fmaf(ss, 1.0f / D, eps));
+      }
+      uint32_t z[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        z[i] = pack2(r * (y[2 * i] * t.a0[i] - y[2 * i + 1] * t.b1[i]),
+                     r * (y[2 * i] * t.b0[i] + y[2 * i + 1] * t.a1[i]));
+      if (h < count)
+        *reinterpret_cast<uint4 *>(out + h * out_step) =
+            make_uint4(z[0], z[1], z[2], z[3]);
+    }
+  }
+}
+
 template <int D>
-__global__ void __launch_bounds__(kApThreads)
+__global__ void __launch_bounds__(kApThreads, 6)
 append_kernel(const PagedView v, const AppendArgs a) {
-  constexpr int kLanes = D / 8;            // lanes of a head
-  constexpr int kHeads = 32 / kLanes;      // heads of a warp and pass
-  constexpr int kPass = kApWarps * kHeads; // heads of a CTA and pass
-  constexpr int kAhead = 2;                // passes loaded at once
+  constexpr int kLanes = D / 8;        // lanes of a head
+  constexpr int kHeads = 32 / kLanes;  // heads of a warp at a time
   pipe::pdl_wait();
   pipe::pdl_trigger();
-  const int t = blockIdx.x;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int sub = lane / kLanes, hl = lane % kLanes;
-  const int n_heads = a.H + 2 * v.hkv;
-  const __nv_bfloat16 *row = a.qkv + int64_t(t) * a.qkv_ld + hl * 8;
-  const int h0 = warp * kHeads + sub;
-
-  uint4 x[kAhead];
-#pragma unroll
-  for (int u = 0; u < kAhead; ++u) {
-    const int h = h0 + u * kPass;
-    x[u] = h < n_heads ? *reinterpret_cast<const uint4 *>(row + h * D)
-                       : make_uint4(0u, 0u, 0u, 0u);
-  }
-  // The gains of this lane's dims; 1 / 0 flags where there is no norm.
-  float gq[8], gk[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) gq[i] = gk[i] = 1.0f;
-  if (a.q_gamma) {
-    const float4 g0 = *reinterpret_cast<const float4 *>(a.q_gamma + hl * 8);
-    const float4 g1 = *reinterpret_cast<const float4 *>(a.q_gamma + hl * 8 + 4);
-    gq[0] = g0.x; gq[1] = g0.y; gq[2] = g0.z; gq[3] = g0.w;
-    gq[4] = g1.x; gq[5] = g1.y; gq[6] = g1.z; gq[7] = g1.w;
-  }
-  if (a.k_gamma) {
-    const float4 g0 = *reinterpret_cast<const float4 *>(a.k_gamma + hl * 8);
-    const float4 g1 = *reinterpret_cast<const float4 *>(a.k_gamma + hl * 8 + 4);
-    gk[0] = g0.x; gk[1] = g0.y; gk[2] = g0.z; gk[3] = g0.w;
-    gk[4] = g1.x; gk[5] = g1.y; gk[6] = g1.z; gk[7] = g1.w;
-  }
-
-  // ---- the token's sequence, position and page ----
-  int b, pos = -1;
-  if (a.q_start) {
-    b = find_seq(a.q_start, v.n_seqs, t);
-    const int q0 = __ldcg(a.q_start + b), q1 = __ldcg(a.q_start + b + 1);
-    if (t >= q0 && t < q1) {  // else a row of no sequence
-      const int len = seq_len(v, b);
-      if (q0 < 0 || q1 > a.n_tokens || len < q1 - q0)
-        atomicOr(v.err, kPagedErr);
-      else
-        pos = len - q1 + t;
-    }
-  } else {
-    b = t;
-    pos = seq_len(v, b) - 1;
-  }
-  if (a.q_start && t == 0) {
+  const int hl = lane % kLanes;
+  const int in_group = warp % a.group;
+  const int64_t t = (int64_t(blockIdx.x) * kApWarps + warp) / a.group;
+  const int first = in_group * kHeads + lane / kLanes;  // this lane's heads
+  const int step = a.group * kHeads;
+  if (a.q_start && blockIdx.x == 0) {
     // A decreasing or escaping q_start may leave no row that notices it.
     for (int i = threadIdx.x; i < v.n_seqs; i += kApThreads) {
       const int q0 = __ldcg(a.q_start + i), q1 = __ldcg(a.q_start + i + 1);
       if (q0 < 0 || q1 > a.n_tokens || q0 > q1) atomicOr(v.err, kPagedErr);
     }
   }
+  if (t >= a.n_tokens) return;
+  const __nv_bfloat16 *row = a.qkv + t * a.qkv_ld;
+  if (in_group == 0 && lane == 0)
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(row),
+                 "r"(uint32_t(a.H + 2 * v.hkv) * D * 2)
+                 : "memory");
+  const __nv_bfloat16 *q_in = row + hl * 8;
+  const __nv_bfloat16 *k_in = q_in + int64_t(a.H) * D;
+  const __nv_bfloat16 *v_in = k_in + int64_t(v.hkv) * D;
+  uint4 xq[4], xk[2], xv[2];
+  load_heads<D, 2>(xv, v_in, v.hkv, first, step);
+  load_heads<D, 2>(xk, k_in, v.hkv, first, step);
+  load_heads<D, 4>(xq, q_in, a.H, first, step);
+
+  // ---- the token's sequence, position and page ----
+  int b = int(t), pos = -1;
+  if (a.q_start) {
+    b = find_seq(a.q_start, v.n_seqs, int(t));
+    const int q0 = __ldcg(a.q_start + b), q1 = __ldcg(a.q_start + b + 1);
+    if (t >= q0 && t < q1) {  // else a row of no sequence
+      const int len = seq_len(v, b);
+      if (q0 < 0 || q1 > a.n_tokens || len < q1 - q0)
+        atomicOr(v.err, kPagedErr);
+      else
+        pos = len - q1 + int(t);
+    }
+  } else {
+    pos = seq_len(v, b) - 1;
+  }
   if (pos < 0) return;
   const int page = seq_page(v, b, pos);
   const int64_t slot =
       int64_t(page) * v.page_stride +
       (int64_t(pos & ((1 << v.page_shift) - 1)) * D) + hl * 8;
-  const int64_t head_stride = int64_t(D) << v.page_shift;
+  const int64_t head_step = int64_t(D) << v.page_shift;
 
+  // ---- values are copied ----
+  if (page >= 0)
+    for (int h0 = first; h0 < v.hkv; h0 += 2 * step) {
+      if (h0 != first) load_heads<D, 2>(xv, v_in, v.hkv, h0, step);
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+        if (h0 + u * step < v.hkv)
+          *reinterpret_cast<uint4 *>(v.v + slot + (h0 + u * step) * head_step) = xv[u];
+    }
+  // ---- keys and queries are normed and turned ----
   float c[4], s[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -127,57 +218,15 @@ append_kernel(const PagedView v, const AppendArgs a) {
     c[i] = __cosf(ang);  // 2 pi 2^-32 turns above: ang in [-pi, pi)
     s[i] = __sinf(ang);
   }
-
-  for (int hb = h0; hb - sub < n_heads; hb += kAhead * kPass) {
-    if (hb != h0) {
-#pragma unroll
-      for (int u = 0; u < kAhead; ++u) {
-        const int h = hb + u * kPass;
-        x[u] = h < n_heads ? *reinterpret_cast<const uint4 *>(row + h * D)
-                           : make_uint4(0u, 0u, 0u, 0u);
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-      const int h = hb + u * kPass;
-      if (h - sub >= n_heads) break;  // warp-uniform
-      const bool is_q = h < a.H, is_k = !is_q && h < a.H + v.hkv;
-      const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
-      float y[8], ss = 0.0f;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        y[2 * i] = __uint_as_float(w[i] << 16);
-        y[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-        ss = fmaf(y[2 * i], y[2 * i], ss);
-        ss = fmaf(y[2 * i + 1], y[2 * i + 1], ss);
-      }
-#pragma unroll
-      for (int o = kLanes / 2; o > 0; o >>= 1)
-        ss += __shfl_xor_sync(0xffffffffu, ss, o);
-      if (h >= n_heads) continue;
-      if (is_q || is_k) {
-        const bool norm = is_q ? a.q_gamma != nullptr : a.k_gamma != nullptr;
-        const float r = norm ? 1.0f / sqrtf(ss * (1.0f / D) + a.eps) : 1.0f;
-        uint32_t z[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float g0 = is_q ? gq[2 * i] : gk[2 * i];
-          const float g1 = is_q ? gq[2 * i + 1] : gk[2 * i + 1];
-          const float y0 = y[2 * i] * r * g0, y1 = y[2 * i + 1] * r * g1;
-          z[i] = pack2(y0 * c[i] - y1 * s[i], y0 * s[i] + y1 * c[i]);
-        }
-        const uint4 o = make_uint4(z[0], z[1], z[2], z[3]);
-        if (is_q)
-          *reinterpret_cast<uint4 *>(a.q_out + int64_t(t) * a.q_ld + h * D +
-                                     hl * 8) = o;
-        else if (page >= 0)
-          *reinterpret_cast<uint4 *>(v.k + slot + (h - a.H) * head_stride) = o;
-      } else if (page >= 0) {
-        *reinterpret_cast<uint4 *>(v.v + slot +
-                                   (h - a.H - v.hkv) * head_stride) = x[u];
-      }
-    }
+  Turn turn;
+  if (page >= 0) {
+    make_turn(turn, a.k_gamma, hl * 8, c, s);
+    turn_heads<D, 2>(xk, k_in, v.hkv, v.k + slot, head_step, turn,
+                     a.k_gamma != nullptr, a.eps, first, step);
   }
+  make_turn(turn, a.q_gamma, hl * 8, c, s);
+  turn_heads<D, 4>(xq, q_in, a.H, a.q_out + t * a.q_ld + hl * 8, D, turn,
+                   a.q_gamma != nullptr, a.eps, first, step);
 }
 
 }  // namespace
@@ -210,8 +259,14 @@ cudaError_t launch_paged_append(const PagedView &v, const AppendLaunch &l,
     table_dim = l.D;
   }
   for (int i = 0; i < l.D / 2; ++i) a.turn[i] = table[i];
+  // Warps a token (us with 1, 2, 4; 20 + 2 x 5 heads of 128): 1 token 5.4, 3.7,
+  // 3.0; 256 tokens 6.5, 4.7, 4.0; 512 tokens 7.0, 5.3, 5.6; 1500 tokens 9.2,
+  // 8.0, 9.8; 2048 tokens 11.0, 10.7, 12.4; 2900 tokens 12.3, 12.8, 15.7; 8192
+  // tokens 28, 30, 40.
+  a.group = l.n_tokens >= 2048 ? 1 : l.n_tokens >= 512 ? 2 : 4;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(l.n_tokens));
+  cfg.gridDim = dim3(
+      unsigned((int64_t(l.n_tokens) * a.group + kApWarps - 1) / kApWarps));
   cfg.blockDim = dim3(kApThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
