@@ -1043,6 +1043,18 @@ cudaError_t launch_t(const PagedView &v, const PagedAttnLaunch &l,
   cudaError_t e = paged_resident(prefill_kernel<D>, cached, kPfThreads,
                                  PfCfg<D>::kSmem, &resident);
   if (e != cudaSuccess) return e;
+  // setmaxnreg draws on the registers of the launch: a build that gives the
+  // threads fewer than the roles' sum would wait for ever, so it is refused.
+  static std::atomic<int> regs{0};  // a property of the build, not the device
+  if (regs.load(std::memory_order_relaxed) == 0) {
+    cudaFuncAttributes fa{};
+    e = cudaFuncGetAttributes(&fa, prefill_kernel<D>);
+    if (e != cudaSuccess) return e;
+    regs.store(fa.numRegs, std::memory_order_relaxed);
+  }
+  if (regs.load(std::memory_order_relaxed) * kPfThreads <
+      kPfSoftRegs * 256 + kPfOtherRegs * 128)
+    return cudaErrorInvalidConfiguration;
   CUtensorMap qmap, kmap, vmap;
   PFN_cuTensorMapEncodeTiled_v12000 fn = tensor_map_encoder();
   if (!fn) return cudaErrorInvalidValue;
