@@ -525,6 +525,12 @@ def _rows(t, dtypes, dev: int, rows: int, H: int, D: int, name: str):
             "contiguous rows")
 
 
+def _positions(window: int, sinks: int):
+    """Counts that the C call's int cannot hold would wrap."""
+    if max(abs(window), abs(sinks)) > 0x7fffffff:
+        raise ValueError("window and sinks must be below 2^31")
+
+
 def _vector(t, dtype, dev: int, count: int, name: str) -> int:
     """Pointer of a contiguous tensor of at least `count` elements."""
     if not _is(t, dtype, dev) or not t.is_contiguous() or t.numel() < count:
@@ -618,12 +624,14 @@ def bw_attn_paged_decode(q: torch.Tensor, k_pages: torch.Tensor,
     bf16 by the tensor given.  window > 0: the last `window` positions and
     the first `sinks` ones.  scale: 1/sqrt(D) if None.  `workspace`: a uint8
     device tensor of at least bw_attn_paged_decode_workspace_bytes bytes,
-    zeroed before its first use; if omitted, one is made for this call."""
+    zeroed before its first use; paged calls of any kind and shape may share
+    it one after the other; if omitted, one is made for this call."""
     kv, dev, n, hkv, D = _paged_kv(k_pages, v_pages, page_table, kv_len)
     if not isinstance(q, torch.Tensor) or q.dim() != 3:
         _refuse(q, (_BF16,), dev, "q must be [n_seqs][H][D]")
     H = q.shape[1]
     ptr, ld = _rows(q, (_BF16,), dev, n, H, D, "q")
+    _positions(window, sinks)
     context, s = _where(dev, stream)
     with context:
         if out is None:
@@ -667,6 +675,7 @@ def bw_attn_paged_prefill(q: torch.Tensor, k_pages: torch.Tensor,
     n, H = q.shape[0], q.shape[1]
     ptr, ld = _rows(q, (_BF16,), dev, n, H, D, "q")
     starts = _vector(q_start, _I32, dev, n_seqs + 1, "q_start")
+    _positions(window, sinks)
     context, s = _where(dev, stream)
     with context:
         if out is None:

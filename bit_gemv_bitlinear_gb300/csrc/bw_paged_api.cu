@@ -163,6 +163,7 @@ bw_status bw_attn_paged_decode(const bw_bf16 *q, int64_t q_ld, int H,
   if (st != BW_OK) return st;
   st = check_rows(out, out_ld, need);
   if (st != BW_OK) return st;
+  if (out == q) return BW_ERR_INVALID_ARG;
   st = check_attn_args(scale, window, sinks, workspace, workspace_bytes,
                        paged_decode_workspace_bytes(
                            kv->n_seqs, H, kv->n_kv_heads, kv->head_dim));

@@ -35,6 +35,8 @@
 //    shared memory.  A part that is the whole goes straight to the output;
 //    others go to the workspace, and a second kernel, launched along with the
 //    first and waiting for its end, joins them.
+#include <climits>
+
 #include "bw_paged_tc.cuh"
 
 namespace bw {
@@ -75,7 +77,6 @@ struct DecodeArgs {
   float scale2;         // scale log2(e)
   int window, sinks;
   int box_rows;
-  int min_tiles;
 };
 
 // A tile as the producer leaves it next to its stage.
@@ -162,51 +163,6 @@ __device__ __forceinline__ uint32_t take_bf16(float &a, float &b) {
 __device__ __forceinline__ TilePlan seq_plan(int len, int window, int sinks) {
   if (len <= 0) return TilePlan{};
   return tile_plan(len - 1, len - 1, window, sinks, kDcTile);
-}
-
-// How a call's tiles are dealt: [0, dealt) in equal shares to n_ctas CTAs
-// (units 0 .. n_ctas - 1); [dealt, late) in units of unit_a tiles, the rest in
-// units of unit_b, both claimed.  Few tiles are all dealt.
-struct Dealing {
-  int64_t total, dealt, late;
-  int n_ctas, n_a, unit_a, unit_b;
-};
-__device__ __forceinline__ Dealing deal(int64_t total, int min_tiles, int grid) {
-  Dealing d{total, total, total, 0, 0, 1, 1};
-  const int64_t n = (total + min_tiles - 1) / min_tiles;
-  d.n_ctas = n < grid ? int(n) : grid;
-  if (total >= 64 * int64_t(d.n_ctas)) {
-    // 20 % in at most 1.5 units a CTA, 10 % in at most 2: the shorter the
-    // unit, the less the last one keeps the call waiting, and the more parts
-    // there are to join.
-    d.late = total - total / 10;
-    d.dealt = d.late - total / 5;
-    const int64_t ua = (2 * (d.late - d.dealt) + 3 * d.n_ctas - 1) / (3 * d.n_ctas);
-    const int64_t ub = (total - d.late + 2 * d.n_ctas - 1) / (2 * d.n_ctas);
-    d.unit_a = ua < 4 ? 4 : int(ua);
-    d.unit_b = ub < 2 ? 2 : int(ub);
-    d.n_a = int((d.late - d.dealt + d.unit_a - 1) / d.unit_a);
-  }
-  return d;
-}
-__device__ __forceinline__ int unit_of(const Dealing &d, int64_t tile) {
-  if (tile < d.dealt) return int(((tile + 1) * d.n_ctas - 1) / d.dealt);
-  if (tile < d.late) return d.n_ctas + int((tile - d.dealt) / d.unit_a);
-  return d.n_ctas + d.n_a + int((tile - d.late) / d.unit_b);
-}
-// The tiles of a unit (none past the last unit).
-__device__ __forceinline__ void unit_range(const Dealing &d, int unit,
-                                           int64_t *lo, int64_t *hi) {
-  if (unit < d.n_ctas) {
-    *lo = unit * d.dealt / d.n_ctas;
-    *hi = (unit + 1) * d.dealt / d.n_ctas;
-  } else if (unit < d.n_ctas + d.n_a) {
-    *lo = d.dealt + int64_t(unit - d.n_ctas) * d.unit_a;
-    *hi = *lo + d.unit_a < d.late ? *lo + d.unit_a : d.late;
-  } else {
-    *lo = d.late + int64_t(unit - d.n_ctas - d.n_a) * d.unit_b;
-    *hi = *lo + d.unit_b < d.total ? *lo + d.unit_b : d.total;
-  }
 }
 
 // A (sequence, head) and its tiles.
@@ -345,7 +301,7 @@ decode_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap kmap,
     total += s_sum[w];
   }
   s_before[tid] = before;
-  const Dealing dl = deal(total, a.min_tiles, int(gridDim.x));
+  const Dealing dl = deal(total, int(gridDim.x));
   if (int(blockIdx.x) >= dl.n_ctas) return;  // the whole CTA
   __syncthreads();
 
@@ -412,8 +368,10 @@ decode_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap kmap,
       bool looked = false;
       auto find_next = [&] {
         looked = true;
-        // (at most 3.5 units and one claim too many a CTA)
-        found = find(next, dl.n_ctas + int(__shfl_sync(0xffffffffu, claimed, 0)));
+        // (a counter that was not zero at first claims nothing)
+        const unsigned int c = __shfl_sync(0xffffffffu, claimed, 0);
+        found = find(next, c < unsigned(dc_max_units(D, a.G)) ? dl.n_ctas + int(c)
+                                                              : INT_MAX);
       };
       int unit0 = 0, parts = 0;  // of the item
       auto count_parts = [&] {
@@ -933,14 +891,14 @@ cudaError_t launch_t(const DecodeArgs &a, const CUtensorMap &kmap,
       paged_resident(decode_kernel<D, GH, BF16>, cached, kDcThreads,
                      DcCfg<D, GH>::kSmem, &resident);
   if (e != cudaSuccess) return e;
-  // Shares of at least min_tiles tiles: more CTAs than that have nothing to
-  // do, however long the sequences may be.
+  // More CTAs than tiles have nothing to do, however long the sequences may
+  // be.  (Shares of at least 2 or 4 tiles were slower for windowed batches: a
+  // CTA's tiles come one after the other.)
   constexpr int kMost = dc_ctas(D, GH) * kDcMaxSms;
   int64_t ctas = resident < kMost ? resident : kMost;
   const int64_t most = int64_t(a.v.n_seqs) * a.v.hkv *
                        ((int64_t(a.v.max_pages) << a.v.page_shift) / kDcTile + 1);
-  const int64_t useful = (most + a.min_tiles - 1) / a.min_tiles;
-  if (ctas > useful) ctas = useful;
+  if (ctas > most) ctas = most;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(ctas));
   cfg.blockDim = dim3(kDcThreads);
@@ -981,7 +939,7 @@ cudaError_t launch_d(const DecodeArgs &a, const CUtensorMap &kmap,
 
 size_t paged_decode_workspace_bytes(int n_seqs, int H, int Hkv, int D) {
   return part_bytes(H / Hkv, D) +
-         align256(size_t(n_seqs) * Hkv * sizeof(DcParts)) + 256;
+         align256(size_t(n_seqs) * Hkv * sizeof(DcParts)) + kPagedClaimBytes;
 }
 
 cudaError_t launch_paged_decode(const PagedView &v, const PagedAttnLaunch &l,
@@ -994,16 +952,16 @@ cudaError_t launch_paged_decode(const PagedView &v, const PagedAttnLaunch &l,
   a.out_ld = l.out_ld;
   a.H = l.H;
   a.G = l.H / v.hkv;
-  a.part = static_cast<float *>(l.workspace);
-  uint8_t *rest = static_cast<uint8_t *>(l.workspace) + part_bytes(a.G, l.D);
-  a.claim = reinterpret_cast<unsigned int *>(rest);
-  a.parts = reinterpret_cast<DcParts *>(rest + 256);
+  // the counter lies first, whatever the shape (kPagedClaimBytes)
+  uint8_t *rest = static_cast<uint8_t *>(l.workspace) + kPagedClaimBytes;
+  a.claim = static_cast<unsigned int *>(l.workspace);
+  a.part = reinterpret_cast<float *>(rest);
+  a.parts = reinterpret_cast<DcParts *>(rest + part_bytes(a.G, l.D));
   a.scale2 = l.scale * kLog2e;
   a.window = l.window;
   a.sinks = l.sinks;
   const int page = 1 << v.page_shift;
   a.box_rows = page < kDcTile ? page : kDcTile;
-  a.min_tiles = 1;
   CUtensorMap kmap, vmap;
   if (!encode_pool(&kmap, v.k, v, l.D, a.box_rows) ||
       !encode_pool(&vmap, v.v, v, l.D, a.box_rows))

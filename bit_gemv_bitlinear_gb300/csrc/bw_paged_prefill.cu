@@ -1035,7 +1035,8 @@ cudaError_t launch_t(const PagedView &v, const PagedAttnLaunch &l,
   a.split = split_of(l.n_tokens, v.n_seqs, a.G, v.hkv,
                      int64_t(v.max_pages) << v.page_shift);
   const size_t rows = size_t(a.split) * l.n_tokens * l.H;
-  a.part = static_cast<float *>(l.workspace);
+  a.part = reinterpret_cast<float *>(static_cast<uint8_t *>(l.workspace) +
+                                     kPagedClaimBytes);
   a.ml = reinterpret_cast<float2 *>(a.part + rows * D);
 
   static std::atomic<int> cached[64];
@@ -1096,7 +1097,7 @@ size_t paged_prefill_workspace_bytes(int n_tokens, int n_seqs, int H, int Hkv,
                                      int D) {
   const int split = split_of(n_tokens, n_seqs, H / Hkv, Hkv, BW_PAGED_MAX_LEN);
   if (split == 1) return 16;
-  return size_t(split) * n_tokens * H * (size_t(D) * 4 + 8) + 16;
+  return size_t(split) * n_tokens * H * (size_t(D) * 4 + 8) + kPagedClaimBytes;
 }
 
 cudaError_t launch_paged_prefill(const PagedView &v, const PagedAttnLaunch &l,

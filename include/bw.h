@@ -584,14 +584,17 @@ bw_status bw_qk_norm_rope_append(const bw_bf16 *qkv, int64_t qkv_ld,
  *   q         bf16 [n_seqs][q_ld] device, 16-byte aligned: H rotated heads of
  *             D; q_ld a multiple of 8, at least H D.
  *   out       fp32 or (out_bf16 nonzero) bf16 [n_seqs][out_ld] device,
- *             16-byte aligned; out_ld a multiple of 8, at least H D.
+ *             16-byte aligned; out_ld a multiple of 8, at least H D; out must
+ *             not overlap q.
  *   scale > 0 (usually 1/sqrt(D)), window >= 0, sinks >= 0 (host).
  *   workspace device scratch of at least
  *             bw_attn_paged_decode_workspace_bytes(n_seqs, H, Hkv, D) bytes,
  *             16-byte aligned, owned by the caller.  Zero it once before its
- *             first use: it holds one counter per sequence and key-value
- *             head, which every call leaves at zero again.  Calls that share
- *             a workspace (captured graphs too) must not overlap on the GPU.
+ *             first use (its first 256 bytes are enough): it begins with a
+ *             counter that every call leaves at zero again.  Calls over paged
+ *             caches, of both kinds and any shapes, may share a workspace one
+ *             after the other; calls that share one (captured graphs too)
+ *             must not overlap on the GPU.
  *   Hkv divides H, H / Hkv <= BW_PAGED_MAX_GROUP; strides of rows below
  *   2^31. */
 size_t bw_attn_paged_decode_workspace_bytes(int n_seqs, int H, int Hkv, int D);
@@ -614,7 +617,8 @@ bw_status bw_attn_paged_decode(const bw_bf16 *q, int64_t q_ld, int H,
  *   q_start   as above (required).
  *   scale, window, sinks, H  as for bw_attn_paged_decode.
  *   workspace as above, bw_attn_paged_prefill_workspace_bytes(n_tokens,
- *             n_seqs, H, Hkv, D) bytes, zeroed once before its first use. */
+ *             n_seqs, H, Hkv, D) bytes; on its own it needs no zeroing (only
+ *             the first 256 bytes' counter has to be zero, for decode). */
 size_t bw_attn_paged_prefill_workspace_bytes(int n_tokens, int n_seqs, int H,
                                              int Hkv, int D);
 bw_status bw_attn_paged_prefill(const bw_bf16 *q, int64_t q_ld, int n_tokens,

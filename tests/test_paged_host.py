@@ -159,6 +159,11 @@ def test_prefill_checks(lib):
     assert prefill(lib, out=A) == INVALID  # q itself
 
 
+@pytest.mark.parametrize("bf16", [0, 1])
+def test_decode_checks(lib, bf16):
+    assert decode(lib, out=A, bf16=bf16) == INVALID  # q itself
+
+
 def test_workspace_sizes(lib):
     d, p = (lib.bw_attn_paged_decode_workspace_bytes,
             lib.bw_attn_paged_prefill_workspace_bytes)
