@@ -257,6 +257,19 @@ __device__ __forceinline__ void weights64(const float *s, float scale2, float m,
   sum = add2(sum, add2(acc[0], acc[1]));
 }
 
+// Whether the phase of `parity` is complete by now (it does not wait).
+__device__ __forceinline__ uint32_t mbar_test(uint64_t *bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(smem_addr(bar)), "r"(parity)
+      : "memory");
+  return done;
+}
+
 // Lanes 4 k .. 4 k + 3 hold pieces 0..3 of a row each; afterwards lane 4 k + q
 // holds piece q of the four rows.
 __device__ __forceinline__ void exchange4(uint32_t (&y)[4][4]) {
@@ -721,10 +734,15 @@ prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap qmap,
       head_of[q] = ((r & ~3) + q) - tok_of[q] * G;
     }
     uint32_t used = 0, outs = 0;  // key tiles and items so far
+    // Barriers are tested well before their phase is needed: a wait costs some
+    // 200 cycles even for what is there.
+    uint32_t s_there = 0;
     bool ok = true;
     PfItem it;
-    while (ok && next_item(it)) {
-      const PfWork w = pf_work(a, it);
+    bool more = next_item(it);
+    PfWork w{};
+    if (more) w = pf_work(a, it);
+    while (ok && more) {
       const int n_mine = i ? w.n1 : w.n0, t_mine = i ? w.tok1 : w.tok0;
       const bool live = tok < t_mine;
       const int first = it.pos0 + i * TQ;    // the tile's positions
@@ -741,7 +759,8 @@ prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap qmap,
       float m = live ? -INFINITY : 0.0f, l = 0.0f;
       bool unseen = true;  // of this warp's rows some may have m = -inf
       for (int j = 0; j < n_mine; ++j, ++used) {
-        if (!warp_wait(&bar[C::kFullS + i], used & 1u)) {
+        if (!__all_sync(0xffffffffu, s_there) &&
+            !warp_wait(&bar[C::kFullS + i], used & 1u)) {
           ok = false;
           break;
         }
@@ -785,7 +804,8 @@ prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap qmap,
           const float f = grow ? ex2(m - top) : 1.0f;
           if (grow) m = top;
           l *= f;
-          if (has_o && __any_sync(0xffffffffu, grow)) {
+          // (what a row that has seen nothing yet holds is zeros)
+          if (has_o && __any_sync(0xffffffffu, grow && f > 0.0f)) {
             if (wait && !warp_wait(&bar[C::kDoneO + i], phase & 1u)) ok = false;
             tc_fence_after();
 #pragma unroll 1
@@ -807,10 +827,10 @@ prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap qmap,
           if (lane == 0) mbar_arrive(&bar[C::kFullP + 2 * i + hh]);
         };
         // Weights against the m of the tiles before.  Where a row's weights
-        // sum to more than 2^16 (or some row has seen nothing yet, or not all
-        // of the tile is seen), the tile's maximum is looked for; otherwise no
-        // maximum is looked for at all: the scale cancels in o / l, and
-        // neither bf16 nor the fp32 sums lose anything by 2^16.
+        // sum to more than 2^16 (or some row has seen nothing yet) the tile's
+        // maximum is looked for; otherwise no maximum is looked for at all: the
+        // scale cancels in o / l, and neither bf16 nor the fp32 sums lose
+        // anything by 2^16.
         constexpr float kMost = 65536.0f;
         if constexpr (C::kOwnP) {
 #pragma unroll
@@ -823,7 +843,7 @@ prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap qmap,
           if (!all) mask();
           // (loops, here and below, so that the code, which is fetched anew
           // whenever the warp comes back to it, is there once)
-          for (bool must = !all || unseen;; must = true) {
+          for (bool must = unseen;; must = true) {
             if (must) follow(j > 0, true, used - 1);
             sum = make_float2(0.0f, 0.0f);
             weights64(s, a.scale2, m == -INFINITY ? 0.0f : m, wt, sum);
@@ -832,6 +852,7 @@ prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap qmap,
               tc_fence_after();
             }
             tmem_st32(t_p, wt);
+            s_there = mbar_test(&bar[C::kFullS + i], (used + 1) & 1u);
             weights64(s + 64, a.scale2, m == -INFINITY ? 0.0f : m, wt, sum);
             if (must || !__any_sync(0xffffffffu, sum.x + sum.y > kMost)) break;
           }
@@ -870,7 +891,11 @@ prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap qmap,
         if (w.j_lo + j + 1 == w.plan.n_sink) x += x_gap;
       }
 
-      // ---- out, or this part's sums ----
+      // ---- out, or this part's sums; the next item while the last product
+      // runs ----
+      PfItem next;
+      more = ok && next_item(next);
+      if (more) w = pf_work(a, next);
       if (ok && n_mine > 0) {
         // (A barrier of its own: kDoneO may be one or two products behind, and
         // a parity tells a phase only from the next one.)
@@ -934,6 +959,7 @@ prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap qmap,
           }
         }
       }
+      it = next;
       // The next item's first product overwrites O_i only after this
       // warpgroup has written its P, so after these loads.
       tc_fence_before();
