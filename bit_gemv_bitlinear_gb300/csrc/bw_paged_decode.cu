@@ -35,6 +35,9 @@
 //    shared memory.  A part that is the whole goes straight to the output;
 //    others go to the workspace, and a second kernel, launched along with the
 //    first and waiting for its end, joins them.
+// 64 sequences of up to 8191 positions, 20 + 2 x 5 heads of 128: 107 us, 0.97
+// of the measured copy rate; one of 131071: 55 us, 0.91 (the start and the join
+// are 5 us of it); 120 windows of 1000, 32 + 2 x 4 heads of 64: 31 us, 0.55.
 #include <climits>
 
 #include "bw_paged_tc.cuh"

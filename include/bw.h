@@ -591,7 +591,8 @@ bw_status bw_qk_norm_rope_append(const bw_bf16 *qkv, int64_t qkv_ld,
  *             bw_attn_paged_decode_workspace_bytes(n_seqs, H, Hkv, D) bytes,
  *             16-byte aligned, owned by the caller.  Zero it once before its
  *             first use (its first 256 bytes are enough): it begins with a
- *             counter that every call leaves at zero again.  Calls over paged
+ *             counter that every call leaves at zero again (zero it anew
+ *             after BW_ERR_CUDA or BW_ERR_TIMEOUT).  Calls over paged
  *             caches, of both kinds and any shapes, may share a workspace one
  *             after the other; calls that share one (captured graphs too)
  *             must not overlap on the GPU.
