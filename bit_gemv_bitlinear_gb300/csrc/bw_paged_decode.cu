@@ -15,7 +15,7 @@
 //  * Work is cut into tiles of 64 positions of one (sequence, head), all tiles
 //    in one order, found on the device from the lengths, so ragged batches
 //    and long single sequences balance alike and one launch serves every step
-//    of a graph.  The first 70 % of a long call are dealt to the CTAs in equal
+//    of a graph.  The first 90 % of a long call are dealt to the CTAs in equal
 //    contiguous shares, the rest in small units that a CTA claims when it is
 //    about to run out: SMs stream at unlike rates (equal shares of 50 us took
 //    42 to 61), and every piece ends in a part to be joined.
@@ -51,13 +51,14 @@ constexpr int kDcTile = 64;
 constexpr int kDcMaxSms = 160;
 // CTAs an SM: a tile takes a CTA's warps about 0.9 us from end to end, so it
 // takes several CTAs to keep up with the copies (the smaller the rows, the
-// more); what their stages and sums leave room for.
+// more); what their stages and sums leave room for.  120 windows of 1000, 32 +
+// 2 x 4 heads of 64: 31.4 us with 3, 34.0 with 2.
 __host__ __device__ constexpr int dc_ctas(int D, int GH) {
   return GH == 1 && D == 64 ? 3 : 2;
 }
 // Shares and claimed units, at most.
 __host__ __device__ constexpr int dc_max_units(int D, int G) {
-  return 5 * dc_ctas(D, G > 8 ? 2 : 1) * kDcMaxSms;
+  return 3 * dc_ctas(D, G > 8 ? 2 : 1) * kDcMaxSms;
 }
 
 // What the workspace keeps of a (sequence, head): its parts are those of units
@@ -304,7 +305,7 @@ decode_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap kmap,
     total += s_sum[w];
   }
   s_before[tid] = before;
-  const Dealing dl = deal(total, int(gridDim.x));
+  const Dealing dl = deal(total, int(gridDim.x), GH == 1);
   if (int(blockIdx.x) >= dl.n_ctas) return;  // the whole CTA
   __syncthreads();
 
@@ -371,7 +372,8 @@ decode_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap kmap,
       bool looked = false;
       auto find_next = [&] {
         looked = true;
-        // (a counter that was not zero at first claims nothing)
+        // (a counter that was not zero at first claims nothing; at most 2 units
+        // and one claim too many a CTA)
         const unsigned int c = __shfl_sync(0xffffffffu, claimed, 0);
         found = find(next, c < unsigned(dc_max_units(D, a.G)) ? dl.n_ctas + int(c)
                                                               : INT_MAX);
@@ -915,7 +917,8 @@ cudaError_t launch_t(const DecodeArgs &a, const CUtensorMap &kmap,
   e = cudaLaunchKernelEx(&cfg, decode_kernel<D, GH, BF16>, a, kmap, vmap);
   if (e != cudaSuccess) return e;
   // Few heads (so likely many parts each): a large block for each; else a
-  // small block for 8.
+  // small block for 8.  (Small blocks for one sequence of 131071 positions: 66
+  // us, not 55; large ones for 120 windows of 1000: 98, not 31.)
   const unsigned n = unsigned(a.v.n_seqs) * unsigned(a.H);
   cfg.dynamicSmemBytes = 0;
   if (n <= unsigned(device_sm_count())) {

@@ -57,34 +57,33 @@ BW_PLAN_FN int tile_pos(const TilePlan &t, int i, int tile) {
 }
 
 // How a decode call's tiles are dealt to `grid` CTAs: [0, dealt) in equal
-// shares (units 0 .. n_ctas - 1); [dealt, late) in units of unit_a tiles, the
-// rest in units of unit_b, both claimed while the call runs.  Few tiles are
-// all dealt.  At most 5 grid units in all; total below 2^32 grid.
+// shares (units 0 .. n_ctas - 1), the rest in units of `unit` tiles that are
+// claimed while the call runs (none if `claimed` is false or where they are
+// few).  At most 3 grid units in all; total below 2^32 grid.
 struct Dealing {
-  int64_t total, dealt, late;
-  int n_ctas, n_a, unit_a, unit_b;
+  int64_t total, dealt;
+  int n_ctas, unit;
 };
-BW_PLAN_FN Dealing deal(int64_t total, int grid) {
-  Dealing d{total, total, total, 0, 0, 1, 1};
+constexpr int kDealClaimTiles = 96;  // tiles a CTA from which some are claimed
+BW_PLAN_FN Dealing deal(int64_t total, int grid, bool claimed) {
+  Dealing d{total, total, 0, 1};
   d.n_ctas = total < grid ? int(total) : grid;
-  if (total > 0 && total >= 64 * int64_t(d.n_ctas)) {
-    // 20 % in at most 1.5 units a CTA, 10 % in at most 2: the shorter the
-    // unit, the less the last one keeps the call waiting, and the more parts
-    // there are to join.
-    d.late = total - total / 10;
-    d.dealt = d.late - total / 5;
-    const int64_t ua = (2 * (d.late - d.dealt) + 3 * d.n_ctas - 1) / (3 * d.n_ctas);
-    const int64_t ub = (total - d.late + 2 * d.n_ctas - 1) / (2 * d.n_ctas);
-    d.unit_a = ua < 4 ? 4 : int(ua);
-    d.unit_b = ub < 2 ? 2 : int(ub);
-    d.n_a = int((d.late - d.dealt + d.unit_a - 1) / d.unit_a);
+  if (claimed && total > 0 && total >= kDealClaimTiles * int64_t(d.n_ctas)) {
+    // 10 % in at most 2 units a CTA: the shorter the unit, the less the last
+    // one keeps the call waiting, and the more parts there are to join.  us of
+    // a decode call, 20 + 2 x 5 heads of 128, with claims and with equal
+    // shares: 32 sequences of 32768 positions (276 tiles a CTA) 374 and 384; 64
+    // of 8191 (135) 193 and 198; one of 262144 (68) 108 and 103, so from 96 on.
+    // More than 8 heads a key head (large parts to join): 16 + 2 x 1 of 64,
+    // 3000000 positions, 145 and 140, so none there.
+    d.dealt = total - total / 10;
+    d.unit = int((total - d.dealt + 2 * d.n_ctas - 1) / (2 * d.n_ctas));
   }
   return d;
 }
 BW_PLAN_FN int unit_of(const Dealing &d, int64_t tile) {
   if (tile < d.dealt) return int(((tile + 1) * d.n_ctas - 1) / d.dealt);
-  if (tile < d.late) return d.n_ctas + int((tile - d.dealt) / d.unit_a);
-  return d.n_ctas + d.n_a + int((tile - d.late) / d.unit_b);
+  return d.n_ctas + int((tile - d.dealt) / d.unit);
 }
 // The tiles of a unit (none past the last unit).
 BW_PLAN_FN void unit_range(const Dealing &d, int unit, int64_t *lo,
@@ -92,12 +91,9 @@ BW_PLAN_FN void unit_range(const Dealing &d, int unit, int64_t *lo,
   if (unit < d.n_ctas) {
     *lo = unit * d.dealt / d.n_ctas;
     *hi = (unit + 1) * d.dealt / d.n_ctas;
-  } else if (unit < d.n_ctas + d.n_a) {
-    *lo = d.dealt + int64_t(unit - d.n_ctas) * d.unit_a;
-    *hi = *lo + d.unit_a < d.late ? *lo + d.unit_a : d.late;
   } else {
-    *lo = d.late + int64_t(unit - d.n_ctas - d.n_a) * d.unit_b;
-    *hi = *lo + d.unit_b < d.total ? *lo + d.unit_b : d.total;
+    *lo = d.dealt + int64_t(unit - d.n_ctas) * d.unit;
+    *hi = *lo + d.unit < d.total ? *lo + d.unit : d.total;
   }
 }
 

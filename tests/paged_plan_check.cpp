@@ -69,38 +69,40 @@ int main() {
   for (int grid : {1, 2, 3, 152, 304, 456, 480}) {
     std::vector<int64_t> totals;
     for (int64_t n = 0; n < 400; ++n) totals.push_back(n);
-    for (int64_t k = 60; k < 70; ++k)
+    for (int64_t k = kDealClaimTiles - 5; k < kDealClaimTiles + 5; ++k)
       for (int64_t e = -3; e < 4; ++e)
         if (k * grid + e >= 0) totals.push_back(k * grid + e);
     for (int64_t n = 1000; n < (int64_t(grid < 32 ? grid : 32) << 32); n = n * 7 / 3 + 1)
       totals.push_back(n);
     for (int64_t total : totals) {
-      const Dealing d = deal(total, grid);
-      int64_t at = 0;
-      int unit = 0;
-      for (; at < total; ++unit) {
-        int64_t lo, hi;
-        unit_range(d, unit, &lo, &hi);
-        bool good = lo == at && hi > lo && hi <= total && unit < 5 * grid;
-        for (int64_t x : {lo, lo + (hi - lo) / 2, hi - 1})
-          good = good && unit_of(d, x) == unit;
-        ++checks;
-        if (!good) {
-          std::printf("unit grid=%d total=%lld unit=%d\n", grid,
-                      static_cast<long long>(total), unit);
-          return 1;
+      for (bool claimed : {false, true}) {
+        const Dealing d = deal(total, grid, claimed);
+        int64_t at = 0;
+        int unit = 0;
+        for (; at < total; ++unit) {
+          int64_t lo, hi;
+          unit_range(d, unit, &lo, &hi);
+          bool good = lo == at && hi > lo && hi <= total && unit < 3 * grid;
+          for (int64_t x : {lo, lo + (hi - lo) / 2, hi - 1})
+            good = good && unit_of(d, x) == unit;
+          ++checks;
+          if (!good) {
+            std::printf("unit grid=%d total=%lld unit=%d\n", grid,
+                        static_cast<long long>(total), unit);
+            return 1;
+          }
+          at = hi;
         }
-        at = hi;
-      }
-      // past the last unit there is nothing, however far
-      for (int past : {unit, unit + 1, unit + grid, 2147483647}) {
-        int64_t lo, hi;
-        unit_range(d, past, &lo, &hi);
-        ++checks;
-        if (past >= d.n_ctas && lo < total) {
-          std::printf("past grid=%d total=%lld unit=%d\n", grid,
-                      static_cast<long long>(total), past);
-          return 1;
+        // past the last unit there is nothing, however far
+        for (int past : {unit, unit + 1, unit + grid, 2147483647}) {
+          int64_t lo, hi;
+          unit_range(d, past, &lo, &hi);
+          ++checks;
+          if (past >= d.n_ctas && lo < total) {
+            std::printf("past grid=%d total=%lld unit=%d\n", grid,
+                        static_cast<long long>(total), past);
+            return 1;
+          }
         }
       }
     }

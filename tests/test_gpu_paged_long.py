@@ -78,7 +78,13 @@ def check_means(c, out, G, window, sinks, lens=None):
 
 
 CLAIMED = [
-    # H, Hkv, D, page, lens, window, sinks: 64 tiles and more a CTA
+    # H, Hkv, D, page, lens, window, sinks: tiles for which some are claimed,
+    # then more than 64 tiles a CTA that are all dealt
+    (16, 2, 128, 64, [600003, 0, 1] + [18000 + 37 * i for i in range(20)], 0, 0),
+    (4, 4, 64, 16, [24000 + 11 * i for i in range(31)] + [5], 0, 0),
+    (32, 8, 128, 256, [240001], 0, 0),
+    (5, 1, 64, 128, [2900007], 0, 0),
+    (16, 2, 128, 64, [130000] * 8, 120000, 130),
     (16, 2, 128, 64, [400003, 0, 1] + [12000 + 37 * i for i in range(20)], 0, 0),
     (4, 4, 64, 16, [16000 + 11 * i for i in range(31)] + [5], 0, 0),
     (32, 8, 128, 256, [160001], 0, 0),
@@ -110,7 +116,7 @@ def test_decode_replays_with_other_lengths(bw):
     """One captured call serves lengths of every kind: all claimed, all dealt,
     none; a second graph shares the workspace."""
     H, Hkv, D, page = 16, 2, 128, 64
-    full = [300000] + [18000 + i for i in range(24)]
+    full = [500000] + [24000 + i for i in range(24)]
     c = Long(2, full, Hkv, D, page)
     n = len(full)
     q = torch.zeros((n, H, D), dtype=torch.bfloat16, device="cuda")
@@ -125,7 +131,7 @@ def test_decode_replays_with_other_lengths(bw):
             with torch.cuda.graph(g, stream=side):
                 bw.bw_attn_paged_decode(q, *c.args, out=o, workspace=ws)
             graphs.append(g)
-        for lens in (full, [0] * n, [1] * n, [290017] + [17011 + i for i in range(24)],
+        for lens in (full, [0] * n, [1] * n, [480017] + [23011 + i for i in range(24)],
                      [777] * n, full):
             # pages past a shorter length are used no more: no NaN needed there
             c.len_d.copy_(torch.tensor(lens))
@@ -141,7 +147,7 @@ def test_decode_replays_with_other_lengths(bw):
 def test_decode_long_random(bw):
     """Scores that differ, over claimed units: against 64 bits."""
     H, Hkv, D, page = 8, 2, 128, 64
-    lens = [640001, 20, 4000]
+    lens = [960001, 20, 4000]
     c = Long(3, lens, Hkv, D, page)
     q = torch.randn((3, H, D), device="cuda").bfloat16()
     out = bw.bw_attn_paged_decode(q, *c.args, scale=0.2)
@@ -303,7 +309,7 @@ def test_offsets_past_31_bits(bw):
 def test_one_workspace_under_calls_of_many_shapes(bw):
     """Decode of several shapes and split prefill, one after the other on one
     workspace that was zeroed once."""
-    shapes = [(16, 2, 128, [650000]), (4, 4, 64, [500001]), (5, 1, 64, [77, 3]),
+    shapes = [(16, 2, 128, [960000]), (4, 4, 64, [720001]), (5, 1, 64, [77, 3]),
               (16, 1, 128, [1300000])]
     caches = [Long(6 + i, lens, Hkv, D, 64) for i, (_, Hkv, D, lens)
               in enumerate(shapes)]
