@@ -984,22 +984,46 @@ prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap qmap,
   }
 }
 
-// Joins the parts of a row (token, head): a warp per row.
+// Joins the parts of a row (token, head): a warp per row.  Everything is asked
+// for at once, before it is known which parts there are (what others hold is
+// not used): one load after the other took 8 us for 6000 rows of 6 parts.
 template <int D>
 __global__ void __launch_bounds__(256)
 prefill_join_kernel(const PrefillArgs a) {
+  constexpr int kE = D / 32;   // dims a lane
+  constexpr int kAhead = 8;    // parts in flight
+  struct alignas(kE * 4) Piece {
+    float v[kE];
+  };
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x & 31;
   const int64_t r = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  const int64_t rows = int64_t(a.n_tokens) * a.H;
+  if (r >= rows) return;
   const int t = int(r / a.H), h = int(r - int64_t(t) * a.H);
-  if (t >= a.n_tokens) return;
+  const float2 ml = lane < a.split ? __ldcg(a.ml + lane * rows + r)
+                                   : make_float2(-INFINITY, 0.0f);
+  const float *base = a.part + r * D + lane * kE;
+  Piece x[kAhead];
+  auto load = [&](int s0) {
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u)
+      if (s0 + u < a.split) {
+        const float *p = base + (s0 + u) * rows * D;
+        if constexpr (kE == 4) {
+          const float4 y = __ldcg(reinterpret_cast<const float4 *>(p));
+          x[u] = Piece{y.x, y.y, y.z, y.w};
+        } else {
+          const float2 y = __ldcg(reinterpret_cast<const float2 *>(p));
+          x[u] = Piece{y.x, y.y};
+        }
+      }
+  };
+  load(0);
   const int b = find_seq(a.q_start, a.v.n_seqs, t);
   const SeqTokens sq = seq_tokens(a.v, a.q_start, a.n_tokens, b);
   if (sq.bad || t < sq.q0 || t >= sq.q0 + sq.n) return;
-  const float2 ml = lane < a.split
-                        ? __ldcg(a.ml + (int64_t(lane) * a.n_tokens + t) * a.H + h)
-                        : make_float2(-INFINITY, 0.0f);
   const float mine = ml.y > 0.0f ? ml.x : -INFINITY;
   float top = mine;
 #pragma unroll
@@ -1009,18 +1033,16 @@ prefill_join_kernel(const PrefillArgs a) {
   float l = w * ml.y;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-  constexpr int kE = D / 32;
   float acc[kE] = {};
-  for (int s = 0; s < a.split; ++s) {
-    const float ws = __shfl_sync(0xffffffffu, w, s);
-    if (ws == 0.0f) continue;
-    const float *p =
-        a.part + ((int64_t(s) * a.n_tokens + t) * a.H + h) * D + lane * kE;
+  for (int s0 = 0; s0 < a.split; s0 += kAhead) {
+    if (s0 > 0) load(s0);
 #pragma unroll
-    for (int e = 0; e < kE; e += 2) {
-      const float2 x = __ldcg(reinterpret_cast<const float2 *>(p + e));
-      acc[e] = fmaf(ws, x.x, acc[e]);
-      acc[e + 1] = fmaf(ws, x.y, acc[e + 1]);
+    for (int u = 0; u < kAhead; ++u) {
+      const float ws = __shfl_sync(0xffffffffu, w, (s0 + u) & 31);
+      if (s0 + u < a.split && ws != 0.0f) {
+#pragma unroll
+        for (int e = 0; e < kE; ++e) acc[e] = fmaf(ws, x[u].v[e], acc[e]);
+      }
     }
   }
   const float inv = l > 0.0f ? 1.0f / l : 0.0f;
