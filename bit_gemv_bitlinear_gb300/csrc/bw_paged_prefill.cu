@@ -43,6 +43,8 @@
 // 2480 cycles, bound by the softmax's chain.  A window's masked tiles and the
 // ends of its short items (2900 tokens, window 700: seven tiles) cost half as
 // much again.
+#include <algorithm>
+
 #include "bw_paged_tc.cuh"
 
 namespace bw {
@@ -1061,14 +1063,22 @@ int64_t max_items(int n_tokens, int n_seqs, int TI, int Hkv) {
 }
 
 // Parts of an item's key axis: as many as fill the device, by the call's
-// sizes alone (max_len: the longest cache that the page table allows), so
-// that a captured graph serves every length.
-int split_of(int n_tokens, int n_seqs, int G, int Hkv, int64_t max_len) {
-  const int64_t items = max_items(n_tokens, n_seqs, 2 * (kPfRows / G), Hkv);
+// sizes alone (`see`: the positions that an item's tokens may see, by the page
+// table's width and the window), so that a captured graph serves every length.
+int split_of(int n_tokens, int n_seqs, int G, int Hkv, int64_t see) {
+  const int TQ = kPfRows / G;
+  const int64_t items = max_items(n_tokens, n_seqs, 2 * TQ, Hkv);
   int64_t s = kPfTargetCtas / items;
-  const int64_t tiles = (max_len + kPfTile - 1) / kPfTile;
+  const int64_t tiles = (see + kPfTile - 1) / kPfTile;
   if (s > tiles / kPfMinTiles) s = tiles / kPfMinTiles;
   if (s > kPfMaxSplit) s = kPfMaxSplit;
+  // Not worth it over a short axis where items of one query tile fit: about
+  // 9 + 1.2 tiles us, and 18.5 + 1.65 tiles / s with parts and their join (2000
+  // tokens, 8 + 2 x 8 heads of 128: 28.2 and 32.8 us; 1030 tokens, 16 + 2 x 8
+  // of 64: 16.0 and 27.8).
+  if (s > 1 && tiles * (8 * s - 11) <= 63 * s &&
+      max_items(n_tokens, n_seqs, TQ, Hkv) <= kPfTargetCtas)
+    return 1;
   return s < 1 ? 1 : int(s);
 }
 
@@ -1089,8 +1099,10 @@ cudaError_t launch_t(const PagedView &v, const PagedAttnLaunch &l,
   a.sinks = l.sinks;
   const int page = 1 << v.page_shift;
   a.box_rows = page < kPfTile ? page : kPfTile;
-  a.split = split_of(l.n_tokens, v.n_seqs, a.G, v.hkv,
-                     int64_t(v.max_pages) << v.page_shift);
+  int64_t see = int64_t(v.max_pages) << v.page_shift;
+  if (l.window > 0)  // (two tiles' edges and the first tokens' one)
+    see = std::min(see, int64_t(l.window) + l.sinks + 2 * a.TQ + 3 * kPfTile);
+  a.split = split_of(l.n_tokens, v.n_seqs, a.G, v.hkv, see);
   // One query tile an item where the device has room for the items (a prompt of
   // 509 tokens, 20 + 2 x 5 heads: 15.7 against 17.4 us); items that are cut
   // into parts fill it already.
