@@ -24,12 +24,15 @@ struct PagedView {
   unsigned int *err;
 };
 
-// The length of sequence b; -1 if it is bad (reported).
-__device__ __forceinline__ int seq_len(const PagedView &v, int b) {
-  const int n = __ldcg(v.len + b);
+// The length of a sequence, read as n; -1 if it is bad (reported).
+__device__ __forceinline__ int checked_len(const PagedView &v, int n) {
   if (n >= 0 && n <= (v.max_pages << v.page_shift)) return n;
   atomicOr(v.err, kPagedErr);
   return -1;
+}
+
+__device__ __forceinline__ int seq_len(const PagedView &v, int b) {
+  return checked_len(v, __ldcg(v.len + b));
 }
 
 // The page of position j >= 0 of sequence b (j below its length); -1 if the
@@ -55,6 +58,7 @@ __device__ __forceinline__ SeqTokens seq_tokens(const PagedView &v,
                                                 int n_tokens, int b) {
   SeqTokens r{0, 0, 0, false};
   const int a = __ldcg(q_start + b), e = __ldcg(q_start + b + 1);
+  const int n = __ldcg(v.len + b);  // asked for along with them
   if (a < 0 || e > n_tokens || a > e) {
     atomicOr(v.err, kPagedErr);
     r.bad = true;
@@ -63,7 +67,7 @@ __device__ __forceinline__ SeqTokens seq_tokens(const PagedView &v,
   r.q0 = a;
   r.n = e - a;
   if (r.n == 0) return r;
-  const int len = seq_len(v, b);
+  const int len = checked_len(v, n);
   if (len < r.n) {
     atomicOr(v.err, kPagedErr);
     r.bad = true;

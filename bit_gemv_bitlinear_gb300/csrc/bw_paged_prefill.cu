@@ -346,7 +346,11 @@ __device__ __forceinline__ PfWork pf_work(const PrefillArgs &a, const PfItem &it
   return w;
 }
 
-template <int D>
+// Alone (128 dims): items of one query tile.  Nothing else fills the time
+// between its products, so the next scores are made during its softmax, in the
+// other tile's columns, the two in turn (a prompt of 509 tokens, 20 + 2 x 5
+// heads: 15.2 us, 16.0 without, 17.4 with items of two query tiles).
+template <int D, bool Alone>
 __global__ void __launch_bounds__(kPfThreads, 1)
 prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap qmap,
                const __grid_constant__ CUtensorMap kmap,
@@ -363,6 +367,7 @@ prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap qmap,
   const int TQ = a.TQ, G = a.G;
 
   if (tid == 0) {
+#pragma unroll 1
     for (int i = 0; i < C::kNumBars; ++i) mbar_init(&bar[i], C::count(i));
     mbar_arrive(&bar[C::kTurn]);  // query tile 0 begins
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -379,12 +384,15 @@ prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap qmap,
   // ---- items of all sequences: thread t counts those of sequences
   // [t per, (t + 1) per), before[t] is where they begin ----
   const int per = (a.v.n_seqs + kPfScan - 1) / kPfScan;  // at most 16
+  SeqTokens kept{0, 0, 0, false};  // few sequences, the scheduler: one a lane
   {
     const int b_lo = tid < kPfScan ? min(tid * per, a.v.n_seqs) : a.v.n_seqs;
     const int b_hi = min(b_lo + per, a.v.n_seqs);
     int mine = 0;
     for (int b = b_lo; b < b_hi; ++b)
       mine += (seq_tokens(a.v, a.q_start, a.n_tokens, b).n + a.TI - 1) / a.TI;
+    if (warp == kPfItemWarp && a.v.n_seqs <= 32 && lane < a.v.n_seqs)
+      kept = seq_tokens(a.v, a.q_start, a.n_tokens, lane);
     int incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -446,8 +454,15 @@ prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap qmap,
         u -= before[below - 1];
         const int b = (below - 1) * per + lane;
         SeqTokens t{0, 0, 0, false};
-        if (lane < per && b < a.v.n_seqs)
+        if (a.v.n_seqs <= 32) {  // per is 1
+          t.q0 = __shfl_sync(0xffffffffu, kept.q0, below - 1);
+          t.n = __shfl_sync(0xffffffffu, kept.n, below - 1);
+          t.pos0 = __shfl_sync(0xffffffffu, kept.pos0, below - 1);
+          t.bad = __shfl_sync(0xffffffffu, int(kept.bad), below - 1);
+          if (lane > 0) t.n = 0;
+        } else if (lane < per && b < a.v.n_seqs) {
           t = seq_tokens(a.v, a.q_start, a.n_tokens, b);
+        }
         const int n = (t.n + a.TI - 1) / a.TI;
         int incl = n;
 #pragma unroll
@@ -618,16 +633,17 @@ prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap qmap,
       const uint32_t t_s = tmem + C::kS + i * 128, t_o = tmem + C::kO + i * D;
       const uint32_t t_p = tmem + C::kP + i * C::kPStep;
       const uint64_t qd = sw128_desc(base + C::kQ + i * C::kQBytes);
-      auto scores = [&](int slot) {  // S_i = Q_i K^T
+      auto scores = [&](int slot, uint32_t t_s, int b) {  // S_i = Q_i K^T
         const uint64_t kd = sw128_desc(base + C::kK + slot * C::kTileBytes);
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks)
           tc_mma_ss(t_s, qd + uint64_t((ks >> 2) * (C::kQHalf / 16) + (ks & 3) * 2),
                     kd + uint64_t((ks >> 2) * (C::kHalf / 16) + (ks & 3) * 2),
                     kIdS, ks > 0);
-        tc_commit(&bar[C::kFullS + i]);
+        tc_commit(&bar[C::kFullS + b]);
       };
-      auto values = [&](int slot, int hh, bool first) {  // O_i += P_i V, a half
+      auto values = [&](int slot, int hh, bool first, uint32_t t_p) {
+        // O_i += P_i V, a half
         const uint64_t vd =
             sw128_desc_t(base + C::kV + slot * C::kTileBytes, C::kHalf);
 #pragma unroll
@@ -651,12 +667,56 @@ prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap qmap,
       const int t_bar = C::kTurn + i;
       int ks = 0, kr = 0, vs = 0, vr = 0;  // stages and rounds
       int used = 0, cq = 0;                // this tile's products, queries
+      int made = 0;                        // and scores (Alone)
       const int p_bar = C::kFullP + 2 * i;
       bool ok = true;
       PfItem it;
       while (ok && next_item(it)) {
         const PfWork w = pf_work(a, it);
         if (w.n == 0) continue;
+        if constexpr (Alone) {
+          if (i == 1) continue;  // (the first warp counts twice)
+          auto twice = [&](int b) {
+            tc_commit(&bar[b]);
+            tc_commit(&bar[b]);
+          };
+          auto next_scores = [&](bool last) {
+            scores(ks, tmem + C::kS + (made & 1) * 128, made & 1);
+            twice(C::kEmptyK + ks);
+            if (last) twice(C::kEmptyQ);
+          };
+          for (int j = -1; ok && j < w.n; ++j) {
+            if (j + 1 < w.n) {
+              const int k_bar = C::kFullK + ks;
+              ok = wait3(k_bar, kr, C::kFullQ, cq, k_bar, kr);
+              if (ok && elect_one()) next_scores(j + 2 == w.n);
+              __syncwarp();
+              ++made;
+              if (++ks == C::kKStages) ks = 0, ++kr;
+            }
+            if (j < 0) continue;
+            const int v_bar = C::kReadyV + vs;
+            const uint32_t t_pj = tmem + C::kS + (used & 1) * 128;
+            ok = ok && wait3(p_bar, used, v_bar, vr, p_bar, used);
+            if (ok && elect_one()) {
+              values(vs, 0, j == 0, t_pj);
+              tc_commit(&bar[C::kDoneO]);
+            }
+            __syncwarp();
+            ok = ok && wait3(p_bar + 1, used, p_bar + 1, used, p_bar + 1, used);
+            if (ok && elect_one()) {
+              values(vs, 1, false, t_pj);
+              tc_commit(&bar[C::kDoneO + 1]);
+              if (j + 1 == w.n) tc_commit(&bar[C::kFullO]);
+              twice(C::kEmptyV + vs);
+            }
+            __syncwarp();
+            ++used;
+            if (++vs == C::kVStages) vs = 0, ++vr;
+          }
+          ++cq;
+          continue;
+        }
         const int n_mine = i ? w.n1 : w.n0;
         // Tile 0's scores; then for every j tile j's values and tile j + 1's
         // scores.  Stages that only the other query tile uses are passed on
@@ -670,7 +730,7 @@ prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap qmap,
             if (j + 2 == w.n) tc_commit(&bar[C::kEmptyQ]);
           };
           auto next_scores = [&] {
-            if (my_next) scores(ks);
+            if (my_next) scores(ks, t_s, i);
             if (!C::kOwnP) mbar_arrive(&bar[C::kTurn + 1 - i]);
             next_stage();
           };
@@ -695,8 +755,8 @@ prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap qmap,
             __syncwarp();
             ok = ok && wait3(p_bar + 1, used, v_bar, vr, p_bar + 1, used);
             if (ok && elect_one()) {
-              values(vs, 0, j == 0);
-              values(vs, 1, false);
+              values(vs, 0, j == 0, t_p);
+              values(vs, 1, false, t_p);
               tc_commit(&bar[C::kDoneO + i]);
               if (j + 1 == n_mine) tc_commit(&bar[C::kFullO + i]);
               tc_commit(&bar[C::kEmptyV + vs]);
@@ -704,15 +764,15 @@ prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap qmap,
           } else {
             ok = wait3(p_bar, used, v_bar, vr, t_bar, turns++);
             if (ok && elect_one()) {
-              values(vs, 0, j == 0);
+              values(vs, 0, j == 0, t_p);
               tc_commit(&bar[C::kDoneO + i]);
             }
             __syncwarp();
             ok = ok && wait3(p_bar + 1, used, next ? k_bar : p_bar + 1,
                              next ? kr : used, p_bar + 1, used);
             if (ok && elect_one()) {
-              values(vs, 1, false);
-              if (my_next) scores(ks);
+              values(vs, 1, false, t_p);
+              if (my_next) scores(ks, t_s, i);
               mbar_arrive(&bar[C::kTurn + 1 - i]);
               if (j + 1 == n_mine) tc_commit(&bar[C::kFullO + i]);
               next_stage();
@@ -734,8 +794,8 @@ prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap qmap,
     const int i = warp >> 2;
     const int r = (warp & 3) * 32 + lane;
     const uint32_t t_lane = tmem + (uint32_t((warp & 3) * 32) << 16);
-    const uint32_t t_s = t_lane + C::kS + i * 128;
-    const uint32_t t_p = t_lane + C::kP + i * C::kPStep;
+    const uint32_t t_s0 = t_lane + C::kS + i * 128;
+    const uint32_t t_p0 = t_lane + C::kP + i * C::kPStep;
     const uint32_t t_o = t_lane + C::kO + i * D;
     const int tok = r / G;
     // token and head of the four rows that this lane stores a piece of
@@ -771,12 +831,16 @@ prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap qmap,
       float m = live ? -INFINITY : 0.0f, l = 0.0f;
       bool unseen = true;  // of this warp's rows some may have m = -inf
       for (int j = 0; j < n_mine; ++j, ++used) {
+        // (alone: a barrier for each of the two places)
         if (!__all_sync(0xffffffffu, s_there) &&
-            !warp_wait(&bar[C::kFullS + i], used & 1u)) {
+            !warp_wait(&bar[C::kFullS + (Alone ? used & 1u : uint32_t(i))],
+                       (Alone ? used >> 1 : used) & 1u)) {
           ok = false;
           break;
         }
         tc_fence_after();
+        const uint32_t t_s = Alone ? t_s0 + (used & 1u) * 128 : t_s0;
+        const uint32_t t_p = Alone ? t_s : t_p0;
         float s[128];
         uint32_t wt[32];
         float2 sum = make_float2(0.0f, 0.0f);
@@ -798,9 +862,9 @@ prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap qmap,
         };
         // m follows this tile's maximum where that is more than 8 above; what
         // was summed before is rescaled, O_i too where it holds something
-        // (has_o), once the products that were issued are done (kDoneO's phase
-        // `phase`, if wait).
-        auto follow = [&](bool has_o, bool wait, uint32_t phase) {
+        // (has_o), once the products that were issued are done (phase `phase` of
+        // the barrier `wait`, if any).
+        auto follow = [&](bool has_o, int wait, uint32_t phase) {
           float mx[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k) mx[k] = max3(s[3 * k], s[3 * k + 1], s[3 * k + 2]);
@@ -818,7 +882,7 @@ prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap qmap,
           l *= f;
           // (what a row that has seen nothing yet holds is zeros)
           if (has_o && __any_sync(0xffffffffu, grow && f > 0.0f)) {
-            if (wait && !warp_wait(&bar[C::kDoneO + i], phase & 1u)) ok = false;
+            if (wait >= 0 && !warp_wait(&bar[wait], phase & 1u)) ok = false;
             tc_fence_after();
 #pragma unroll 1
             for (int c = 0; c < D; c += 32) {
@@ -856,7 +920,7 @@ prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap qmap,
           // (loops, here and below, so that the code, which is fetched anew
           // whenever the warp comes back to it, is there once)
           for (bool must = unseen;; must = true) {
-            if (must) follow(j > 0, true, used - 1);
+            if (must) follow(j > 0, C::kDoneO + i, used - 1);
             sum = make_float2(0.0f, 0.0f);
             weights64(s, a.scale2, m == -INFINITY ? 0.0f : m, wt, sum);
             if (j > 0) {  // O_i(j - 1) has read the weights before
@@ -882,18 +946,30 @@ prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap qmap,
           tmem_landed(s + 96);
           if (!all) mask();
           if (!all || unseen || __any_sync(0xffffffffu, sum.x + sum.y > kMost)) {
-            follow(j > 0, false, 0);  // S_i(j) came after O_i(j - 1)
+            // (S_i(j) came after O_i(j - 1), but not if alone)
+            follow(j > 0, Alone ? C::kDoneO + 1 : -1, used - 1);
             sum = make_float2(0.0f, 0.0f);
             weights64(s, a.scale2, m == -INFINITY ? 0.0f : m, wt, sum);
           }
+          // (Alone, these scores were there before O_i(j - 1): the weights go
+          // out only after it, or kFullP would be two phases ahead of the
+          // products' warp.)
+          uint32_t o_done = 0;
+          if (Alone && j > 0) o_done = mbar_test(&bar[C::kDoneO + 1], (used - 1) & 1u);
           tmem_st32(t_p, wt);
+          if (Alone && j > 0 && !__all_sync(0xffffffffu, o_done) &&
+              !warp_wait(&bar[C::kDoneO + 1], (used - 1) & 1u))
+            ok = false;
           hand_over(0);  // its product starts
+          if (Alone)
+            s_there = mbar_test(&bar[C::kFullS + ((used + 1) & 1u)],
+                                ((used + 1) >> 1) & 1u);
           l += sum.x + sum.y;
           for (bool again = false;; again = true) {
             sum = make_float2(0.0f, 0.0f);
             weights64(s + 64, a.scale2, m == -INFINITY ? 0.0f : m, wt, sum);
             if (again || !__any_sync(0xffffffffu, sum.x + sum.y > kMost)) break;
-            follow(true, true, used);  // after the first half's product
+            follow(true, C::kDoneO + i, used);  // after the first half's product
           }
         }
         tmem_st32(t_p + 32, wt);
@@ -1062,29 +1138,33 @@ int64_t max_items(int n_tokens, int n_seqs, int TI, int Hkv) {
   return (int64_t(n_tokens) / TI + seqs) * Hkv;
 }
 
-// Parts of an item's key axis: as many as fill the device, by the call's
-// sizes alone (`see`: the positions that an item's tokens may see, by the page
-// table's width and the window), so that a captured graph serves every length.
-int split_of(int n_tokens, int n_seqs, int G, int Hkv, int64_t see) {
+// How a call is cut, by its sizes alone (`see`: the positions that an item's
+// tokens may see, by the page table's width and the window), so that a
+// captured graph serves every length: into items of one query tile or of two,
+// and those into parts of the key axis, at most `split`.
+struct PfCut {
+  bool one;
+  int split;
+};
+PfCut cut_of(int n_tokens, int n_seqs, int G, int Hkv, int64_t see) {
   const int TQ = kPfRows / G;
   const int64_t items = max_items(n_tokens, n_seqs, 2 * TQ, Hkv);
+  const bool one = max_items(n_tokens, n_seqs, TQ, Hkv) <= kPfTargetCtas;
   int64_t s = kPfTargetCtas / items;
   const int64_t tiles = (see + kPfTile - 1) / kPfTile;
   if (s > tiles / kPfMinTiles) s = tiles / kPfMinTiles;
   if (s > kPfMaxSplit) s = kPfMaxSplit;
-  // Not worth it over a short axis where items of one query tile fit: about
-  // 9 + 1.2 tiles us, and 18.5 + 1.65 tiles / s with parts and their join (2000
-  // tokens, 8 + 2 x 8 heads of 128: 28.2 and 32.8 us; 1030 tokens, 16 + 2 x 8
-  // of 64: 16.0 and 27.8).
-  if (s > 1 && tiles * (8 * s - 11) <= 63 * s &&
-      max_items(n_tokens, n_seqs, TQ, Hkv) <= kPfTargetCtas)
-    return 1;
-  return s < 1 ? 1 : int(s);
+  // Parts are not worth it over a short axis where items of one query tile fit:
+  // about 9 + 1.1 tiles us, and 18.5 + 1.65 tiles / s with parts and their join
+  // (2000 tokens, 8 + 2 x 8 heads of 128: 25.8 and 32.8 us; 1030 tokens, 16 +
+  // 2 x 8 of 64: 16.1 and 27.8).
+  if (s <= 1 || (one && tiles * (22 * s - 33) <= 190 * s)) return {one, 1};
+  return {false, int(s)};
 }
 
-template <int D>
+template <int D, bool Alone>
 cudaError_t launch_t(const PagedView &v, const PagedAttnLaunch &l,
-                     cudaStream_t stream) {
+                     const PfCut &cut, cudaStream_t stream) {
   PrefillArgs a{};
   a.v = v;
   a.q_start = l.q_start;
@@ -1099,17 +1179,8 @@ cudaError_t launch_t(const PagedView &v, const PagedAttnLaunch &l,
   a.sinks = l.sinks;
   const int page = 1 << v.page_shift;
   a.box_rows = page < kPfTile ? page : kPfTile;
-  int64_t see = int64_t(v.max_pages) << v.page_shift;
-  if (l.window > 0)  // (two tiles' edges and the first tokens' one)
-    see = std::min(see, int64_t(l.window) + l.sinks + 2 * a.TQ + 3 * kPfTile);
-  a.split = split_of(l.n_tokens, v.n_seqs, a.G, v.hkv, see);
-  // One query tile an item where the device has room for the items (a prompt of
-  // 509 tokens, 20 + 2 x 5 heads: 15.7 against 17.4 us); items that are cut
-  // into parts fill it already.
-  a.TI = 2 * a.TQ;
-  if (a.split == 1 &&
-      max_items(l.n_tokens, v.n_seqs, a.TQ, v.hkv) <= kPfTargetCtas)
-    a.TI = a.TQ;
+  a.split = cut.split;
+  a.TI = cut.one ? a.TQ : 2 * a.TQ;
   const size_t rows = size_t(a.split) * l.n_tokens * l.H;
   a.part = reinterpret_cast<float *>(static_cast<uint8_t *>(l.workspace) +
                                      kPagedClaimBytes);
@@ -1117,7 +1188,7 @@ cudaError_t launch_t(const PagedView &v, const PagedAttnLaunch &l,
 
   static std::atomic<int> cached[64];
   int resident = 0;
-  cudaError_t e = paged_resident(prefill_kernel<D>, cached, kPfThreads,
+  cudaError_t e = paged_resident(prefill_kernel<D, Alone>, cached, kPfThreads,
                                  PfCfg<D>::kSmem, &resident);
   if (e != cudaSuccess) return e;
   // setmaxnreg draws on the registers of the launch: a build that gives the
@@ -1125,7 +1196,7 @@ cudaError_t launch_t(const PagedView &v, const PagedAttnLaunch &l,
   static std::atomic<int> regs{0};  // a property of the build, not the device
   if (regs.load(std::memory_order_relaxed) == 0) {
     cudaFuncAttributes fa{};
-    e = cudaFuncGetAttributes(&fa, prefill_kernel<D>);
+    e = cudaFuncGetAttributes(&fa, prefill_kernel<D, Alone>);
     if (e != cudaSuccess) return e;
     regs.store(fa.numRegs, std::memory_order_relaxed);
   }
@@ -1159,7 +1230,7 @@ cudaError_t launch_t(const PagedView &v, const PagedAttnLaunch &l,
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, prefill_kernel<D>, a, qmap, kmap, vmap);
+  e = cudaLaunchKernelEx(&cfg, prefill_kernel<D, Alone>, a, qmap, kmap, vmap);
   if (e != cudaSuccess || a.split == 1) return e;
   cfg.gridDim = dim3(unsigned((int64_t(l.n_tokens) * l.H + 7) / 8));
   cfg.blockDim = dim3(256);
@@ -1171,14 +1242,23 @@ cudaError_t launch_t(const PagedView &v, const PagedAttnLaunch &l,
 
 size_t paged_prefill_workspace_bytes(int n_tokens, int n_seqs, int H, int Hkv,
                                      int D) {
-  const int split = split_of(n_tokens, n_seqs, H / Hkv, Hkv, BW_PAGED_MAX_LEN);
+  const int split =
+      cut_of(n_tokens, n_seqs, H / Hkv, Hkv, BW_PAGED_MAX_LEN).split;
   if (split == 1) return 16;
   return size_t(split) * n_tokens * H * (size_t(D) * 4 + 8) + kPagedClaimBytes;
 }
 
 cudaError_t launch_paged_prefill(const PagedView &v, const PagedAttnLaunch &l,
                                  cudaStream_t stream) {
-  return l.D == 64 ? launch_t<64>(v, l, stream) : launch_t<128>(v, l, stream);
+  const int G = l.H / v.hkv;
+  int64_t see = int64_t(v.max_pages) << v.page_shift;
+  if (l.window > 0)  // (two tiles' edges and the first tokens' one)
+    see = std::min(see,
+                   int64_t(l.window) + l.sinks + 2 * (kPfRows / G) + 3 * kPfTile);
+  const PfCut cut = cut_of(l.n_tokens, v.n_seqs, G, v.hkv, see);
+  if (l.D == 64) return launch_t<64, false>(v, l, cut, stream);
+  return cut.one ? launch_t<128, true>(v, l, cut, stream)
+                 : launch_t<128, false>(v, l, cut, stream);
 }
 
 }  // namespace bw
