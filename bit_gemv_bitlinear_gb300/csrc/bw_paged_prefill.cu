@@ -33,9 +33,9 @@
 //  * CTAs stay: one per SM, each goes through its items (a scheduler warp
 //    finds them), so the next item's copies and first scores run while the
 //    last one's softmax and output do.
-//  * Where there are too few tiles for the device, the key axis is cut too:
-//    the parts' o and (m, l) go to the workspace and a second kernel joins
-//    them, a warp per row.
+//  * Where there are too few tiles for the device, a CTA takes one query tile,
+//    or, over a long axis, the key axis is cut too: the parts' o and (m, l)
+//    go to the workspace and a second kernel joins them, a warp per row.
 // 8192 tokens, 20 + 2 x 5 heads of 128: 217 us, 1580 TFLOP/s of the visible
 // pairs, 0.82 of the rate of a large cuBLAS product here; the tensor pipe is
 // busy 69 % of the time, the rest is the softmax's latency around it (a pair of

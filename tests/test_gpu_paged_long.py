@@ -382,6 +382,23 @@ def test_captured_prefill_and_append(bw, H, Hkv, D, lens, new):
         assert (out[n0 + n1:] == 5.0).all()
 
 
+@pytest.mark.parametrize("H,Hkv,D", [(20, 5, 128), (8, 8, 128), (6, 1, 64)])
+def test_short_prompts_again_and_again(bw, H, Hkv, D):
+    """Few tiles, copies that land late or early: the same every time."""
+    lens = [200, 130, 517, 64]
+    c = Long(14, lens, Hkv, D, 32)
+    q = torch.randn((sum(lens), H, D), device="cuda").bfloat16()
+    st = torch.tensor(np.concatenate([[0], np.cumsum(lens)]), dtype=torch.int32,
+                      device="cuda")
+    sweep = torch.empty(64 << 20, device="cuda")  # more than L2 holds
+    want = bw.bw_attn_paged_prefill(q, *c.args, st)
+    for i in range(200):
+        if i % 4 == 0:
+            sweep.fill_(i)
+        assert torch.equal(want, bw.bw_attn_paged_prefill(q, *c.args, st))
+    assert bw.bw_device_error() == 0
+
+
 def test_calls_at_once_on_two_streams(bw):
     """Prefill, split and not, and decode beside each other, a workspace each."""
     H, Hkv, D, page = 16, 4, 128, 64
