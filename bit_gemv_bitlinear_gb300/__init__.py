@@ -487,12 +487,38 @@ def _paged_kv(k_pages, v_pages, page_table, kv_len):
     """(bw_paged_kv as bytes, device, n_seqs, Hkv, D) of four tensors.  The
     pools [n_pages][Hkv][page][D] may be strided from page to page (two views
     of one pool, say)."""
+    try:
+        dev, shape, st = k_pages.get_device(), k_pages.shape, k_pages.stride()
+        n_pages, hkv, page, D = shape
+        n, = kv_len.shape
+        rows, max_pages = page_table.shape
+        ok = dev >= 0 and k_pages.dtype is _BF16 and \
+            (st[3] == 1 or D == 1) and (st[2] == D or page == 1) and \
+            (st[1] == page * D or hkv == 1) and \
+            v_pages.dtype is _BF16 and v_pages.get_device() == dev and \
+            v_pages.shape == shape and v_pages.stride() == st and \
+            kv_len.dtype is _I32 and kv_len.get_device() == dev and \
+            kv_len.is_contiguous() and rows == n and \
+            page_table.dtype is _I32 and page_table.get_device() == dev and \
+            page_table.is_contiguous()
+    except (AttributeError, TypeError, ValueError):
+        ok = False
+    if not ok:
+        _refuse_kv(k_pages, v_pages, page_table, kv_len)
+    return _PAGED_KV.pack(
+        k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(),
+        kv_len.data_ptr(), st[0] if n_pages > 1 else hkv * page * D, n_pages,
+        page, hkv, D, n, max_pages), dev, n, hkv, D
+
+
+def _refuse_kv(k_pages, v_pages, page_table, kv_len):
+    """Says which tensor of a cache failed its checks."""
     pages = "must be [n_pages][Hkv][page][D] with contiguous pages"
     if not isinstance(k_pages, torch.Tensor) or not k_pages.is_cuda or \
             k_pages.dtype is not _BF16 or k_pages.dim() != 4:
         _refuse(k_pages, (_BF16,), -1, f"k_pages {pages}")
     dev, shape, st = k_pages.get_device(), k_pages.shape, k_pages.stride()
-    n_pages, hkv, page, D = shape
+    _, hkv, page, D = shape
     if st[3] != 1 and D > 1 or st[2] != D and page > 1 or \
             st[1] != page * D and hkv > 1:
         _refuse(k_pages, (_BF16,), dev, f"k_pages {pages}")
@@ -503,24 +529,20 @@ def _paged_kv(k_pages, v_pages, page_table, kv_len):
     if not _is(kv_len, _I32, dev) or kv_len.dim() != 1 or \
             not kv_len.is_contiguous():
         _refuse(kv_len, (_I32,), dev, "kv_len must be a contiguous [n_seqs]")
-    n = kv_len.shape[0]
-    if not _is(page_table, _I32, dev) or page_table.dim() != 2 or \
-            page_table.shape[0] != n or not page_table.is_contiguous():
-        _refuse(page_table, (_I32,), dev,
-                f"page_table must be a contiguous [{n}][max_pages]")
-    return _PAGED_KV.pack(
-        k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(),
-        kv_len.data_ptr(), st[0] if n_pages > 1 else hkv * page * D, n_pages,
-        page, hkv, D, n, page_table.shape[1]), dev, n, hkv, D
+    _refuse(page_table, (_I32,), dev, "page_table must be a contiguous "
+            f"[{kv_len.shape[0]}][max_pages]")
 
 
 def _rows(t, dtypes, dev: int, rows: int, H: int, D: int, name: str):
     """(pointer, row stride) of [rows][H][D] with contiguous rows."""
-    if isinstance(t, torch.Tensor) and t.dtype in dtypes and \
-            t.get_device() == dev and t.shape == (rows, H, D):
-        st = t.stride()
-        if (st[2] == 1 or D == 1) and (st[1] == D or H == 1):
-            return t.data_ptr(), (st[0] if rows > 1 else H * D)
+    try:
+        if t.dtype in dtypes and t.get_device() == dev and \
+                t.shape == (rows, H, D):
+            st = t.stride()
+            if (st[2] == 1 or D == 1) and (st[1] == D or H == 1):
+                return t.data_ptr(), (st[0] if rows > 1 else H * D)
+    except AttributeError:
+        pass
     _refuse(t, dtypes, dev, f"{name} must be [{rows}][{H}][{D}] with "
             "contiguous rows")
 
@@ -533,10 +555,14 @@ def _positions(window: int, sinks: int):
 
 def _vector(t, dtype, dev: int, count: int, name: str) -> int:
     """Pointer of a contiguous tensor of at least `count` elements."""
-    if not _is(t, dtype, dev) or not t.is_contiguous() or t.numel() < count:
-        _refuse(t, (dtype,), dev,
-                f"{name} must be contiguous with at least {count} elements")
-    return t.data_ptr()
+    try:
+        if t.dtype is dtype and t.get_device() == dev and \
+                t.is_contiguous() and t.numel() >= count:
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _refuse(t, (dtype,), dev,
+            f"{name} must be contiguous with at least {count} elements")
 
 
 _NO_CONTEXT = contextlib.nullcontext()
