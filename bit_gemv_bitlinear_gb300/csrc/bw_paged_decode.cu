@@ -52,13 +52,12 @@ constexpr int kDcMaxSms = 160;
 // CTAs an SM: a tile takes a CTA's warps about 0.9 us from end to end, so it
 // takes several CTAs to keep up with the copies (the smaller the rows, the
 // more); what their stages and sums leave room for.  120 windows of 1000, 32 +
-// 2 x 4 heads of 64: 31.4 us with 3, 34.0 with 2.
-__host__ __device__ constexpr int dc_ctas(int D, int GH) {
-  return GH == 1 && D == 64 ? 3 : 2;
-}
+// 2 x 4 heads of 64: 31.4 us with 3, 34.0 with 2; 32 sequences of up to 53787,
+// 32 + 2 x 2 heads: 100 with 3 (of 3 stages), 111 with 2 (of 4 or 5).
+__host__ __device__ constexpr int dc_ctas(int D) { return D == 64 ? 3 : 2; }
 // Shares and claimed units, at most.
-__host__ __device__ constexpr int dc_max_units(int D, int G) {
-  return 3 * dc_ctas(D, G > 8 ? 2 : 1) * kDcMaxSms;
+__host__ __device__ constexpr int dc_max_units(int D) {
+  return 3 * dc_ctas(D) * kDcMaxSms;
 }
 
 // What the workspace keeps of a (sequence, head): its parts are those of units
@@ -99,9 +98,9 @@ struct DcCfg {
   static constexpr uint32_t kHalf = kDcTile * 128;        // 64 dims
   static constexpr uint32_t kKBytes = kHalf * (D / 64);
   static constexpr uint32_t kStage = 2 * kKBytes;
-  static constexpr int kCtas = dc_ctas(D, GH);
+  static constexpr int kCtas = dc_ctas(D);
   // 128 to 192 KB of stages an SM
-  static constexpr int kStages = GH == 1 ? (D == 128 ? 3 : 4) : (D == 128 ? 2 : 4);
+  static constexpr int kStages = GH == 1 ? (D == 128 ? 3 : 4) : (D == 128 ? 2 : 3);
   static constexpr int kPad = D + 4;                       // floats a row
   // the warps' sums [3][8 GH][kPad] and (m, l)
   static constexpr uint32_t kDump = kStages * kStage;
@@ -375,7 +374,7 @@ decode_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap kmap,
         // (a counter that was not zero at first claims nothing; at most 2 units
         // and one claim too many a CTA)
         const unsigned int c = __shfl_sync(0xffffffffu, claimed, 0);
-        found = find(next, c < unsigned(dc_max_units(D, a.G)) ? dl.n_ctas + int(c)
+        found = find(next, c < unsigned(dc_max_units(D)) ? dl.n_ctas + int(c)
                                                               : INT_MAX);
       };
       int unit0 = 0, parts = 0;  // of the item
@@ -856,7 +855,7 @@ decode_join_kernel(const DecodeArgs a) {
   // is not followed)
   auto parts_of = [&](int head) {
     DcParts ps = a.parts[head / a.G];
-    const int most = dc_max_units(D, a.G);
+    const int most = dc_max_units(D);
     if (ps.unit0 < 0 || ps.parts > most || ps.unit0 > most - ps.parts)
       ps.parts = 0;
     return ps;
@@ -883,7 +882,7 @@ decode_join_kernel(const DecodeArgs a) {
 size_t align256(size_t b) { return (b + 255) / 256 * 256; }
 
 size_t part_bytes(int G, int D) {
-  return align256(size_t(2) * dc_max_units(D, G) * part_floats(G, D) *
+  return align256(size_t(2) * dc_max_units(D) * part_floats(G, D) *
                   sizeof(float));
 }
 
@@ -899,7 +898,7 @@ cudaError_t launch_t(const DecodeArgs &a, const CUtensorMap &kmap,
   // More CTAs than tiles have nothing to do, however long the sequences may
   // be.  (Shares of at least 2 or 4 tiles were slower for windowed batches: a
   // CTA's tiles come one after the other.)
-  constexpr int kMost = dc_ctas(D, GH) * kDcMaxSms;
+  constexpr int kMost = dc_ctas(D) * kDcMaxSms;
   int64_t ctas = resident < kMost ? resident : kMost;
   const int64_t most = int64_t(a.v.n_seqs) * a.v.hkv *
                        ((int64_t(a.v.max_pages) << a.v.page_shift) / kDcTile + 1);
