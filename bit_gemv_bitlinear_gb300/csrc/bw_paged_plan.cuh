@@ -75,7 +75,7 @@ BW_PLAN_FN Dealing deal(int64_t total, int grid, bool claimed) {
     // shares: 32 sequences of 32768 positions (276 tiles a CTA) 374 and 384; 64
     // of 8191 (135) 193 and 198; one of 262144 (68) 108 and 103, so from 96 on.
     // More than 8 heads a key head (large parts to join): 16 + 2 x 1 of 64,
-    // 3000000 positions, 145 and 140, so none there.
+    // 3000000 positions, 140 and 128, so none there.
     d.dealt = total - total / 10;
     d.unit = int((total - d.dealt + 2 * d.n_ctas - 1) / (2 * d.n_ctas));
   }
