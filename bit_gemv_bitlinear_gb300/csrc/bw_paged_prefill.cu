@@ -877,11 +877,14 @@ prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap qmap,
           mx[1] = max3(mx[1], s[126], s[127]);
           const float top = max3(mx[0], mx[1], fmaxf(mx[2], mx[3])) * a.scale2;
           const bool grow = top > m + 8.0f;
+          // What a row that has seen nothing yet holds is zeros.  That goes by
+          // its m, not by f: over a jump of 127 and more f is 0, and what the
+          // row holds has to go.
+          const bool held = m > -INFINITY;
           const float f = grow ? ex2(m - top) : 1.0f;
           if (grow) m = top;
           l *= f;
-          // (what a row that has seen nothing yet holds is zeros)
-          if (has_o && __any_sync(0xffffffffu, grow && f > 0.0f)) {
+          if (has_o && __any_sync(0xffffffffu, grow && held)) {
             if (wait >= 0 && !warp_wait(&bar[wait], phase & 1u)) ok = false;
             tc_fence_after();
 #pragma unroll 1
