@@ -1105,12 +1105,14 @@ prefill_join_kernel(const PrefillArgs a) {
   const int b = find_seq(a.q_start, a.v.n_seqs, t);
   const SeqTokens sq = seq_tokens(a.v, a.q_start, a.n_tokens, b);
   if (sq.bad || t < sq.q0 || t >= sq.q0 + sq.n) return;
-  const float mine = ml.y > 0.0f ? ml.x : -INFINITY;
+  // A part without visible positions has the sum 0.  One that holds NaN (a
+  // query's, or of a score past fp32's range) keeps it, and so does the row.
+  const float mine = ml.y == 0.0f ? -INFINITY : ml.x;
   float top = mine;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1)
     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-  const float w = mine == -INFINITY ? 0.0f : ex2(mine - top);
+  const float w = ml.y == 0.0f ? 0.0f : ex2(mine - top);
   float l = w * ml.y;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
@@ -1126,7 +1128,7 @@ prefill_join_kernel(const PrefillArgs a) {
       }
     }
   }
-  const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
   __nv_bfloat16 *o = a.out + int64_t(t) * a.out_ld + h * D + lane * kE;
 #pragma unroll
   for (int e = 0; e < kE; e += 2)

@@ -611,7 +611,9 @@ bw_status bw_attn_paged_decode(const bw_bf16 *q, int64_t q_ld, int H,
  * positions j <= p, with a window those of bw_attn_paged_decode.
  * Products run on the tensor cores with fp32 accumulation; the exp weights
  * are rounded to bf16, like the output.  What a position that some new token
- * of its sequence sees holds must be finite; others may hold anything.
+ * of its sequence sees holds must be finite; others may hold anything.  A
+ * query that is not finite, or whose scores leave fp32's range, gives NaN in
+ * its own row and head alone.
  *   q         bf16 [n_tokens][q_ld] device, out bf16 [n_tokens][out_ld]
  *             device: 16-byte aligned, both strides multiples of 8, at least
  *             H D and below 2^31; out must not overlap q.

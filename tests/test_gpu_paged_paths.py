@@ -6,11 +6,37 @@ test_gpu_paged.py, whose caches these are.
 import numpy as np
 import pytest
 
-from test_gpu_paged import Cache, as_bf16, bw, f64  # noqa: F401
+from test_gpu_paged import U, Cache, as_bf16, bw  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
 torch = pytest.importorskip("torch")
+
+
+def exact(q, k, v, first, window, sinks, scale):
+    """Tokens q [T][H][D] at positions first and on over k, v [n][Hkv][D]:
+    (out, bound), [T][H][D] in 64 bits; the bound is that of attend() in
+    test_gpu_paged.py for bf16 weights and a bf16 output."""
+    T, H, D = q.shape
+    q, k, v = q.double(), k.cuda().double(), v.cuda().double()
+    G = H // k.shape[1]
+    p = first + torch.arange(T, device="cuda")[:, None]
+    j = torch.arange(len(k), device="cuda")[None, :]
+    vis = j <= p
+    if window:
+        vis &= (j > p - window) | (j < sinks)
+    out, bound = torch.empty_like(q), torch.empty_like(q)
+    for h in range(H):
+        kh, vh = k[:, h // G], v[:, h // G]
+        s = (q[:, h] @ kh.T * scale).masked_fill(~vis, float("-inf"))
+        mass = (q[:, h].abs() @ kh.abs().T * scale).masked_fill(~vis, 0.0)
+        w = torch.softmax(s, 1)
+        out[:, h] = w @ vh
+        rel = (D + 4) * 2 * U * mass.amax(1) + (8 + vis.sum(1)) * U
+        top = vh.abs().amax(1)[None, :].expand_as(vis).masked_fill(~vis, 0.0)
+        tol = (2 * rel * top.amax(1))[:, None] + 2.0 ** -8 * (w @ vh.abs())
+        bound[:, h] = tol + 2.0 ** -8 * (out[:, h].abs() + tol)
+    return out, bound
 
 
 # ---------------------------------------------------------------------------
@@ -56,3 +82,51 @@ def test_a_jump_clears_what_was_summed(bw, path, H, Hkv, n, new, at, D, jump):
     for got in (out, one):
         err = (got.double() - want).abs()
         assert (err <= 2.0 ** -8 * want.abs() + 1e-18).all(), float(err.max())
+
+
+# ---------------------------------------------------------------------------
+# queries that are not finite
+# ---------------------------------------------------------------------------
+
+ODD = [
+    # path, H, Hkv, positions, new tokens, window, sinks
+    ("one", 4, 1, 330, 60, 0, 0),
+    ("two", 16, 1, 1600, 1300, 0, 0),
+    ("parts", 4, 2, 9000, 40, 0, 0),
+    ("parts", 16, 1, 9000, 5, 5000, 4),
+]
+
+
+@pytest.mark.parametrize("path,H,Hkv,n,new,window,sinks", ODD)
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("odd", [float("nan"), float("inf"), 3.0e38])
+def test_a_query_that_is_not_finite_shows(bw, path, H, Hkv, n, new, window,
+                                          sinks, D, odd):
+    """A query with NaN or an infinity, or with scores past fp32's range: NaN
+    in that token's head and nowhere else, as a softmax of such scores has it
+    (whose sum is NaN), and as decode gives it.
+
+    One position's first key value is 64, so that 3e38 times it is +infinity in
+    fp32.  The other rows stay within the bound (not the same bit for bit: the
+    rows of a warp decide together when a maximum follows, and the bf16 weights
+    are relative to it)."""
+    c = Cache(141, [n], Hkv, D, 64)
+    at = n - new - 70
+    c.k[0][at, :, 0] = 64.0
+    c.kp[int(c.table[0, at // 64]), :, at % 64, 0] = 64.0
+    rng = np.random.default_rng(142)
+    q = as_bf16(rng.standard_normal((new, H, D))).cuda()
+    st = torch.tensor([0, new], dtype=torch.int32, device="cuda")
+    kw = dict(window=window, sinks=sinks)
+    want, tol = exact(q, c.k[0], c.v[0], n - new, window, sinks, D ** -0.5)
+    q[new - 1, 1, 0] = odd
+    got = bw.bw_attn_paged_prefill(q, *c.args, st, **kw)
+    one = bw.bw_attn_paged_decode(q[-1:], *c.args, **kw)
+    assert bw.bw_device_error() == 0
+    assert torch.isnan(got[new - 1, 1]).all()
+    assert torch.isnan(one[0, 1]).all()
+    keep = torch.ones((new, H), dtype=torch.bool, device="cuda")
+    keep[new - 1, 1] = False
+    err = (got.double() - want).abs()[keep]
+    assert (err <= tol[keep]).all(), float((err - tol[keep]).max())
+    assert torch.isfinite(one[0, keep[-1]]).all()
