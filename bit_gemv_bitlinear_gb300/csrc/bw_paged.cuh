@@ -126,9 +126,10 @@ struct PagedAttnLaunch {
   int out_bf16;
   void *workspace;
 };
-// The attention calls' workspaces begin with decode's counter of claimed units,
-// zero between calls; prefill leaves it alone, so that calls of any kind and
-// shape may follow one another on one workspace.
+// The attention calls' workspaces begin with decode's counter of claimed units
+// and its mark of the first claim, zero between calls; prefill leaves them
+// alone, so that calls of any kind and shape may follow one another on one
+// workspace.
 constexpr size_t kPagedClaimBytes = 256;
 size_t paged_decode_workspace_bytes(int n_seqs, int H, int Hkv, int D);
 cudaError_t launch_paged_decode(const PagedView &v, const PagedAttnLaunch &l,

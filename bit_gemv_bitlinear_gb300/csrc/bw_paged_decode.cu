@@ -60,6 +60,10 @@ __host__ __device__ constexpr int dc_max_units(int D) {
   return 3 * dc_ctas(D) * kDcMaxSms;
 }
 
+// A counter that was not zero when a call began loses units.  Nobody gets the
+// first one then (or a claim is above all units), and that is reported.
+constexpr unsigned int kDcFirst = 0x706b7631u;
+
 // What the workspace keeps of a (sequence, head): its parts are those of units
 // unit0 .. unit0 + parts - 1 (parts 1: the output is written already, 0: zeros
 // are).
@@ -75,7 +79,9 @@ struct DecodeArgs {
   int64_t out_ld;
   float *part;          // [2 dc_max_units][part_floats(G, D)]
   DcParts *parts;       // [n_seqs][Hkv]
-  unsigned int *claim;  // units claimed so far; zero between calls
+  // units claimed so far, and kDcFirst once the first of them is; both zero
+  // between calls
+  unsigned int *claim;
   int H, G;
   float scale2;         // scale log2(e)
   int window, sinks;
@@ -371,11 +377,14 @@ decode_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap kmap,
       bool looked = false;
       auto find_next = [&] {
         looked = true;
-        // (a counter that was not zero at first claims nothing; at most 2 units
-        // and one claim too many a CTA)
+        // (at most 2 units and one claim too many a CTA)
         const unsigned int c = __shfl_sync(0xffffffffu, claimed, 0);
-        found = find(next, c < unsigned(dc_max_units(D)) ? dl.n_ctas + int(c)
-                                                              : INT_MAX);
+        const bool possible = c < unsigned(dc_max_units(D));
+        if (lane == 0) {
+          if (c == 0) a.claim[1] = kDcFirst;
+          if (!possible) atomicOr(a.v.err, kPagedErr);
+        }
+        found = find(next, possible ? dl.n_ctas + int(c) : INT_MAX);
       };
       int unit0 = 0, parts = 0;  // of the item
       auto count_parts = [&] {
@@ -754,7 +763,13 @@ decode_join_kernel(const DecodeArgs a) {
   __shared__ DcParts s_parts[kHeads];
   pdl_wait();
   pdl_trigger();
-  if (blockIdx.x == 0 && threadIdx.x == 0) *a.claim = 0u;  // for the next call
+  // The claims' two words, asked for here and looked at at the end; zero for
+  // the next call.
+  uint2 claims = make_uint2(0u, 0u);
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
+    claims = __ldcg(reinterpret_cast<const uint2 *>(a.claim));
+    *reinterpret_cast<uint2 *>(a.claim) = make_uint2(0u, 0u);
+  }
   const int stride = part_floats(a.G, D);
   const int n = a.v.n_seqs * a.H;
 
@@ -877,6 +892,7 @@ decode_join_kernel(const DecodeArgs a) {
     const DcParts ps = s_parts[k];
     if (ps.parts > kFew) join(first + k * step, ps, threadIdx.x, std::true_type{});
   }
+  if (claims.x != 0u && claims.y != kDcFirst) atomicOr(a.v.err, kPagedErr);
 }
 
 size_t align256(size_t b) { return (b + 255) / 256 * 256; }

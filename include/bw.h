@@ -507,7 +507,8 @@ bw_status bw_attn_decode_ex(const bw_bf16 *qkv, const int *pos, int H,
  * host.  Bit 256 of the device error word is set (bw_device_error then
  * returns BW_ERR_INVALID_ARG) for a length outside [0, max_pages *
  * page_size], a token range of a sequence that is not within [0, n_tokens]
- * or is longer than the sequence, and a used entry outside [0, n_pages).
+ * or is longer than the sequence, a used entry outside [0, n_pages), and a
+ * decode workspace whose counter was not zero.
  * Nothing outside the buffers is read or written for them: a bad sequence
  * counts as one without visible positions (its attention rows are zeros, it
  * appends nothing), and a bad page reads as zeros and is not written.
@@ -592,7 +593,9 @@ bw_status bw_qk_norm_rope_append(const bw_bf16 *qkv, int64_t qkv_ld,
  *             16-byte aligned, owned by the caller.  Zero it once before its
  *             first use (its first 256 bytes are enough): it begins with a
  *             counter that every call leaves at zero again (zero it anew
- *             after BW_ERR_CUDA or BW_ERR_TIMEOUT).  Calls over paged
+ *             after BW_ERR_CUDA or BW_ERR_TIMEOUT).  A call that finds
+ *             something else there may leave positions out; it sets bit 256
+ *             of the device error word.  Calls over paged
  *             caches, of both kinds and any shapes, may share a workspace one
  *             after the other; calls that share one (captured graphs too)
  *             must not overlap on the GPU.
@@ -642,7 +645,8 @@ bw_status bw_attn_paged_prefill(const bw_bf16 *q, int64_t q_ld, int n_tokens,
  * outside its cache.  Bit 128: bw_attn_decode_ex with BW_ATTN_PAST_READY
  * read a different position after its dependency wait than before it (the
  * promise was broken; the call used the later one).  Bit 256: a call over
- * a paged cache met a bad length, token range or page number.
+ * a paged cache met a bad length, token range or page number, or a workspace
+ * that was not zeroed.
  * Returns BW_ERR_TIMEOUT if any bit other than 16, 128 and 256 was set, else
  * BW_ERR_INVALID_ARG if one of these was, else BW_OK; *bits receives the
  * word.

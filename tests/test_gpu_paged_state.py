@@ -1,0 +1,36 @@
+"""What calls over a paged key-value cache (GB300) find in device memory that
+the host cannot check: reported by bit 256 of the device error word, and
+without harm for the calls after.  Every case stays within the buffers.
+"""
+import pytest
+
+from test_gpu_paged import bw, take_bad  # noqa: F401
+from test_gpu_paged_long import Long, check_means
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+
+@pytest.mark.parametrize("words", [
+    [1], [3], [200], [10 ** 6], [2 ** 31 - 1], [-1], [-40], [-304], [-500],
+    [7, 1], [1, 1], [0x01010101] * 64, [-1] * 64])
+@pytest.mark.parametrize("lens", [[240001], [777, 0, 50]])
+def test_a_workspace_that_was_not_zeroed_is_reported(bw, words, lens):
+    """Long calls (some units claimed) and short ones; the next call on the
+    same workspace is right again."""
+    H, Hkv, D = 32, 8, 128
+    c = Long(171, lens, Hkv, D, 256)
+    n = len(lens)
+    q = torch.zeros((n, H, D), dtype=torch.bfloat16, device="cuda")
+    ws = torch.zeros((bw.bw_attn_paged_decode_workspace_bytes(n, H, Hkv, D),),
+                     dtype=torch.uint8, device="cuda")
+    ws.view(torch.int32)[:len(words)] = torch.tensor(words, dtype=torch.int32,
+                                                     device="cuda")
+    bw.bw_attn_paged_decode(q, *c.args, workspace=ws)
+    torch.cuda.synchronize()
+    take_bad(bw)
+    for _ in range(2):
+        out = bw.bw_attn_paged_decode(q, *c.args, workspace=ws)
+        assert bw.bw_device_error() == 0
+        check_means(c, out, H // Hkv, 0, 0)
