@@ -48,20 +48,21 @@ __device__ __forceinline__ int seq_page(const PagedView &v, int b, int j) {
 // The new tokens of sequence b: rows q0 .. q0 + n - 1 of n_tokens at
 // positions pos0 .. pos0 + n - 1; n = 0 without tokens.  bad: the range or
 // the length is bad (reported); the range is kept where it lies within the
-// call's rows.
+// call's rows.  back: it runs backwards, so that others may overlap.
 struct SeqTokens {
   int q0, n, pos0;
-  bool bad;
+  bool bad, back;
 };
 __device__ __forceinline__ SeqTokens seq_tokens(const PagedView &v,
                                                 const int *q_start,
                                                 int n_tokens, int b) {
-  SeqTokens r{0, 0, 0, false};
+  SeqTokens r{0, 0, 0, false, false};
   const int a = __ldcg(q_start + b), e = __ldcg(q_start + b + 1);
   const int n = __ldcg(v.len + b);  // asked for along with them
   if (a < 0 || e > n_tokens || a > e) {
     atomicOr(v.err, kPagedErr);
     r.bad = true;
+    r.back = a > e;
     return r;
   }
   r.q0 = a;
@@ -131,6 +132,8 @@ struct PagedAttnLaunch {
 // alone, so that calls of any kind and shape may follow one another on one
 // workspace.
 constexpr size_t kPagedClaimBytes = 256;
+// Prefill in parts leaves a word of its own there, for its join.
+constexpr size_t kPagedVoidAt = 128;
 size_t paged_decode_workspace_bytes(int n_seqs, int H, int Hkv, int D);
 cudaError_t launch_paged_decode(const PagedView &v, const PagedAttnLaunch &l,
                                 cudaStream_t stream);

@@ -73,6 +73,7 @@ struct PrefillArgs {
   int64_t out_ld;
   float *part;   // [split][n_tokens][H][D]
   float2 *ml;    // [split][n_tokens][H]
+  int *void_call;  // split > 1: nothing was done, so there is nothing to join
   int H, G, TQ;
   int TI;        // tokens of an item: TQ or 2 TQ
   float scale2;
@@ -384,13 +385,20 @@ prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap qmap,
   // ---- items of all sequences: thread t counts those of sequences
   // [t per, (t + 1) per), before[t] is where they begin ----
   const int per = (a.v.n_seqs + kPfScan - 1) / kPfScan;  // at most 16
-  SeqTokens kept{0, 0, 0, false};  // few sequences, the scheduler: one a lane
+  // Ranges that run backwards let others overlap, and the items of 4096
+  // sequences that all hold every row would go on for hours: no items then.
+  bool void_call;
+  SeqTokens kept{0, 0, 0, false, false};  // few sequences, the scheduler: one a lane
   {
     const int b_lo = tid < kPfScan ? min(tid * per, a.v.n_seqs) : a.v.n_seqs;
     const int b_hi = min(b_lo + per, a.v.n_seqs);
     int mine = 0;
-    for (int b = b_lo; b < b_hi; ++b)
-      mine += (seq_tokens(a.v, a.q_start, a.n_tokens, b).n + a.TI - 1) / a.TI;
+    bool back = false;
+    for (int b = b_lo; b < b_hi; ++b) {
+      const SeqTokens t = seq_tokens(a.v, a.q_start, a.n_tokens, b);
+      mine += (t.n + a.TI - 1) / a.TI;
+      back |= t.back;
+    }
     if (warp == kPfItemWarp && a.v.n_seqs <= 32 && lane < a.v.n_seqs)
       kept = seq_tokens(a.v, a.q_start, a.n_tokens, lane);
     int incl = mine;
@@ -400,12 +408,13 @@ prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap qmap,
       if (lane >= o) incl += x;
     }
     if (lane == 31 && tid < kPfScan) s_sum[warp] = incl;
-    __syncthreads();
+    void_call = __syncthreads_or(back);
     int at = incl - mine;
 #pragma unroll
     for (int w = 0; w < kPfScan / 32; ++w)
       if (w < warp) at += s_sum[w];
     if (tid < kPfScan) before[tid] = at;
+    if (a.split > 1 && blockIdx.x == 0 && tid == 0) *a.void_call = void_call;
   }
   tc_fence_before();
   __syncthreads();
@@ -437,6 +446,7 @@ prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap qmap,
       // zeros of the value rows that no token of the item sees. ----
       int total = 0;
       for (int w = 0; w < kPfScan / 32; ++w) total += s_sum[w];
+      if (void_call) total = 0;
       const int n_items = total * a.v.hkv * a.split;  // below 2^23
       auto find = [&](int k, PfItem &it) {
         it = PfItem{-1, 0, 0, 0, 0, 0, 0};
@@ -453,7 +463,7 @@ prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap qmap,
           below += __shfl_xor_sync(0xffffffffu, below, o);
         u -= before[below - 1];
         const int b = (below - 1) * per + lane;
-        SeqTokens t{0, 0, 0, false};
+        SeqTokens t{0, 0, 0, false, false};
         if (a.v.n_seqs <= 32) {  // per is 1
           t.q0 = __shfl_sync(0xffffffffu, kept.q0, below - 1);
           t.n = __shfl_sync(0xffffffffu, kept.n, below - 1);
@@ -1102,9 +1112,10 @@ prefill_join_kernel(const PrefillArgs a) {
       }
   };
   load(0);
+  const int void_call = __ldcg(a.void_call);
   const int b = find_seq(a.q_start, a.v.n_seqs, t);
   const SeqTokens sq = seq_tokens(a.v, a.q_start, a.n_tokens, b);
-  if (sq.bad || t < sq.q0 || t >= sq.q0 + sq.n) return;
+  if (void_call || sq.bad || t < sq.q0 || t >= sq.q0 + sq.n) return;
   // A part without visible positions has the sum 0.  One that holds NaN (a
   // query's, or of a score past fp32's range) keeps it, and so does the row.
   const float mine = ml.y == 0.0f ? -INFINITY : ml.x;
@@ -1190,6 +1201,8 @@ cudaError_t launch_t(const PagedView &v, const PagedAttnLaunch &l,
   a.part = reinterpret_cast<float *>(static_cast<uint8_t *>(l.workspace) +
                                      kPagedClaimBytes);
   a.ml = reinterpret_cast<float2 *>(a.part + rows * D);
+  a.void_call = reinterpret_cast<int *>(static_cast<uint8_t *>(l.workspace) +
+                                        kPagedVoidAt);
 
   static std::atomic<int> cached[64];
   int resident = 0;

@@ -510,8 +510,11 @@ bw_status bw_attn_decode_ex(const bw_bf16 *qkv, const int *pos, int H,
  * or is longer than the sequence, a used entry outside [0, n_pages), and a
  * decode workspace whose counter was not zero.
  * Nothing outside the buffers is read or written for them: a bad sequence
- * counts as one without visible positions (its attention rows are zeros, it
- * appends nothing), and a bad page reads as zeros and is not written.
+ * counts as one without visible positions (its attention rows are zeros where
+ * its range lies within the call's rows, it appends nothing), and a bad page
+ * reads as zeros and is not written.  Where q_start decreases, ranges may
+ * overlap: bw_attn_paged_prefill then writes nothing at all, and
+ * bw_qk_norm_rope_append takes each row into one range that holds it, or none.
  * q_start (int32 [n_seqs + 1] device, 4-byte aligned): sequence b owns the
  * rows q_start[b] .. q_start[b + 1] - 1 of the call's n_tokens rows, its last
  * q_start[b + 1] - q_start[b] positions; q_start does not decrease.  Rows

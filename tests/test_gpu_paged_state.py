@@ -34,3 +34,37 @@ def test_a_workspace_that_was_not_zeroed_is_reported(bw, words, lens):
         out = bw.bw_attn_paged_decode(q, *c.args, workspace=ws)
         assert bw.bw_device_error() == 0
         check_means(c, out, H // Hkv, 0, 0)
+
+
+@pytest.mark.parametrize("lens,tokens,window", [
+    ([20000, 300, 40, 900], 30, 0),         # the key axis in parts
+    ([20000, 300, 40, 900], 30, 64),        # items of one query tile
+    ([3000, 3000, 3000, 3000], 2600, 0),    # items of two
+])
+@pytest.mark.parametrize("D", [64, 128])
+def test_ranges_that_run_backwards(bw, lens, tokens, window, D):
+    """q_start that decreases: ranges that overlap.  Reported, no row written,
+    and the next call on the same workspace is right."""
+    H, Hkv = 8, 8
+    c = Long(181, lens, Hkv, D, 64)
+    n = len(lens)
+    q = torch.zeros((tokens, H, D), dtype=torch.bfloat16, device="cuda")
+    ws = torch.zeros((bw.bw_attn_paged_prefill_workspace_bytes(
+        tokens, n, H, Hkv, D),), dtype=torch.uint8, device="cuda")
+    good = torch.tensor([0, tokens - 9, tokens - 6, tokens - 6, tokens],
+                        dtype=torch.int32, device="cuda")
+    want = bw.bw_attn_paged_prefill(q, *c.args, good, window=window)
+    assert bw.bw_device_error() == 0
+    for bad in ([0, tokens, 0, tokens, 0], [tokens, 0, 0, 0, 0],
+                [0, 5, 3, 12, tokens], [0, 0, 0, tokens, tokens - 1]):
+        st = torch.tensor(bad, dtype=torch.int32, device="cuda")
+        out = torch.full(q.shape, 9.0, dtype=torch.bfloat16, device="cuda")
+        bw.bw_attn_paged_prefill(q, *c.args, st, window=window, out=out,
+                                 workspace=ws)
+        torch.cuda.synchronize()
+        take_bad(bw)
+        assert (out == 9.0).all()
+        got = bw.bw_attn_paged_prefill(q, *c.args, good, window=window,
+                                       workspace=ws)
+        assert bw.bw_device_error() == 0
+        assert torch.equal(got, want)
