@@ -1,6 +1,6 @@
 // bw_paged_plan.cuh -- which cache positions the tokens of a paged-attention
-// call see, in which tiles they are visited, and how a decode call's tiles are
-// dealt to its CTAs.  Integer arithmetic only, on the host and on the device,
+// call see, in which tiles they are visited, how a decode call's tiles are
+// dealt to its CTAs, and how a prefill call is cut into items.  Integer arithmetic only, on the host and on the device,
 // and plain C++ as well, so that a host program can check every plan without a
 // GPU.
 //
@@ -95,6 +95,59 @@ BW_PLAN_FN void unit_range(const Dealing &d, int unit, int64_t *lo,
     *lo = d.dealt + int64_t(unit - d.n_ctas) * d.unit;
     *hi = *lo + d.unit < d.total ? *lo + d.unit : d.total;
   }
+}
+
+// ---- prefill: two query tiles of 128 rows (128 / G tokens each) an item, or
+// one, and the key axis whole or in parts ----
+constexpr int kPfTile = 128;     // positions of a key tile
+constexpr int kPfRows = 128;     // rows of a query tile
+constexpr int kPfMostCtas = 152;  // CTAs that a call is cut for, at most
+constexpr int kPfMaxSplit = 16;
+constexpr int kPfMinTiles = 4;   // key tiles of a part, at least
+
+// Items of a call that is not cut into parts, at most, of `tokens` tokens:
+// every sequence may leave one partly filled.
+BW_PLAN_FN int64_t prefill_items(int n_tokens, int n_seqs, int tokens,
+                                 int Hkv) {
+  const int64_t seqs = n_seqs < n_tokens ? n_seqs : n_tokens;
+  return (int64_t(n_tokens) / tokens + seqs) * Hkv;
+}
+
+// The positions that an item's tokens may see, in a cache of `longest` ones
+// (with a window: two tiles' edges and the first tokens' one beside it).
+BW_PLAN_FN int64_t prefill_axis(int64_t longest, int window, int sinks,
+                                int G) {
+  if (window <= 0) return longest;
+  const int64_t see =
+      int64_t(window) + sinks + 2 * (kPfRows / G) + 3 * kPfTile;
+  return see < longest ? see : longest;
+}
+
+// How a call is cut for `ctas` CTAs, one an SM: into items of one query tile
+// or of two, and those into parts of the key axis, at most `split`.
+struct PfCut {
+  bool one;
+  int split;
+};
+BW_PLAN_FN PfCut prefill_cut(int n_tokens, int n_seqs, int G, int Hkv,
+                             int64_t see, int ctas) {
+  const int TQ = kPfRows / G;
+  const int64_t items = prefill_items(n_tokens, n_seqs, 2 * TQ, Hkv);
+  const bool one = prefill_items(n_tokens, n_seqs, TQ, Hkv) <= ctas;
+  int64_t s = ctas / items;
+  const int64_t tiles = (see + kPfTile - 1) / kPfTile;
+  if (s > tiles / kPfMinTiles) s = tiles / kPfMinTiles;
+  if (s > kPfMaxSplit) s = kPfMaxSplit;
+  // Parts are not worth it over a short axis where items of one query tile fit:
+  // about 9 + 1.1 tiles us, and 18.5 + 1.65 tiles / s with parts and their join
+  // (2000 tokens, 8 + 2 x 8 heads of 128: 25.8 and 32.8 us; 1030 tokens, 16 +
+  // 2 x 8 of 64: 16.1 and 27.8).
+  PfCut cut{one, 1};
+  if (s > 1 && !(one && tiles * (22 * s - 33) <= 190 * s)) {
+    cut.one = false;
+    cut.split = int(s);
+  }
+  return cut;
 }
 
 }  // namespace bw

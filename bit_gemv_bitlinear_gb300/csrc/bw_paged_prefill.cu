@@ -50,8 +50,6 @@
 namespace bw {
 namespace {
 
-constexpr int kPfTile = 128;       // positions of a key tile
-constexpr int kPfRows = 128;       // rows of a query tile
 constexpr int kPfSoftWarps = 8;    // two warpgroups, one per query tile
 constexpr int kPfMmaWarp = 8;      // and 9: one per query tile
 constexpr int kPfLoadWarp = 10;
@@ -61,9 +59,6 @@ constexpr int kPfThreads = 384;
 constexpr int kPfSoftRegs = 224;
 constexpr int kPfOtherRegs = 56;
 constexpr int kPfScan = 256;       // threads that count items
-constexpr int kPfTargetCtas = 152;  // one CTA per SM
-constexpr int kPfMaxSplit = 16;
-constexpr int kPfMinTiles = 4;      // key tiles of a part, at least
 
 struct PrefillArgs {
   PagedView v;
@@ -1147,37 +1142,6 @@ prefill_join_kernel(const PrefillArgs a) {
         __floats2bfloat162_rn(acc[e] * inv, acc[e + 1] * inv);
 }
 
-// Items of a call without splitting, at most, of `TI` tokens: every sequence
-// may leave one partly filled.
-int64_t max_items(int n_tokens, int n_seqs, int TI, int Hkv) {
-  const int64_t seqs = n_seqs < n_tokens ? n_seqs : n_tokens;
-  return (int64_t(n_tokens) / TI + seqs) * Hkv;
-}
-
-// How a call is cut, by its sizes alone (`see`: the positions that an item's
-// tokens may see, by the page table's width and the window), so that a
-// captured graph serves every length: into items of one query tile or of two,
-// and those into parts of the key axis, at most `split`.
-struct PfCut {
-  bool one;
-  int split;
-};
-PfCut cut_of(int n_tokens, int n_seqs, int G, int Hkv, int64_t see) {
-  const int TQ = kPfRows / G;
-  const int64_t items = max_items(n_tokens, n_seqs, 2 * TQ, Hkv);
-  const bool one = max_items(n_tokens, n_seqs, TQ, Hkv) <= kPfTargetCtas;
-  int64_t s = kPfTargetCtas / items;
-  const int64_t tiles = (see + kPfTile - 1) / kPfTile;
-  if (s > tiles / kPfMinTiles) s = tiles / kPfMinTiles;
-  if (s > kPfMaxSplit) s = kPfMaxSplit;
-  // Parts are not worth it over a short axis where items of one query tile fit:
-  // about 9 + 1.1 tiles us, and 18.5 + 1.65 tiles / s with parts and their join
-  // (2000 tokens, 8 + 2 x 8 heads of 128: 25.8 and 32.8 us; 1030 tokens, 16 +
-  // 2 x 8 of 64: 16.1 and 27.8).
-  if (s <= 1 || (one && tiles * (22 * s - 33) <= 190 * s)) return {one, 1};
-  return {false, int(s)};
-}
-
 template <int D, bool Alone>
 cudaError_t launch_t(const PagedView &v, const PagedAttnLaunch &l,
                      const PfCut &cut, cudaStream_t stream) {
@@ -1238,7 +1202,8 @@ cudaError_t launch_t(const PagedView &v, const PagedAttnLaunch &l,
       !encode_pool(&vmap, v.v, v, D, a.box_rows))
     return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
-  const int64_t items = max_items(l.n_tokens, v.n_seqs, a.TI, v.hkv) * a.split;
+  const int64_t items =
+      prefill_items(l.n_tokens, v.n_seqs, a.TI, v.hkv) * a.split;
   cfg.gridDim = dim3(unsigned(items < resident ? items : resident));
   cfg.blockDim = dim3(kPfThreads);
   cfg.dynamicSmemBytes = PfCfg<D>::kSmem;
@@ -1260,8 +1225,8 @@ cudaError_t launch_t(const PagedView &v, const PagedAttnLaunch &l,
 
 size_t paged_prefill_workspace_bytes(int n_tokens, int n_seqs, int H, int Hkv,
                                      int D) {
-  const int split =
-      cut_of(n_tokens, n_seqs, H / Hkv, Hkv, BW_PAGED_MAX_LEN).split;
+  const int split = prefill_cut(n_tokens, n_seqs, H / Hkv, Hkv,
+                                BW_PAGED_MAX_LEN, kPfMostCtas).split;
   if (split == 1) return 16;
   return size_t(split) * n_tokens * H * (size_t(D) * 4 + 8) + kPagedClaimBytes;
 }
@@ -1269,11 +1234,12 @@ size_t paged_prefill_workspace_bytes(int n_tokens, int n_seqs, int H, int Hkv,
 cudaError_t launch_paged_prefill(const PagedView &v, const PagedAttnLaunch &l,
                                  cudaStream_t stream) {
   const int G = l.H / v.hkv;
-  int64_t see = int64_t(v.max_pages) << v.page_shift;
-  if (l.window > 0)  // (two tiles' edges and the first tokens' one)
-    see = std::min(see,
-                   int64_t(l.window) + l.sinks + 2 * (kPfRows / G) + 3 * kPfTile);
-  const PfCut cut = cut_of(l.n_tokens, v.n_seqs, G, v.hkv, see);
+  const int sms = device_sm_count();
+  if (sms < 1) return cudaErrorInvalidDevice;
+  const int64_t see = prefill_axis(int64_t(v.max_pages) << v.page_shift,
+                                   l.window, l.sinks, G);
+  const PfCut cut = prefill_cut(l.n_tokens, v.n_seqs, G, v.hkv, see,
+                                std::min(sms, kPfMostCtas));
   if (l.D == 64) return launch_t<64, false>(v, l, cut, stream);
   return cut.one ? launch_t<128, true>(v, l, cut, stream)
                  : launch_t<128, false>(v, l, cut, stream);
