@@ -130,3 +130,130 @@ def test_a_query_that_is_not_finite_shows(bw, path, H, Hkv, n, new, window,
     err = (got.double() - want).abs()[keep]
     assert (err <= tol[keep]).all(), float((err - tol[keep]).max())
     assert torch.isfinite(one[0, keep[-1]]).all()
+
+
+# ---------------------------------------------------------------------------
+# random queries
+# ---------------------------------------------------------------------------
+
+LEAD = 3  # rows of no sequence, before and after
+
+RANDOM = [
+    # path, H, Hkv, page, lens, new, window, sinks
+    ("one", 20, 5, 16, [509], [509], 0, 0),
+    ("one", 4, 1, 64, [5000, 90], [60, 90], 300, 4),
+    ("two", 16, 1, 64, [1600, 700], [1300, 300], 0, 0),
+    ("two", 8, 8, 32, [2500, 300], [2400, 290], 0, 0),
+    ("two", 20, 5, 16, [3000], [3000], 0, 0),
+    ("two", 16, 8, 32, [1500, 130, 1400, 0, 1], [1400, 130, 1390, 0, 1], 700, 5),
+    ("two", 6, 2, 64, [4000], [4000], 100, 200),
+    ("two", 7, 1, 128, [3000, 41], [2990, 30], 1, 1),
+    ("parts", 8, 2, 64, [9000, 5000, 70, 0], [40, 90, 70, 0], 0, 0),
+    ("parts", 20, 5, 128, [32801], [200], 0, 0),
+    ("parts", 8, 2, 64, [30000, 20000, 500], [40, 90, 2], 9000, 40),
+    ("parts", 6, 2, 32, [12000], [300], 6000, 300),
+    ("parts", 16, 1, 16, [9000, 4000], [5, 33], 5000, 4),
+]
+
+
+@pytest.mark.parametrize("path,H,Hkv,page,lens,new,window,sinks", RANDOM)
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("peaked", [False, True])
+def test_random_queries(bw, path, H, Hkv, page, lens, new, window, sinks, D,
+                        peaked):
+    """Every row against 64 bits, whatever way the call is cut, and the same
+    twice.  peaked: few keys far above the others, the later the further, so
+    that the maximum follows often and late.  Rows and pages that no token
+    sees hold anything."""
+    c = Cache(151, lens, Hkv, D, page)
+    rng = np.random.default_rng(152)
+    for b, (n, a) in enumerate(zip(lens, new)):
+        if peaked and n:
+            g = np.where(rng.random(n) < 0.02, 6.0 * (np.arange(n) + 50) / n, 0.2)
+            c.k[b] = as_bf16(c.k[b].float().numpy() * g[:, None, None])
+        p = torch.arange(n - a, n)[:, None]
+        j = torch.arange(n)[None, :]
+        vis = ((j <= p) & ((window == 0) | (j > p - window) | (j < sinks))).any(0)
+        ids = torch.from_numpy(c.table[b].astype(np.int64))
+        at, row = ids[torch.arange(n) // page], torch.arange(n) % page
+        k = torch.where(vis[:, None, None], c.k[b], float("nan")).cuda()
+        v = torch.where(vis[:, None, None], c.v[b], float("nan")).cuda()
+        c.kp[at.cuda(), :, row.cuda()] = k
+        c.vp[at.cuda(), :, row.cuda()] = v
+        for i in range(-(-n // page)):
+            if not vis[i * page:(i + 1) * page].any():
+                c.table_d[b, i] = -1
+    tokens = sum(new) + 2 * LEAD
+    start = LEAD + np.concatenate([[0], np.cumsum(new)])
+    q = as_bf16((3.0 if peaked else 1.5) *
+                rng.standard_normal((tokens, H, D))).cuda()
+    st = torch.from_numpy(start.astype(np.int32)).cuda()
+    outs = []
+    for _ in range(2):
+        out = torch.full((tokens, H, D), 9.0, dtype=torch.bfloat16, device="cuda")
+        bw.bw_attn_paged_prefill(q, *c.args, st, window=window, sinks=sinks,
+                                 out=out)
+        assert bw.bw_device_error() == 0
+        outs.append(out)
+    assert torch.equal(*outs)
+    assert (out[:LEAD] == 9.0).all() and (out[tokens - LEAD:] == 9.0).all()
+    for b, (n, a) in enumerate(zip(lens, new)):
+        if a == 0:
+            continue
+        rows = slice(int(start[b]), int(start[b + 1]))
+        want, tol = exact(q[rows], c.k[b], c.v[b], n - a, window, sinks, D ** -0.5)
+        err = (out[rows].double() - want).abs()
+        assert (err <= tol).all(), (b, float((err - tol).max()))
+
+
+# ---------------------------------------------------------------------------
+# a captured call in parts
+# ---------------------------------------------------------------------------
+
+CAPTURED = [
+    # H, Hkv, lens, tokens of the call, window, sinks
+    (8, 2, [9000, 700], 60, 0, 0),
+    (16, 1, [20000, 7000], 20, 8000, 30),
+]
+
+
+@pytest.mark.parametrize("H,Hkv,lens,tokens,window,sinks", CAPTURED)
+@pytest.mark.parametrize("D", [64, 128])
+def test_captured_in_parts(bw, H, Hkv, lens, tokens, window, sinks, D):
+    """Captured once, replayed with other queries, lengths and ranges: as eager
+    calls, bit for bit, and within the bound."""
+    c = Cache(161, lens, Hkv, D, 64)
+    q = torch.zeros((tokens, H, D), dtype=torch.bfloat16, device="cuda")
+    out = torch.zeros_like(q)
+    st = torch.zeros(3, dtype=torch.int32, device="cuda")
+    ws = torch.zeros((bw.bw_attn_paged_prefill_workspace_bytes(
+        tokens, 2, H, Hkv, D),), dtype=torch.uint8, device="cuda")
+    side = torch.cuda.Stream()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(side):
+        with torch.cuda.graph(g, stream=side):
+            bw.bw_attn_paged_prefill(q, *c.args, st, window=window, sinks=sinks,
+                                     out=out, workspace=ws)
+    for step, (n0, cut) in enumerate([(tokens - 4, 0), (tokens - 9, 5003),
+                                      (0, 8990), (3, 300)]):
+        q.copy_(torch.randn(q.shape, device="cuda"))
+        st.copy_(torch.tensor([0, n0, tokens - step]))
+        n = [lens[0] - cut, lens[1]]
+        c.len_d.copy_(torch.tensor(n))
+        out.fill_(9.0)
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        assert bw.bw_device_error() == 0
+        eager = torch.full_like(out, 9.0)
+        bw.bw_attn_paged_prefill(q, *c.args, st, window=window, sinks=sinks,
+                                 out=eager)
+        assert torch.equal(out, eager)
+        assert (out[tokens - step:] == 9.0).all()
+        for b, (lo, hi) in enumerate([(0, n0), (n0, tokens - step)]):
+            if lo == hi:
+                continue
+            want, tol = exact(q[lo:hi], c.k[b][:n[b]], c.v[b][:n[b]],
+                              n[b] - (hi - lo), window, sinks, D ** -0.5)
+            err = (out[lo:hi].double() - want).abs()
+            assert (err <= tol).all(), (step, b, float((err - tol).max()))

@@ -1,6 +1,7 @@
 """Host check of how bw_attn_paged_prefill cuts a call (prefill_cut() in
 bw_paged_plan.cuh, the code that the launch runs), without a GPU: the plan
-over many shapes and device sizes."""
+over many shapes and device sizes, and that the cases of
+test_gpu_paged_paths.py go the way that they name on a device of 152 SMs."""
 import os
 import shutil
 import subprocess
@@ -8,6 +9,9 @@ import subprocess
 import pytest
 
 from conftest import ROOT
+
+pytest.importorskip("torch")
+
 
 @pytest.fixture(scope="module")
 def check(tmp_path_factory):
@@ -30,3 +34,25 @@ def check(tmp_path_factory):
 
 def test_cuts_fit_their_workspace_and_device(check):
     assert check()[0] == "ok"
+
+
+def test_cases_go_the_way_they_name(check):
+    import test_gpu_paged_paths as paths
+
+    def path(n_tokens, n_seqs, H, Hkv, longest, window, sinks):
+        return check(n_tokens, n_seqs, H // Hkv, Hkv, longest, window, sinks,
+                     152)[0]
+
+    def table(lens, page):  # the width that Cache makes
+        return (-(-max(lens) // page) + 1) * page
+
+    for name, H, Hkv, n, new, _ in paths.JUMPS:
+        assert path(new, 1, H, Hkv, table([n], 64), 0, 0) == name, (H, n, new)
+    for name, H, Hkv, n, new, window, sinks in paths.ODD:
+        assert path(new, 1, H, Hkv, table([n], 64), window, sinks) == name
+    for name, H, Hkv, page, lens, new, window, sinks in paths.RANDOM:
+        assert path(sum(new) + 2 * paths.LEAD, len(lens), H, Hkv,
+                    table(lens, page), window, sinks) == name, (H, lens, new)
+    for H, Hkv, lens, tokens, window, sinks in paths.CAPTURED:
+        assert path(tokens, len(lens), H, Hkv, table(lens, 64), window,
+                    sinks) == "parts"
