@@ -1003,7 +1003,9 @@ prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap qmap,
       const int64_t row0 = int64_t(it.row0) + i * TQ;  // of this query tile
       const int h0 = it.g * G;
       const bool direct = a.split == 1 || (it.bad && it.s == 0);
-      const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+      // (A live row sees its own position: a sum of 0 where there were tiles
+      // is one of scores that are all -infinity, whose answer is NaN.)
+      const float inv = n_mine > 0 ? 1.0f / l : 0.0f;
       if (live && a.split > 1)
         a.ml[(int64_t(it.s) * a.n_tokens + row0 + tok) * a.H + h0 + r - tok * G] =
             make_float2(m, l);
@@ -1134,7 +1136,7 @@ prefill_join_kernel(const PrefillArgs a) {
       }
     }
   }
-  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+  const float inv = 1.0f / l;  // a row sees its own position
   __nv_bfloat16 *o = a.out + int64_t(t) * a.out_ld + h * D + lane * kE;
 #pragma unroll
   for (int e = 0; e < kE; e += 2)

@@ -132,6 +132,32 @@ def test_a_query_that_is_not_finite_shows(bw, path, H, Hkv, n, new, window,
     assert torch.isfinite(one[0, keep[-1]]).all()
 
 
+@pytest.mark.parametrize("path,H,Hkv,n,new,window,sinks", ODD)
+@pytest.mark.parametrize("D", [64, 128])
+def test_scores_that_are_all_minus_infinity(bw, path, H, Hkv, n, new, window,
+                                            sinks, D):
+    """An infinite query against keys that are all below 0 there: the softmax of
+    scores that are all -infinity is NaN, in that token's head alone."""
+    c = Cache(143, [n], Hkv, D, 64)
+    c.k[0][:, :, 0] = -1.0
+    c.kp[..., 0] = -1.0
+    rng = np.random.default_rng(144)
+    q = as_bf16(rng.standard_normal((new, H, D))).cuda()
+    st = torch.tensor([0, new], dtype=torch.int32, device="cuda")
+    kw = dict(window=window, sinks=sinks)
+    want, tol = exact(q, c.k[0], c.v[0], n - new, window, sinks, D ** -0.5)
+    q[new - 1, 1, 0] = float("inf")
+    got = bw.bw_attn_paged_prefill(q, *c.args, st, **kw)
+    one = bw.bw_attn_paged_decode(q[-1:], *c.args, **kw)
+    assert bw.bw_device_error() == 0
+    assert torch.isnan(got[new - 1, 1]).all()
+    assert torch.isnan(one[0, 1]).all()
+    keep = torch.ones((new, H), dtype=torch.bool, device="cuda")
+    keep[new - 1, 1] = False
+    err = (got.double() - want).abs()[keep]
+    assert (err <= tol[keep]).all(), float((err - tol[keep]).max())
+
+
 # ---------------------------------------------------------------------------
 # random queries
 # ---------------------------------------------------------------------------
