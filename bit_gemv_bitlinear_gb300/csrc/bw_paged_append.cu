@@ -25,7 +25,7 @@
 // where latency counts.  The row is fetched into L2 as a whole at once (the
 // loads in flight alone are too few to cover the memory's latency), and the
 // first loads go out before the token's position is known.
-// 16381 tokens of 20 + 2 x 5 heads of 128: 49.0 us, 5.1 TB/s of its 252 MB;
+// 16381 tokens of 20 + 2 x 5 heads of 128: 48.6 us, 5.2 TB/s of its 252 MB;
 // without the fetch of whole rows 61.5 us; CTAs of 256 threads at 3 an SM
 // 50.9 us (a CTA leaves when its slowest warp does), persistent CTAs that
 // walk the tokens 66 us (each warp waits out its next token's loads).

@@ -15,10 +15,12 @@
 //  * Work is cut into tiles of 64 positions of one (sequence, head), all tiles
 //    in one order, found on the device from the lengths, so ragged batches
 //    and long single sequences balance alike and one launch serves every step
-//    of a graph.  The first 90 % of a long call are dealt to the CTAs in equal
-//    contiguous shares, the rest in small units that a CTA claims when it is
-//    about to run out: SMs stream at unlike rates (equal shares of 50 us took
-//    42 to 61), and every piece ends in a part to be joined.
+//    of a graph.  A call's tiles are dealt to the CTAs in equal contiguous
+//    shares; in a long one (96 tiles a CTA and more, at most 8 query heads a key
+//    head) only the first 90 % are, and the rest in small units that a CTA
+//    claims when it is about to run out: SMs stream at unlike rates (equal
+//    shares of 50 us took 42 to 61), and every piece ends in a part to be
+//    joined.
 //  * A producer warp looks up the pages and brings a tile's keys and values
 //    into a ring of shared-memory stages with tiled copies (128-byte
 //    swizzle), a lane per box; positions nobody sees are not read.  Next to
@@ -37,7 +39,7 @@
 //    first and waiting for its end, joins them.
 // 64 sequences of up to 8191 positions, 20 + 2 x 5 heads of 128: 107 us, 0.97
 // of the measured copy rate; one of 131071: 55 us, 0.91 (the start and the join
-// are 5 us of it); 120 windows of 1000, 32 + 2 x 4 heads of 64: 31 us, 0.55.
+// are 5 us of it); 120 windows of 1000, 32 + 2 x 4 heads of 64: 31.6 us, 0.54.
 #include <climits>
 
 #include "bw_paged_tc.cuh"
@@ -52,8 +54,9 @@ constexpr int kDcMaxSms = 160;
 // CTAs an SM: a tile takes a CTA's warps about 0.9 us from end to end, so it
 // takes several CTAs to keep up with the copies (the smaller the rows, the
 // more); what their stages and sums leave room for.  120 windows of 1000, 32 +
-// 2 x 4 heads of 64: 31.4 us with 3, 34.0 with 2; 32 sequences of up to 53787,
-// 32 + 2 x 2 heads: 100 with 3 (of 3 stages), 111 with 2 (of 4 or 5).
+// 2 x 4 heads of 64: 31.4 us with 3, 34.0 with 2; 32 sequences of 18310 to
+// 53787 (590 MB), 32 + 2 x 2 heads: 100 with 3 (of 3 stages), 111 with 2 (of 4 or
+// 5).
 __host__ __device__ constexpr int dc_ctas(int D) { return D == 64 ? 3 : 2; }
 // Shares and claimed units, at most.
 __host__ __device__ constexpr int dc_max_units(int D) {
@@ -181,8 +184,6 @@ struct Item {
   int64_t first;  // first tile of the item
 };
 
-// Both return false past the last sequence, which only lengths that change
-// under the call can bring about.
 // Where the sequences begin, for one warp: entry t = 32 k + lane is the first
 // tile of sequences t per and on, and the first one's length.
 struct Begins {
@@ -191,7 +192,8 @@ struct Begins {
   int len0[kPer];
   int per;
 };
-// The item of tile `at` (by a whole warp).
+// The item of tile `at` (by a whole warp).  Like item_next, false past the last
+// sequence, which only lengths that change under the call can bring about.
 __device__ __forceinline__ bool item_at(const DecodeArgs &a, const Begins &bg,
                                         int64_t at, Item &it) {
   int n = 0;

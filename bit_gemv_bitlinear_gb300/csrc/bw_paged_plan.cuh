@@ -141,7 +141,12 @@ BW_PLAN_FN PfCut prefill_cut(int n_tokens, int n_seqs, int G, int Hkv,
   // Parts are not worth it over a short axis where items of one query tile fit:
   // about 9 + 1.1 tiles us, and 18.5 + 1.65 tiles / s with parts and their join
   // (2000 tokens, 8 + 2 x 8 heads of 128: 25.8 and 32.8 us; 1030 tokens, 16 +
-  // 2 x 8 of 64: 16.1 and 27.8).
+  // 2 x 8 of 64: 16.1 and 27.8).  The rates are those of 128 dims.
+  // The axis is the longest that the table allows, so a short prompt in a wide
+  // table is cut for more than it has.  us with a table as wide as the prompt
+  // and with one of 32768 positions: 128 tokens, 20 + 2 x 5 heads of 128: 9.6
+  // and 18.1; 509 tokens 13.5 and 24.8 (from 2177 positions on); 1030 tokens
+  // 21.4 and 21.2; 509 tokens, 16 + 2 x 8 of 64: 10.5 and 19.7.
   PfCut cut{one, 1};
   if (s > 1 && !(one && tiles * (22 * s - 33) <= 190 * s)) {
     cut.one = false;

@@ -36,10 +36,11 @@
 //  * Where there are too few tiles for the device, a CTA takes one query tile,
 //    or, over a long axis, the key axis is cut too: the parts' o and (m, l)
 //    go to the workspace and a second kernel joins them, a warp per row.
-// 8192 tokens, 20 + 2 x 5 heads of 128: 217 us, 1580 TFLOP/s of the visible
-// pairs, 0.82 of the rate of a large cuBLAS product here; the tensor pipe is
-// busy 69 % of the time, the rest is the softmax's latency around it (a pair of
-// query tiles takes 3040 cycles a key tile, 2530 of them products).  64 dims:
+// 8192 tokens, 20 + 2 x 5 heads of 128: 217 us in short runs, 234 us at the
+// clocks that the power limit leaves; 1580 and 1470 TFLOP/s of the visible
+// pairs, 0.82 and 0.77 of the burst rate of a large cuBLAS product.  The tensor
+// pipe is busy 69 % of the time, the rest is the softmax's latency around it (a
+// pair of query tiles takes 3040 cycles a key tile, 2530 of them products).  64 dims:
 // 2480 cycles, bound by the softmax's chain.  A window's masked tiles and the
 // ends of its short items (2900 tokens, window 700: seven tiles) cost half as
 // much again.
@@ -345,7 +346,8 @@ __device__ __forceinline__ PfWork pf_work(const PrefillArgs &a, const PfItem &it
 // Alone (128 dims): items of one query tile.  Nothing else fills the time
 // between its products, so the next scores are made during its softmax, in the
 // other tile's columns, the two in turn (a prompt of 509 tokens, 20 + 2 x 5
-// heads: 15.2 us, 16.0 without, 17.4 with items of two query tiles).
+// heads, in a table of no more positions: 15.2 us, 16.0 without, 17.4 with items
+// of two query tiles).
 template <int D, bool Alone>
 __global__ void __launch_bounds__(kPfThreads, 1)
 prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap qmap,

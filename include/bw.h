@@ -584,7 +584,9 @@ bw_status bw_qk_norm_rope_append(const bw_bf16 *qkv, int64_t qkv_ld,
  * must be in the pages already (bw_qk_norm_rope_append).
  * Pages that hold no visible position are not read; rows of the others that
  * are not visible may hold anything (NaN included).  Scores, softmax and
- * sums are fp32, and the fp32 output keeps fp32 precision.
+ * sums are fp32, and the fp32 output keeps fp32 precision.  A visible score
+ * that is NaN or +infinity, scores that are all -infinity, and a visible value
+ * that is not finite give NaN in the heads that they belong to.
  *   q         bf16 [n_seqs][q_ld] device, 16-byte aligned: H rotated heads of
  *             D; q_ld a multiple of 8, at least H D.
  *   out       fp32 or (out_bf16 nonzero) bf16 [n_seqs][out_ld] device,
@@ -618,13 +620,18 @@ bw_status bw_attn_paged_decode(const bw_bf16 *q, int64_t q_ld, int H,
  * Products run on the tensor cores with fp32 accumulation; the exp weights
  * are rounded to bf16, like the output.  What a position that some new token
  * of its sequence sees holds must be finite; others may hold anything.  A
- * query that is not finite, or whose scores leave fp32's range, gives NaN in
- * its own row and head alone.
+ * visible score that is NaN or +infinity, by its query or beyond fp32's range,
+ * and scores that are all -infinity give NaN in that row and head alone.
  *   q         bf16 [n_tokens][q_ld] device, out bf16 [n_tokens][out_ld]
  *             device: 16-byte aligned, both strides multiples of 8, at least
  *             H D and below 2^31; out must not overlap q.
  *   q_start   as above (required).
  *   scale, window, sinks, H  as for bw_attn_paged_decode.
+ *   max_pages  the work is cut by the call's sizes: for the longest sequence
+ *             that the table (or the window) allows.  Short prompts are faster
+ *             with a table no wider than their longest sequence (509 tokens,
+ *             20 + 2 x 5 heads of 128: 13.5 us, and 25 in one of 32768
+ *             positions); a captured graph keeps the width it was made with.
  *   workspace as above, bw_attn_paged_prefill_workspace_bytes(n_tokens,
  *             n_seqs, H, Hkv, D) bytes; on its own it needs no zeroing (only
  *             the first 256 bytes' counter has to be zero, for decode). */
