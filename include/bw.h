@@ -634,7 +634,9 @@ bw_status bw_attn_paged_decode(const bw_bf16 *q, int64_t q_ld, int H,
  *             positions); a captured graph keeps the width it was made with.
  *   workspace as above, bw_attn_paged_prefill_workspace_bytes(n_tokens,
  *             n_seqs, H, Hkv, D) bytes; on its own it needs no zeroing (only
- *             the first 256 bytes' counter has to be zero, for decode). */
+ *             the first 256 bytes' counter has to be zero, for decode).  Few
+ *             tokens may need more than many; 20 MiB are enough for every
+ *             prefill call and for every decode call. */
 size_t bw_attn_paged_prefill_workspace_bytes(int n_tokens, int n_seqs, int H,
                                              int Hkv, int D);
 bw_status bw_attn_paged_prefill(const bw_bf16 *q, int64_t q_ld, int n_tokens,

@@ -56,3 +56,26 @@ def test_cases_go_the_way_they_name(check):
     for H, Hkv, lens, tokens, window, sinks in paths.CAPTURED:
         assert path(tokens, len(lens), H, Hkv, table(lens, 64), window,
                     sinks) == "parts"
+
+
+def test_20_mib_are_enough_for_every_call():
+    import ctypes
+
+    from conftest import build_lib
+    lib = ctypes.CDLL(build_lib())
+    decode, prefill = (lib.bw_attn_paged_decode_workspace_bytes,
+                       lib.bw_attn_paged_prefill_workspace_bytes)
+    decode.restype = prefill.restype = ctypes.c_size_t
+    most = 0
+    for D in (64, 128):
+        for Hkv in (1, 2, 3, 5, 8, 19, 38, 64):
+            for G in range(1, 17):
+                most = max(most, decode(4096, G * Hkv, Hkv, D))
+                TQ2 = 2 * (128 // G)
+                for k in (1, 2, 3, 5, 10, 19, 38, 50, 76, 152, 500):
+                    for n in (k * TQ2 - 1, k * TQ2):
+                        for seqs in (1, 2, 7, 4096):
+                            need = prefill(n, seqs, G * Hkv, Hkv, D)
+                            assert need > 0
+                            most = max(most, need)
+    assert most <= 20 << 20, most
