@@ -1,8 +1,8 @@
 // bw_paged_plan.cuh -- which cache positions the tokens of a paged-attention
 // call see, in which tiles they are visited, how a decode call's tiles are
-// dealt to its CTAs, and how a prefill call is cut into items.  Integer arithmetic only, on the host and on the device,
-// and plain C++ as well, so that a host program can check every plan without a
-// GPU.
+// dealt to its CTAs, and how a prefill call is cut into items.  Integer
+// arithmetic only, on the host and on the device, and plain C++ as well, so
+// that a host program can check every plan without a GPU.
 //
 // Source: "BitNet GPU 推理框架：从零构建 W2A8 的 2-bit 大模型 CUDA GEMV 内核",
 // §六 item 2 (a preallocated KV cache, the position read on the device).

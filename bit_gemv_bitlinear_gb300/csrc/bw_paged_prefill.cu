@@ -40,10 +40,10 @@
 // clocks that the power limit leaves; 1580 and 1470 TFLOP/s of the visible
 // pairs, 0.82 and 0.77 of the burst rate of a large cuBLAS product.  The tensor
 // pipe is busy 69 % of the time, the rest is the softmax's latency around it (a
-// pair of query tiles takes 3040 cycles a key tile, 2530 of them products).  64 dims:
-// 2480 cycles, bound by the softmax's chain.  A window's masked tiles and the
-// ends of its short items (2900 tokens, window 700: seven tiles) cost half as
-// much again.
+// pair of query tiles takes 3040 cycles a key tile, 2530 of them products).
+// 64 dims: 2480 cycles, bound by the softmax's chain.  A window's masked tiles
+// and the ends of its short items (2900 tokens, window 700: seven tiles) cost
+// half as much again.
 #include <algorithm>
 
 #include "bw_paged_tc.cuh"
@@ -385,7 +385,8 @@ prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap qmap,
   // Ranges that run backwards let others overlap, and the items of 4096
   // sequences that all hold every row would go on for hours: no items then.
   bool void_call;
-  SeqTokens kept{0, 0, 0, false, false};  // few sequences, the scheduler: one a lane
+  // (few sequences, the scheduler: one a lane)
+  SeqTokens kept{0, 0, 0, false, false};
   {
     const int b_lo = tid < kPfScan ? min(tid * per, a.v.n_seqs) : a.v.n_seqs;
     const int b_hi = min(b_lo + per, a.v.n_seqs);

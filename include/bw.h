@@ -585,8 +585,8 @@ bw_status bw_qk_norm_rope_append(const bw_bf16 *qkv, int64_t qkv_ld,
  * Pages that hold no visible position are not read; rows of the others that
  * are not visible may hold anything (NaN included).  Scores, softmax and
  * sums are fp32, and the fp32 output keeps fp32 precision.  A visible score
- * that is NaN or +infinity, scores that are all -infinity, and a visible value
- * that is not finite give NaN in the heads that they belong to.
+ * that is NaN or +infinity and scores that are all -infinity give NaN in that
+ * head, a visible value that is not finite NaN or an infinity in its dim.
  *   q         bf16 [n_seqs][q_ld] device, 16-byte aligned: H rotated heads of
  *             D; q_ld a multiple of 8, at least H D.
  *   out       fp32 or (out_bf16 nonzero) bf16 [n_seqs][out_ld] device,

@@ -158,6 +158,30 @@ def test_scores_that_are_all_minus_infinity(bw, path, H, Hkv, n, new, window,
     assert (err <= tol[keep]).all(), float((err - tol[keep]).max())
 
 
+@pytest.mark.parametrize("lens", [[300], [5000, 70]])
+@pytest.mark.parametrize("H,Hkv,D", [(4, 2, 128), (12, 1, 64)])
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("odd", [float("nan"), float("inf"), float("-inf")])
+def test_decode_of_a_value_that_is_not_finite(bw, lens, H, Hkv, D, bf16, odd):
+    """Not finite in its dim, whatever its weight; the other dims as ever."""
+    c = Cache(145, lens, Hkv, D, 64)
+    at, dim = 130, 5
+    c.vp[int(c.table[0, at // 64]), 0, at % 64, dim] = odd
+    q = as_bf16(np.random.default_rng(146).standard_normal(
+        (len(lens), H, D))).cuda()
+    out = torch.full(q.shape, 9.0, device="cuda",
+                     dtype=torch.bfloat16 if bf16 else torch.float32)
+    bw.bw_attn_paged_decode(q, *c.args, out=out)
+    assert bw.bw_device_error() == 0
+    assert not torch.isfinite(out[0, :H // Hkv, dim]).any()
+    for b, n in enumerate(lens):
+        want, tol = exact(q[b:b + 1], c.k[b], c.v[b], n - 1, 0, 0, D ** -0.5)
+        ok = (out[b].double() - want[0]).abs() <= tol[0]
+        if b == 0:
+            ok[:H // Hkv, dim] = True
+        assert ok.all()
+
+
 # ---------------------------------------------------------------------------
 # random queries
 # ---------------------------------------------------------------------------
