@@ -10,7 +10,8 @@ Function names follow the C ABI: ``bw_quant_act``, ``bw_repack``,
 ``bw_unrepack``, ``bw_gemv_w2a8``, ``bw_gemv_w2a8_acc``, ``bw_gemm_w2a8``,
 ``bw_gemm_w2a8_acc``, ``bw_attn_decode``, ``bw_attn_decode_ex``,
 ``bw_qk_norm_rope_append``, ``bw_attn_paged_decode``,
-``bw_attn_paged_prefill``.
+``bw_attn_paged_prefill``, ``bw_add_rms_norm_quant``,
+``bw_relu2_rms_norm_quant``, ``bw_lora_add``, ``bw_attn_paged_shared``.
 """
 from __future__ import annotations
 
@@ -51,7 +52,10 @@ EXPORTS = ("bw_status_string", "bw_last_cuda_error", "bw_version",
            "bw_gemv_w2a8_lut_acc", "bw_gemm_workspace_bytes", "bw_gemm_w2a8",
            "bw_gemm_w2a8_acc", "bw_qk_norm_rope_append",
            "bw_attn_paged_decode_workspace_bytes", "bw_attn_paged_decode",
-           "bw_attn_paged_prefill_workspace_bytes", "bw_attn_paged_prefill")
+           "bw_attn_paged_prefill_workspace_bytes", "bw_attn_paged_prefill",
+           "bw_add_rms_norm_quant", "bw_relu2_rms_norm_quant",
+           "bw_lora_workspace_bytes", "bw_lora_add",
+           "bw_attn_paged_shared_workspace_bytes", "bw_attn_paged_shared")
 
 _P = ctypes.c_void_p
 _I = ctypes.c_int
@@ -100,6 +104,14 @@ _SIGS = {
     "bw_attn_paged_prefill_workspace_bytes": (_Z, [_I] * 5),
     "bw_attn_paged_prefill": (_I, [_P, _L, _I, _P, _I, _P, _F, _I, _I, _P,
                                    _L, _P, _Z, _P]),
+    "bw_attn_paged_shared_workspace_bytes": (_Z, [_I] * 4),
+    "bw_attn_paged_shared": (_I, [_P, _L, _I, _P, _P, _I, _P, _F, _P, _L, _P,
+                                  _Z, _P]),
+    "bw_add_rms_norm_quant": (_I, [_P, _I, _L, _P, _P, _P, _F, _I, _I, _P, _P,
+                                   _P]),
+    "bw_relu2_rms_norm_quant": (_I, [_P, _L, _P, _F, _I, _I, _P, _P, _P]),
+    "bw_lora_workspace_bytes": (_Z, [_I, _I]),
+    "bw_lora_add": (_I, [_P] * 6 + [_I] * 5 + [_P, _L, _P, _L, _P, _Z, _P]),
 }
 for _name, (_res, _args) in _SIGS.items():
     _fn = getattr(_lib, _name)
@@ -715,6 +727,194 @@ def bw_attn_paged_prefill(q: torch.Tensor, k_pages: torch.Tensor,
             window, sinks, o, out_ld,
             _vector(workspace, torch.uint8, dev, 0, "workspace"),
             workspace.numel(), s), "bw_attn_paged_prefill")
+    return out
+
+
+def bw_attn_paged_shared_workspace_bytes(n_seqs: int, H: int, Hkv: int,
+                                         D: int) -> int:
+    """Device scratch bw_attn_paged_shared needs (0: unsupported)."""
+    return int(_lib.bw_attn_paged_shared_workspace_bytes(n_seqs, H, Hkv, D))
+
+
+def bw_attn_paged_shared(q: torch.Tensor, k_pages: torch.Tensor,
+                         v_pages: torch.Tensor, page_table: torch.Tensor,
+                         kv_len: torch.Tensor, shared_table: torch.Tensor,
+                         shared_len: torch.Tensor, scale: float | None = None,
+                         out: torch.Tensor | None = None,
+                         workspace: torch.Tensor | None = None,
+                         stream=None) -> torch.Tensor:
+    """bw_attn_paged_decode for a batch that shares a prefix: the first
+    shared_len[0] positions (int32 device tensor of one) of every sequence lie
+    in the pages of shared_table (int32, one row), which are read once for all;
+    later ones in page_table's.  bf16 q [n_seqs][H][D] -> bf16 out
+    [n_seqs][H][D].  scale and workspace as for bw_attn_paged_decode
+    (bw_attn_paged_shared_workspace_bytes)."""
+    kv, dev, n, hkv, D = _paged_kv(k_pages, v_pages, page_table, kv_len)
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        _refuse(q, (_BF16,), dev, "q must be [n_seqs][H][D]")
+    H = q.shape[1]
+    ptr, ld = _rows(q, (_BF16,), dev, n, H, D, "q")
+    table = _vector(shared_table, _I32, dev, 1, "shared_table")
+    length = _vector(shared_len, _I32, dev, 1, "shared_len")
+    context, s = _where(dev, stream)
+    with context:
+        if out is None:
+            out = torch.empty((n, H, D), dtype=_BF16, device=q.device)
+        if workspace is None:
+            workspace = torch.zeros((max(16, bw_attn_paged_shared_workspace_bytes(
+                n, H, hkv, D)),), dtype=torch.uint8, device=q.device)
+        o, out_ld = _rows(out, (_BF16,), dev, n, H, D, "out")
+        _check(_lib.bw_attn_paged_shared(
+            ptr, ld, H, kv, table, shared_table.numel(), length,
+            1.0 / D ** 0.5 if scale is None else scale, o, out_ld,
+            _vector(workspace, torch.uint8, dev, 0, "workspace"),
+            workspace.numel(), s), "bw_attn_paged_shared")
+    return out
+
+
+_I8 = torch.int8
+
+
+def _row_view(t, dtypes, dev: int, rows: int, width: int, name: str):
+    """(pointer, row stride) of [rows][width] with contiguous rows."""
+    try:
+        if t.dtype in dtypes and t.get_device() == dev and \
+                t.shape == (rows, width):
+            st = t.stride()
+            if st[1] == 1 or width == 1:
+                return t.data_ptr(), (st[0] if rows > 1 else width)
+    except AttributeError:
+        pass
+    _refuse(t, dtypes, dev, f"{name} must be [{rows}][{width}] with "
+            "contiguous rows")
+
+
+def _whole(t, dtype, dev: int, shape, name: str) -> int:
+    """Pointer of a contiguous tensor of this shape."""
+    try:
+        if t.dtype is dtype and t.get_device() == dev and t.shape == shape and \
+                t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _refuse(t, (dtype,), dev, f"{name} must be a contiguous "
+            + "".join(f"[{n}]" for n in shape))
+
+
+def _codes(q, s, dev: int, M: int, K: int, like):
+    """The outputs q [M][K] and s [M], made where they are not given."""
+    if q is None:
+        q = torch.empty((M, K), dtype=_I8, device=like.device)
+    if s is None:
+        s = torch.empty((M,), dtype=_F32, device=like.device)
+    return q, s, _whole(q, _I8, dev, (M, K), "q"), _whole(s, _F32, dev, (M,), "s")
+
+
+def bw_add_rms_norm_quant(x: torch.Tensor, gamma: torch.Tensor,
+                          h: torch.Tensor | None = None, eps: float = 1e-5,
+                          h_out: torch.Tensor | None = None,
+                          q: torch.Tensor | None = None,
+                          s: torch.Tensor | None = None, stream=None):
+    """The residual's addition, the RMS norm and the next projection's codes in
+    one pass: bf16 or fp32 x [M][K] (rows may be strided), fp32 h [M][K] or
+    None -> (int8 q [M][K], fp32 s [M]) of (h + x) / rms * gamma, as
+    bw_quant_act's.  h + x goes to h_out (h itself if None)."""
+    try:
+        (M, K), dev = x.shape, x.get_device()
+        ok = dev >= 0
+    except (AttributeError, ValueError):
+        ok = False
+    if not ok:
+        _refuse(x, (_BF16, _F32), -1, "x must be [M][K]")
+    ptr, ld = _row_view(x, (_BF16, _F32), dev, M, K, "x")
+    g = _whole(gamma, _F32, dev, (K,), "gamma")
+    hp = ho = None
+    if h is not None:
+        hp = ho = _whole(h, _F32, dev, (M, K), "h")
+        if h_out is not None:
+            ho = _whole(h_out, _F32, dev, (M, K), "h_out")
+    elif h_out is not None:
+        raise ValueError("h_out without h")
+    context, st = _where(dev, stream)
+    with context:
+        q, s, qp, sp = _codes(q, s, dev, M, K, x)
+        _check(_lib.bw_add_rms_norm_quant(ptr, x.dtype is _BF16, ld, hp, ho, g,
+                                          eps, M, K, qp, sp, st),
+               "bw_add_rms_norm_quant")
+    return q, s
+
+
+def bw_relu2_rms_norm_quant(gu: torch.Tensor, gamma: torch.Tensor,
+                            eps: float = 1e-5, q: torch.Tensor | None = None,
+                            s: torch.Tensor | None = None, stream=None):
+    """The down projection's input from the fused gate|up projection's output:
+    bf16 gu [M][2 F] (rows may be strided) -> (int8 q [M][F], fp32 s [M]) of
+    relu(gate)^2 up / rms * gamma."""
+    try:
+        (M, width), dev = gu.shape, gu.get_device()
+        ok = dev >= 0 and width % 2 == 0
+    except (AttributeError, ValueError):
+        ok = False
+    if not ok:
+        _refuse(gu, (_BF16,), -1, "gu must be [M][2 F]")
+    F = width // 2
+    ptr, ld = _row_view(gu, (_BF16,), dev, M, width, "gu")
+    g = _whole(gamma, _F32, dev, (F,), "gamma")
+    context, st = _where(dev, stream)
+    with context:
+        q, s, qp, sp = _codes(q, s, dev, M, F, gu)
+        _check(_lib.bw_relu2_rms_norm_quant(ptr, ld, g, eps, M, F, qp, sp, st),
+               "bw_relu2_rms_norm_quant")
+    return q, s
+
+
+def bw_lora_workspace_bytes(M: int, R: int) -> int:
+    """Device scratch bw_lora_add needs (0: unsupported)."""
+    return int(_lib.bw_lora_workspace_bytes(M, R))
+
+
+def bw_lora_add(y: torch.Tensor, x: torch.Tensor, s: torch.Tensor,
+                A: torch.Tensor, B: torch.Tensor, adapter: torch.Tensor,
+                scale: torch.Tensor | None = None,
+                out: torch.Tensor | None = None,
+                workspace: torch.Tensor | None = None,
+                stream=None) -> torch.Tensor:
+    """Adds every row's own low-rank adapter to a projection's output: bf16 y
+    [M][N] (rows may be strided) of int8 x [M][K] with scales s [M]; bf16 A
+    [n][R][K] and B [n][N][R], fp32 scale [n] or None, int32 adapter [M] (-1:
+    none).  out: a tensor like y, y itself if None.  `workspace`: a uint8
+    device tensor of at least bw_lora_workspace_bytes(M, R) bytes, made for
+    this call if omitted."""
+    try:
+        dev = y.get_device()
+        (M, N), (n, R, K) = y.shape, A.shape
+        ok = dev >= 0
+    except (AttributeError, ValueError):
+        ok = False
+    if not ok:
+        if not isinstance(y, torch.Tensor) or not y.is_cuda or y.dim() != 2:
+            _refuse(y, (_BF16,), -1, "y must be [M][N]")
+        _refuse(A, (_BF16,), dev, "A must be [n_adapters][R][K]")
+    yp, y_ld = _row_view(y, (_BF16,), dev, M, N, "y")
+    Ap = _whole(A, _BF16, dev, (n, R, K), "A")
+    Bp = _whole(B, _BF16, dev, (n, N, R), "B")
+    xp = _whole(x, _I8, dev, (M, K), "x")
+    sp = _whole(s, _F32, dev, (M,), "s")
+    ap = _whole(adapter, _I32, dev, (M,), "adapter")
+    cp = None if scale is None else _whole(scale, _F32, dev, (n,), "scale")
+    if out is None:
+        out, op, out_ld = y, yp, y_ld
+    else:
+        op, out_ld = _row_view(out, (_BF16,), dev, M, N, "out")
+    context, st = _where(dev, stream)
+    with context:
+        if workspace is None:
+            workspace = torch.empty((max(16, bw_lora_workspace_bytes(M, R)),),
+                                    dtype=torch.uint8, device=y.device)
+        _check(_lib.bw_lora_add(
+            xp, sp, Ap, Bp, cp, ap, n, M, N, K, R, yp, y_ld, op, out_ld,
+            _vector(workspace, torch.uint8, dev, 0, "workspace"),
+            workspace.numel(), st), "bw_lora_add")
     return out
 
 

@@ -341,7 +341,8 @@ bw_status bw_device_error(unsigned int *bits, bw_stream_t stream) {
   cudaError_t e =
       read_device_error(reinterpret_cast<cudaStream_t>(stream), bits);
   if (e != cudaSuccess) return cuda_status(e);
-  if (*bits & ~(16u | 128u | 256u)) return BW_ERR_TIMEOUT;  // the caller's: 16, 128, 256
+  // the caller's: 16, 128, 256, 512
+  if (*bits & ~(16u | 128u | 256u | 512u)) return BW_ERR_TIMEOUT;
   return *bits ? BW_ERR_INVALID_ARG : BW_OK;
 }
 

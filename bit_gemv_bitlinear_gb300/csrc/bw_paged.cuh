@@ -126,6 +126,9 @@ struct PagedAttnLaunch {
   int64_t out_ld;
   int out_bf16;
   void *workspace;
+  // decode behind a shared prefix: its length (device), the pages it may have
+  const int *shared_len;
+  int shared_pages;
 };
 // The attention calls' workspaces begin with decode's counter of claimed units
 // and its mark of the first claim, zero between calls; prefill leaves them

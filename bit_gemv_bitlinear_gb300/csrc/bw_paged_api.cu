@@ -6,7 +6,7 @@
 // §六 item 2 (a preallocated KV cache), §一 (grouped key-value heads).
 #include <cmath>
 
-#include "bw_paged.cuh"
+#include "bw_paged_shared.cuh"
 
 namespace bw {
 namespace {
@@ -235,6 +235,57 @@ bw_status bw_attn_paged_prefill(const bw_bf16 *q, int64_t q_ld, int n_tokens,
   l.workspace = workspace;
   return finish(
       launch_paged_prefill(v, l, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t bw_attn_paged_shared_workspace_bytes(int n_seqs, int H, int Hkv,
+                                            int D) {
+  if (n_seqs < 1 || n_seqs > BW_PAGED_MAX_SEQS ||
+      check_shape(H, Hkv, D) != BW_OK)
+    return 0;
+  return paged_shared_workspace_bytes(n_seqs, H, Hkv, D);
+}
+
+bw_status bw_attn_paged_shared(const bw_bf16 *q, int64_t q_ld, int H,
+                               const bw_paged_kv *kv, const int *shared_table,
+                               int n_shared_pages, const int *shared_len,
+                               float scale, bw_bf16 *out, int64_t out_ld,
+                               void *workspace, size_t workspace_bytes,
+                               bw_stream_t stream) {
+  bw_status st = check_kv(kv, H);
+  if (st != BW_OK) return st;
+  if (!shared_table || !shared_len || n_shared_pages < 1)
+    return BW_ERR_INVALID_ARG;
+  if (int64_t(n_shared_pages) * kv->page_size > BW_PAGED_MAX_LEN)
+    return BW_ERR_UNSUPPORTED_SHAPE;
+  if (!aligned(shared_table, 4) || !aligned(shared_len, 4))
+    return BW_ERR_MISALIGNED;
+  const int64_t need = int64_t(H) * kv->head_dim;
+  st = check_rows(q, q_ld, need);
+  if (st != BW_OK) return st;
+  st = check_rows(out, out_ld, need);
+  if (st != BW_OK) return st;
+  if (out == q) return BW_ERR_INVALID_ARG;
+  st = check_attn_args(scale, 0, 0, workspace, workspace_bytes,
+                       paged_shared_workspace_bytes(
+                           kv->n_seqs, H, kv->n_kv_heads, kv->head_dim));
+  if (st != BW_OK) return st;
+  const PagedView v = paged_view(*kv);
+  if (!v.err) return finish(cudaErrorInvalidSymbol);
+  PagedAttnLaunch l{};
+  l.q = reinterpret_cast<const __nv_bfloat16 *>(q);
+  l.q_ld = q_ld;
+  l.n_tokens = kv->n_seqs;
+  l.H = H;
+  l.D = kv->head_dim;
+  l.scale = scale;
+  l.out = out;
+  l.out_ld = out_ld;
+  l.out_bf16 = 1;
+  l.workspace = workspace;
+  l.shared_len = shared_len;
+  l.shared_pages = n_shared_pages;
+  return finish(launch_paged_shared(v, l, shared_table,
+                                    reinterpret_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -42,6 +42,7 @@
 // are 5 us of it); 120 windows of 1000, 32 + 2 x 4 heads of 64: 31.6 us, 0.54.
 #include <climits>
 
+#include "bw_paged_shared.cuh"
 #include "bw_paged_tc.cuh"
 
 namespace bw {
@@ -50,29 +51,13 @@ namespace {
 constexpr int kDcWarps = 4;                      // consumers
 constexpr int kDcThreads = (kDcWarps + 1) * 32;  // and the producer
 constexpr int kDcTile = 64;
-constexpr int kDcMaxSms = 160;
 // CTAs an SM: a tile takes a CTA's warps about 0.9 us from end to end, so it
 // takes several CTAs to keep up with the copies (the smaller the rows, the
 // more); what their stages and sums leave room for.  120 windows of 1000, 32 +
 // 2 x 4 heads of 64: 31.4 us with 3, 34.0 with 2; 32 sequences of 18310 to
 // 53787 (590 MB), 32 + 2 x 2 heads: 100 with 3 (of 3 stages), 111 with 2 (of 4 or
 // 5).
-__host__ __device__ constexpr int dc_ctas(int D) { return D == 64 ? 3 : 2; }
-// Shares and claimed units, at most.
-__host__ __device__ constexpr int dc_max_units(int D) {
-  return 3 * dc_ctas(D) * kDcMaxSms;
-}
-
-// A counter that was not zero when a call began loses units.  Nobody gets the
-// first one then (or a claim is above all units), and that is reported.
-constexpr unsigned int kDcFirst = 0x706b7631u;
-
-// What the workspace keeps of a (sequence, head): its parts are those of units
-// unit0 .. unit0 + parts - 1 (parts 1: the output is written already, 0: zeros
-// are).
-struct DcParts {
-  int unit0, parts;
-};
+// (dc_ctas: bw_paged_shared.cuh)
 
 struct DecodeArgs {
   PagedView v;
@@ -80,7 +65,7 @@ struct DecodeArgs {
   int64_t q_ld;
   void *out;
   int64_t out_ld;
-  float *part;          // [2 dc_max_units][part_floats(G, D)]
+  float *part;          // [slots][part_floats(G, D)]
   DcParts *parts;       // [n_seqs][Hkv]
   // units claimed so far, and kDcFirst once the first of them is; both zero
   // between calls
@@ -89,6 +74,14 @@ struct DecodeArgs {
   float scale2;         // scale log2(e)
   int window, sinks;
   int box_rows;
+  const int *shared_len;  // positions that are not visited here; or null
+  int shared_pages;
+  // (the view that their number is checked against)
+  __device__ PagedView shared_v() const {
+    PagedView s = v;
+    s.max_pages = shared_pages;
+    return s;
+  }
 };
 
 // A tile as the producer leaves it next to its stage.
@@ -172,7 +165,14 @@ __device__ __forceinline__ uint32_t take_bf16(float &a, float &b) {
 }
 
 // The tiles of sequence b per key-value head, and its plan.
-__device__ __forceinline__ TilePlan seq_plan(int len, int window, int sinks) {
+// (shared >= 0: those from position `shared` on alone, of no window)
+__device__ __forceinline__ TilePlan seq_plan(int len, int window, int sinks,
+                                             int shared) {
+  if (shared >= 0) {
+    if (len <= shared) return TilePlan{};
+    const int w0 = shared / kDcTile;
+    return TilePlan{(len - 1) / kDcTile + 1 - w0, 0, w0, 0, shared};
+  }
   if (len <= 0) return TilePlan{};
   return tile_plan(len - 1, len - 1, window, sinks, kDcTile);
 }
@@ -195,7 +195,7 @@ struct Begins {
 // The item of tile `at` (by a whole warp).  Like item_next, false past the last
 // sequence, which only lengths that change under the call can bring about.
 __device__ __forceinline__ bool item_at(const DecodeArgs &a, const Begins &bg,
-                                        int64_t at, Item &it) {
+                                        int64_t at, int shared, Item &it) {
   int n = 0;
 #pragma unroll
   for (int k = 0; k < Begins::kPer; ++k)
@@ -211,7 +211,7 @@ __device__ __forceinline__ bool item_at(const DecodeArgs &a, const Begins &bg,
     }
   for (it.b = b0; it.b < a.v.n_seqs; ++it.b) {
     it.len = it.b == b0 ? len : seq_len(a.v, it.b);
-    it.plan = seq_plan(it.len, a.window, a.sinks);
+    it.plan = seq_plan(it.len, a.window, a.sinks, shared);
     const int64_t tiles = int64_t(it.plan.n) * a.v.hkv;
     if (at < base + tiles) {
       it.g = int(at - base) / it.plan.n;  // below 2^24
@@ -222,24 +222,24 @@ __device__ __forceinline__ bool item_at(const DecodeArgs &a, const Begins &bg,
   }
   return false;
 }
-__device__ __forceinline__ bool item_next(const DecodeArgs &a, Item &it) {
+__device__ __forceinline__ bool item_next(const DecodeArgs &a, int shared,
+                                          Item &it) {
   it.first += it.plan.n;
   if (++it.g < a.v.hkv) return true;
   it.g = 0;
   for (++it.b; it.b < a.v.n_seqs; ++it.b) {
     it.len = seq_len(a.v, it.b);
-    it.plan = seq_plan(it.len, a.window, a.sinks);
+    it.plan = seq_plan(it.len, a.window, a.sinks, shared);
     if (it.plan.n > 0) return true;
   }
   return false;
 }
-// Floats of a part in the workspace: o [G][D], then (m, l) [G], padded so that
-// every part is 16-byte aligned.
-__host__ __device__ constexpr int part_floats(int G, int D) {
-  return (G * (D + 2) + 3) / 4 * 4;
-}
 
-template <int D, int GH, bool BF16>
+// Shared: the positions behind a prefix that all sequences share, whose own
+// attention the launch before makes.  The call does not wait for that launch
+// (which releases it only after its own wait, so what came before is there)
+// until its own work is done; every part goes to the workspace.
+template <int D, int GH, bool BF16, bool Shared>
 __global__ void __launch_bounds__(kDcThreads, (DcCfg<D, GH>::kCtas))
 decode_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap kmap,
               const __grid_constant__ CUtensorMap vmap) {
@@ -268,8 +268,10 @@ decode_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap kmap,
     mbar_init(q_read, kDcWarps);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  pdl_wait();
+  if (!Shared) pdl_wait();
   pdl_trigger();
+  int shared = -1;
+  if constexpr (Shared) shared = max(checked_len(a.shared_v(), __ldcg(a.shared_len)), 0);
 
   // ---- thread t counts the tiles of sequences [t per, (t + 1) per), a scan
   // over the CTA gives their first tiles ----
@@ -280,11 +282,13 @@ decode_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap kmap,
   for (int b = b_lo; b < b_hi; ++b) {
     const int len = seq_len(a.v, b);
     if (b == b_lo) s_len0[tid] = len;
-    mine += int64_t(seq_plan(len, a.window, a.sinks).n) * a.v.hkv;
-    if (len <= 0 && b % int(gridDim.x) == int(blockIdx.x)) {
-      // an empty sequence: zeros
+    const int tiles = seq_plan(len, a.window, a.sinks, shared).n;
+    mine += int64_t(tiles) * a.v.hkv;
+    if (tiles == 0 && b % int(gridDim.x) == int(blockIdx.x)) {
       for (int g = 0; g < a.v.hkv; ++g)
         a.parts[int64_t(b) * a.v.hkv + g] = DcParts{0, 0};
+      if (len > 0) continue;  // (all of it is shared)
+      // an empty sequence: zeros
       for (int e = 0; e < a.H * D; e += 8) {
         const int64_t at = int64_t(b) * a.out_ld + e;
         const uint4 z = make_uint4(0u, 0u, 0u, 0u);
@@ -313,7 +317,10 @@ decode_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap kmap,
   }
   s_before[tid] = before;
   const Dealing dl = deal(total, int(gridDim.x), GH == 1);
-  if (int(blockIdx.x) >= dl.n_ctas) return;  // the whole CTA
+  if (int(blockIdx.x) >= dl.n_ctas) {  // the whole CTA
+    if (Shared) pdl_wait();
+    return;
+  }
   __syncthreads();
 
   if (warp == kDcWarps) {
@@ -363,7 +370,7 @@ decode_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap kmap,
       w.unit = unit;
       unit_range(dl, unit, &w.t, &w.end);
       if (w.t >= dl.total) return 0;
-      if (!item_at(a, bg, w.t, w.it)) return -1;
+      if (!item_at(a, bg, w.t, shared, w.it)) return -1;
       load_pages(w, tile_pos(w.it.plan, int(w.t - w.it.first), kDcTile) >>
                         a.v.page_shift);
       return 1;
@@ -443,7 +450,7 @@ decode_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap kmap,
         if (dynamic && w.t == claim_at + 1) find_next();
         if (++w.t == w.end) break;
         if (w.t >= w.it.first + w.it.plan.n) {
-          if (!item_next(a, w.it)) {
+          if (!item_next(a, shared, w.it)) {
             ok = false;
             break;
           }
@@ -682,10 +689,11 @@ decode_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap kmap,
       if (lane == 0) mbar_arrive(joined);
     } else {
       wait_for(joined, joins);
-      // slot 2 unit + 1 for a part that begins its item, else 2 unit: a unit
-      // has at most one of each
-      const bool whole = it.parts == 1;
-      float *p = a.part + int64_t(2 * it.unit + it.starts) * part_floats(G, D);
+      // (slots: dc_part_bytes)
+      const bool whole = !Shared && it.parts == 1;
+      const int64_t slot = Shared ? int64_t(it.b) * a.v.hkv + it.g + it.unit
+                                  : 2 * it.unit + it.starts;
+      float *p = a.part + slot * part_floats(G, D);
       if (it.starts && lane == 0)
         a.parts[int64_t(it.b) * a.v.hkv + it.g] = DcParts{it.unit0, it.parts};
 #pragma unroll
@@ -747,6 +755,9 @@ decode_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap kmap,
     }
     ++joins;
   }
+  // The launch after this one joins both launches' parts, and waits for this
+  // one alone.
+  if (Shared) pdl_wait();
 }
 
 // Joins the parts of the query heads: block x takes heads x, x + grid, ... of
@@ -897,20 +908,13 @@ decode_join_kernel(const DecodeArgs a) {
   if (claims.x != 0u && claims.y != kDcFirst) atomicOr(a.v.err, kPagedErr);
 }
 
-size_t align256(size_t b) { return (b + 255) / 256 * 256; }
-
-size_t part_bytes(int G, int D) {
-  return align256(size_t(2) * dc_max_units(D) * part_floats(G, D) *
-                  sizeof(float));
-}
-
-template <int D, int GH, bool BF16>
+template <int D, int GH, bool BF16, bool Shared>
 cudaError_t launch_t(const DecodeArgs &a, const CUtensorMap &kmap,
                      const CUtensorMap &vmap, cudaStream_t stream) {
   static std::atomic<int> cached[64];
   int resident = 0;
   cudaError_t e =
-      paged_resident(decode_kernel<D, GH, BF16>, cached, kDcThreads,
+      paged_resident(decode_kernel<D, GH, BF16, Shared>, cached, kDcThreads,
                      DcCfg<D, GH>::kSmem, &resident);
   if (e != cudaSuccess) return e;
   // More CTAs than tiles have nothing to do, however long the sequences may
@@ -931,8 +935,8 @@ cudaError_t launch_t(const DecodeArgs &a, const CUtensorMap &kmap,
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, decode_kernel<D, GH, BF16>, a, kmap, vmap);
-  if (e != cudaSuccess) return e;
+  e = cudaLaunchKernelEx(&cfg, decode_kernel<D, GH, BF16, Shared>, a, kmap, vmap);
+  if (e != cudaSuccess || Shared) return e;
   // Few heads (so likely many parts each): a large block for each; else a
   // small block for 8.  (Small blocks for one sequence of 131071 positions: 66
   // us, not 55; large ones for 120 windows of 1000: 98, not 31.)
@@ -951,18 +955,21 @@ cudaError_t launch_t(const DecodeArgs &a, const CUtensorMap &kmap,
 template <int D>
 cudaError_t launch_d(const DecodeArgs &a, const CUtensorMap &kmap,
                      const CUtensorMap &vmap, bool bf16, cudaStream_t stream) {
+  if (a.shared_len)
+    return a.G <= 8 ? launch_t<D, 1, true, true>(a, kmap, vmap, stream)
+                    : launch_t<D, 2, true, true>(a, kmap, vmap, stream);
   if (a.G <= 8)
-    return bf16 ? launch_t<D, 1, true>(a, kmap, vmap, stream)
-                : launch_t<D, 1, false>(a, kmap, vmap, stream);
-  return bf16 ? launch_t<D, 2, true>(a, kmap, vmap, stream)
-              : launch_t<D, 2, false>(a, kmap, vmap, stream);
+    return bf16 ? launch_t<D, 1, true, false>(a, kmap, vmap, stream)
+                : launch_t<D, 1, false, false>(a, kmap, vmap, stream);
+  return bf16 ? launch_t<D, 2, true, false>(a, kmap, vmap, stream)
+              : launch_t<D, 2, false, false>(a, kmap, vmap, stream);
 }
 
 }  // namespace
 
 size_t paged_decode_workspace_bytes(int n_seqs, int H, int Hkv, int D) {
-  return part_bytes(H / Hkv, D) +
-         align256(size_t(n_seqs) * Hkv * sizeof(DcParts)) + kPagedClaimBytes;
+  return dc_part_bytes(H / Hkv, D, 0) + dc_parts_bytes(size_t(n_seqs) * Hkv) +
+         kPagedClaimBytes;
 }
 
 cudaError_t launch_paged_decode(const PagedView &v, const PagedAttnLaunch &l,
@@ -979,7 +986,10 @@ cudaError_t launch_paged_decode(const PagedView &v, const PagedAttnLaunch &l,
   uint8_t *rest = static_cast<uint8_t *>(l.workspace) + kPagedClaimBytes;
   a.claim = static_cast<unsigned int *>(l.workspace);
   a.part = reinterpret_cast<float *>(rest);
-  a.parts = reinterpret_cast<DcParts *>(rest + part_bytes(a.G, l.D));
+  a.parts = reinterpret_cast<DcParts *>(
+      rest + dc_part_bytes(a.G, l.D, l.shared_len ? size_t(v.n_seqs) * v.hkv : 0));
+  a.shared_len = l.shared_len;
+  a.shared_pages = l.shared_pages;
   a.scale2 = l.scale * kLog2e;
   a.window = l.window;
   a.sinks = l.sinks;

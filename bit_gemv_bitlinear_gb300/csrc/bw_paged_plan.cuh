@@ -12,8 +12,10 @@
 
 #ifdef __CUDACC__
 #define BW_PLAN_FN __host__ __device__ inline
+#define BW_PLAN_FN_IN __host__ __device__
 #else
 #define BW_PLAN_FN inline
+#define BW_PLAN_FN_IN
 #endif
 
 namespace bw {
@@ -155,6 +157,51 @@ BW_PLAN_FN PfCut prefill_cut(int n_tokens, int n_seqs, int G, int Hkv,
   return cut;
 }
 
+// ---- a prefix that all sequences of a decode call share ----
+// The sequences (a token each) are cut into items of one query tile, or of two
+// where there are more, for each key-value head; an item visits all key tiles of
+// the prefix.
+struct SharedCut {
+  int seqs;   // of an item
+  int items;  // all key-value heads'
+};
+BW_PLAN_FN SharedCut shared_cut(int n_seqs, int G, int Hkv) {
+  SharedCut c{};
+  const int TQ = kPfRows / G;
+  c.seqs = n_seqs <= TQ ? TQ : 2 * TQ;
+  c.items = (n_seqs + c.seqs - 1) / c.seqs * Hkv;
+  return c;
+}
+BW_PLAN_FN int shared_tiles(int shared) {
+  return (shared + kPfTile - 1) / kPfTile;
+}
+// All items' tiles in one order, in equal contiguous shares of `n` CTAs.  The
+// part of item i that CTA c makes lies in slot i + c: along the order either
+// grows from part to part.
+struct SharedDeal {
+  int64_t total;
+  int tiles, n;  // of an item; CTAs that have a share
+  BW_PLAN_FN_IN void share(int c, int64_t *lo, int64_t *hi) const {
+    *lo = c < n ? c * total / n : total;
+    *hi = c < n ? (c + 1) * total / n : total;
+  }
+  // The CTA that has a tile.
+  BW_PLAN_FN_IN int owner(int64_t tile) const {
+    return int(((tile + 1) * n - 1) / total);
+  }
+};
+BW_PLAN_FN SharedDeal shared_deal(int items, int shared, int grid) {
+  SharedDeal d{};
+  d.tiles = shared_tiles(shared);
+  d.total = int64_t(items) * d.tiles;
+  d.n = d.total < grid ? int(d.total) : grid;
+  return d;
+}
+BW_PLAN_FN int shared_slots(const SharedCut &c, int grid) {
+  return c.items + grid;
+}
+
 }  // namespace bw
 
 #undef BW_PLAN_FN
+#undef BW_PLAN_FN_IN

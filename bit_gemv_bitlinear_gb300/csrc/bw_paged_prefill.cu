@@ -45,7 +45,9 @@
 // and the ends of its short items (2900 tokens, window 700: seven tiles) cost
 // half as much again.
 #include <algorithm>
+#include <climits>
 
+#include "bw_paged_shared.cuh"
 #include "bw_paged_tc.cuh"
 
 namespace bw {
@@ -76,6 +78,8 @@ struct PrefillArgs {
   int window, sinks;
   int box_rows;
   int split;
+  const int *shared_len;  // of a shared prefix (v.table: its pages); else null
+  int n_items;            // of a shared prefix, all key-value heads'
 };
 
 template <int D>
@@ -343,12 +347,37 @@ __device__ __forceinline__ PfWork pf_work(const PrefillArgs &a, const PfItem &it
   return w;
 }
 
+// A shared prefix's positions, 0 if the length is bad (reported).
+__device__ __forceinline__ int shared_positions(const PagedView &v,
+                                                const int *shared_len) {
+  const int n = checked_len(v, __ldcg(shared_len));
+  return n < 0 ? 0 : n;
+}
+// An item of a shared prefix: sequences row0 .. row0 + n_tok - 1, a token each,
+// and `bad` key tiles from tile `pos0` on; s is its part's slot.
+__device__ __forceinline__ PfWork pf_work_shared(const PrefillArgs &a,
+                                                 const PfItem &it, int shared) {
+  PfWork w;
+  w.tok0 = min(it.n_tok, a.TQ);
+  w.tok1 = it.n_tok - w.tok0;
+  w.p1 = shared - 1;
+  w.plan = TilePlan{shared_tiles(shared), 0, 0, 0, 0};
+  w.j_lo = it.pos0;
+  w.n = w.n0 = it.bad;
+  w.n1 = w.tok1 > 0 ? w.n : 0;
+  return w;
+}
+
 // Alone (128 dims): items of one query tile.  Nothing else fills the time
 // between its products, so the next scores are made during its softmax, in the
 // other tile's columns, the two in turn (a prompt of 509 tokens, 20 + 2 x 5
 // heads, in a table of no more positions: 15.2 us, 16.0 without, 17.4 with items
 // of two query tiles).
-template <int D, bool Alone>
+// Shared: the prefix that all sequences of a decode call share.  A token per
+// sequence, which sees the prefix up to its own length; the items' key tiles in
+// one order, dealt to the CTAs in equal contiguous shares, so a CTA's share is
+// a part of one item or of several, each left in the workspace for the join.
+template <int D, bool Alone, bool Shared>
 __global__ void __launch_bounds__(kPfThreads, 1)
 prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap qmap,
                const __grid_constant__ CUtensorMap kmap,
@@ -387,7 +416,11 @@ prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap qmap,
   bool void_call;
   // (few sequences, the scheduler: one a lane)
   SeqTokens kept{0, 0, 0, false, false};
-  {
+  int shared = 0;
+  if constexpr (Shared) {
+    shared = shared_positions(a.v, a.shared_len);
+    void_call = false;
+  } else {
     const int b_lo = tid < kPfScan ? min(tid * per, a.v.n_seqs) : a.v.n_seqs;
     const int b_hi = min(b_lo + per, a.v.n_seqs);
     int mine = 0;
@@ -419,6 +452,12 @@ prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap qmap,
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
+  auto work_of = [&](const PfItem &it) {
+    if constexpr (Shared)
+      return pf_work_shared(a, it, shared);
+    else
+      return pf_work(a, it);
+  };
   // The next item, by every role but the scheduler: item k lies in slot k & 1.
   int k_item = 0;
   auto next_item = [&](PfItem &it) {
@@ -443,11 +482,30 @@ prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap qmap,
       // One item ahead of the others, and between two items this warp makes
       // zeros of the value rows that no token of the item sees. ----
       int total = 0;
-      for (int w = 0; w < kPfScan / 32; ++w) total += s_sum[w];
+      if constexpr (!Shared)
+        for (int w = 0; w < kPfScan / 32; ++w) total += s_sum[w];
       if (void_call) total = 0;
+      // (a shared prefix: this CTA's share of the tiles)
+      const SharedDeal deal = shared_deal(a.n_items, shared, int(gridDim.x));
+      int64_t at = 0, share_end = 0;
+      if constexpr (Shared) deal.share(int(blockIdx.x), &at, &share_end);
       const int n_items = total * a.v.hkv * a.split;  // below 2^23
       auto find = [&](int k, PfItem &it) {
         it = PfItem{-1, 0, 0, 0, 0, 0, 0};
+        if constexpr (Shared) {
+          if (at >= share_end) return;
+          const int item = int(at / deal.tiles);
+          const int x = item / a.v.hkv;
+          it.b = 0;
+          it.g = item - x * a.v.hkv;
+          it.s = item + int(blockIdx.x);
+          it.row0 = x * a.TI;
+          it.n_tok = min(a.TI, a.n_tokens - it.row0);
+          it.pos0 = int(at - int64_t(item) * deal.tiles);
+          it.bad = int(min(int64_t(deal.tiles - it.pos0), share_end - at));
+          at += it.bad;
+          return;
+        }
         const int c = (k & 1) ? int(gridDim.x) - 1 - int(blockIdx.x) : int(blockIdx.x);
         const int idx = k * int(gridDim.x) + c;
         if (idx >= n_items) return;
@@ -509,7 +567,7 @@ prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap qmap,
       for (int k = 1; ok && it.b >= 0; ++k) {
         find(k, next);
         ok = give(k, next);
-        const PfWork w = pf_work(a, it);
+        const PfWork w = work_of(it);
         for (int j = 0; ok && j < w.n; ++j) {
           ok = warp_wait(&bar[C::kFullV + vs], uint32_t(vr) & 1u);
           if (!ok) break;
@@ -548,7 +606,7 @@ prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap qmap,
       bool ok = true;
       PfItem it;
       while (ok && next_item(it)) {
-        const PfWork w = pf_work(a, it);
+        const PfWork w = work_of(it);
         if (w.n == 0) continue;
         auto pos_of = [&](int j) { return tile_pos(w.plan, w.j_lo + j, kPfTile) + r0; };
         auto page_of = [&](int j) {
@@ -680,7 +738,7 @@ prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap qmap,
       bool ok = true;
       PfItem it;
       while (ok && next_item(it)) {
-        const PfWork w = pf_work(a, it);
+        const PfWork w = work_of(it);
         if (w.n == 0) continue;
         if constexpr (Alone) {
           if (i == 1) continue;  // (the first warp counts twice)
@@ -821,15 +879,22 @@ prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap qmap,
     PfItem it;
     bool more = next_item(it);
     PfWork w{};
-    if (more) w = pf_work(a, it);
+    if (more) w = work_of(it);
     while (ok && more) {
       const int n_mine = i ? w.n1 : w.n0, t_mine = i ? w.tok1 : w.tok0;
-      const bool live = tok < t_mine;
+      bool live = tok < t_mine;
       const int first = it.pos0 + i * TQ;    // the tile's positions
-      const int p = live ? first + tok : -1; // -1: sees nothing
+      int p = live ? first + tok : -1;       // -1: sees nothing
       // Key tiles that every row sees in whole: from all_lo or up to the first
       // tokens' end, and up to all_hi.
-      const int all_hi = first + 1 - kPfTile;
+      int all_hi = first + 1 - kPfTile;
+      if constexpr (Shared) {
+        // a row that sees nothing of this part is as one that is not there
+        // (an empty sequence's row is left out by the join: it hides nothing)
+        if (live) p = min(max(__ldcg(a.v.len + it.row0 + i * TQ + tok), 0), shared) - 1;
+        all_hi = __reduce_min_sync(0xffffffffu, live && p >= 0 ? p : INT_MAX - 1) + 1 - kPfTile;
+        live = live && p >= w.j_lo * kPfTile;
+      }
       const int all_lo =
           a.window > 0 ? seen_from(first + t_mine - 1, a.window, a.sinks).lo : 0;
       const int all_sk = a.window > 0 ? a.sinks - kPfTile : -1;
@@ -994,7 +1059,7 @@ prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap qmap,
       // runs ----
       PfItem next;
       more = ok && next_item(next);
-      if (more) w = pf_work(a, next);
+      if (more) w = work_of(next);
       if (ok && n_mine > 0) {
         // (A barrier of its own: kDoneO may be one or two products behind, and
         // a parity tells a phase only from the next one.)
@@ -1005,11 +1070,14 @@ prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap qmap,
       if (!ok) break;
       const int64_t row0 = int64_t(it.row0) + i * TQ;  // of this query tile
       const int h0 = it.g * G;
-      const bool direct = a.split == 1 || (it.bad && it.s == 0);
+      const bool direct = !Shared && (a.split == 1 || (it.bad && it.s == 0));
       // (A live row sees its own position: a sum of 0 where there were tiles
       // is one of scores that are all -infinity, whose answer is NaN.)
       const float inv = n_mine > 0 ? 1.0f / l : 0.0f;
-      if (live && a.split > 1)
+      const int64_t part_row = (int64_t(it.s) * a.TI + i * TQ) * G;
+      if constexpr (Shared) {
+        if (tok < t_mine) a.ml[part_row + r] = make_float2(m, l);
+      } else if (live && a.split > 1)
         a.ml[(int64_t(it.s) * a.n_tokens + row0 + tok) * a.H + h0 + r - tok * G] =
             make_float2(m, l);
       // 32 columns at a time (rolled: the code is fetched anew for every
@@ -1054,8 +1122,10 @@ prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap qmap,
               if (tok_of[q] < t_mine)
                 *reinterpret_cast<uint4 *>(
                     a.part +
-                    ((int64_t(it.s) * a.n_tokens + row0 + tok_of[q]) * a.H + h0 +
-                     head_of[q]) * D + c + half + (lane & 3) * 4) =
+                    (Shared ? part_row + (r & ~3) + q
+                            : (int64_t(it.s) * a.n_tokens + row0 + tok_of[q]) * a.H +
+                                  h0 + head_of[q]) * D +
+                    c + half + (lane & 3) * 4) =
                     make_uint4(y[q][0], y[q][1], y[q][2], y[q][3]);
           }
         }
@@ -1147,43 +1217,37 @@ prefill_join_kernel(const PrefillArgs a) {
         __floats2bfloat162_rn(acc[e] * inv, acc[e + 1] * inv);
 }
 
-template <int D, bool Alone>
-cudaError_t launch_t(const PagedView &v, const PagedAttnLaunch &l,
-                     const PfCut &cut, cudaStream_t stream) {
+// The sizes that the prompts' calls and the shared prefix's have in common.
+PrefillArgs make_args(const PagedView &v, const PagedAttnLaunch &l) {
   PrefillArgs a{};
   a.v = v;
-  a.q_start = l.q_start;
   a.n_tokens = l.n_tokens;
-  a.out = static_cast<__nv_bfloat16 *>(l.out);
-  a.out_ld = l.out_ld;
   a.H = l.H;
   a.G = l.H / v.hkv;
   a.TQ = kPfRows / a.G;
   a.scale2 = l.scale * kLog2e;
-  a.window = l.window;
-  a.sinks = l.sinks;
   const int page = 1 << v.page_shift;
   a.box_rows = page < kPfTile ? page : kPfTile;
-  a.split = cut.split;
-  a.TI = cut.one ? a.TQ : 2 * a.TQ;
-  const size_t rows = size_t(a.split) * l.n_tokens * l.H;
-  a.part = reinterpret_cast<float *>(static_cast<uint8_t *>(l.workspace) +
-                                     kPagedClaimBytes);
-  a.ml = reinterpret_cast<float2 *>(a.part + rows * D);
-  a.void_call = reinterpret_cast<int *>(static_cast<uint8_t *>(l.workspace) +
-                                        kPagedVoidAt);
+  a.split = 1;
+  return a;
+}
 
+// Launches `items` items, on as many CTAs as fit at most.
+template <int D, bool Alone, bool Shared>
+cudaError_t launch_items(const PrefillArgs &a, const PagedAttnLaunch &l,
+                         int64_t items, cudaStream_t stream) {
+  const PagedView &v = a.v;
   static std::atomic<int> cached[64];
   int resident = 0;
-  cudaError_t e = paged_resident(prefill_kernel<D, Alone>, cached, kPfThreads,
-                                 PfCfg<D>::kSmem, &resident);
+  cudaError_t e = paged_resident(prefill_kernel<D, Alone, Shared>, cached,
+                                 kPfThreads, PfCfg<D>::kSmem, &resident);
   if (e != cudaSuccess) return e;
   // setmaxnreg draws on the registers of the launch: a build that gives the
   // threads fewer than the roles' sum would wait for ever, so it is refused.
   static std::atomic<int> regs{0};  // a property of the build, not the device
   if (regs.load(std::memory_order_relaxed) == 0) {
     cudaFuncAttributes fa{};
-    e = cudaFuncGetAttributes(&fa, prefill_kernel<D, Alone>);
+    e = cudaFuncGetAttributes(&fa, prefill_kernel<D, Alone, Shared>);
     if (e != cudaSuccess) return e;
     regs.store(fa.numRegs, std::memory_order_relaxed);
   }
@@ -1207,8 +1271,6 @@ cudaError_t launch_t(const PagedView &v, const PagedAttnLaunch &l,
       !encode_pool(&vmap, v.v, v, D, a.box_rows))
     return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
-  const int64_t items =
-      prefill_items(l.n_tokens, v.n_seqs, a.TI, v.hkv) * a.split;
   cfg.gridDim = dim3(unsigned(items < resident ? items : resident));
   cfg.blockDim = dim3(kPfThreads);
   cfg.dynamicSmemBytes = PfCfg<D>::kSmem;
@@ -1218,15 +1280,57 @@ cudaError_t launch_t(const PagedView &v, const PagedAttnLaunch &l,
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, prefill_kernel<D, Alone>, a, qmap, kmap, vmap);
+  return cudaLaunchKernelEx(&cfg, prefill_kernel<D, Alone, Shared>, a, qmap,
+                            kmap, vmap);
+}
+
+template <int D, bool Alone>
+cudaError_t launch_t(const PagedView &v, const PagedAttnLaunch &l,
+                     const PfCut &cut, cudaStream_t stream) {
+  PrefillArgs a = make_args(v, l);
+  a.q_start = l.q_start;
+  a.out = static_cast<__nv_bfloat16 *>(l.out);
+  a.out_ld = l.out_ld;
+  a.window = l.window;
+  a.sinks = l.sinks;
+  a.split = cut.split;
+  a.TI = cut.one ? a.TQ : 2 * a.TQ;
+  const size_t rows = size_t(a.split) * l.n_tokens * l.H;
+  a.part = reinterpret_cast<float *>(static_cast<uint8_t *>(l.workspace) +
+                                     kPagedClaimBytes);
+  a.ml = reinterpret_cast<float2 *>(a.part + rows * D);
+  a.void_call = reinterpret_cast<int *>(static_cast<uint8_t *>(l.workspace) +
+                                        kPagedVoidAt);
+  const cudaError_t e = launch_items<D, Alone, false>(
+      a, l, prefill_items(l.n_tokens, v.n_seqs, a.TI, v.hkv) * a.split, stream);
   if (e != cudaSuccess || a.split == 1) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
   cfg.gridDim = dim3(unsigned((int64_t(l.n_tokens) * l.H + 7) / 8));
   cfg.blockDim = dim3(256);
-  cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, prefill_join_kernel<D>, a);
 }
 
 }  // namespace
+
+cudaError_t launch_shared_prefix(const PagedView &v, const PagedAttnLaunch &l,
+                                 const SharedPrefix &x, int grid,
+                                 cudaStream_t stream) {
+  PrefillArgs a = make_args(v, l);
+  a.shared_len = x.len;
+  a.TI = x.cut.seqs;
+  a.n_items = x.cut.items;
+  a.part = x.part;
+  a.ml = x.ml;
+  if (l.D == 64) return launch_items<64, false, true>(a, l, grid, stream);
+  return a.TI == a.TQ ? launch_items<128, true, true>(a, l, grid, stream)
+                      : launch_items<128, false, true>(a, l, grid, stream);
+}
 
 size_t paged_prefill_workspace_bytes(int n_tokens, int n_seqs, int H, int Hkv,
                                      int D) {

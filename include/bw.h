@@ -646,6 +646,115 @@ bw_status bw_attn_paged_prefill(const bw_bf16 *q, int64_t q_ld, int n_tokens,
                                 void *workspace, size_t workspace_bytes,
                                 bw_stream_t stream);
 
+/* bw_attn_paged_shared -- bw_attn_paged_decode for a batch whose sequences
+ * share a long prefix (a system prompt, a document), which is read and
+ * multiplied once for all of them: position j < *shared_len of every sequence
+ * lies in row j mod page_size of page shared_table[j div page_size], position
+ * j >= *shared_len where page_table has it.  kv_len counts the shared
+ * positions too; a sequence of fewer sees as many of them, an empty one gets
+ * zeros.  Entries of page_table below *shared_len / page_size are not used;
+ * where the prefix ends inside a page, the sequence's own page is read from
+ * there on.
+ * No window; bf16 output.  The shared positions' products run on the tensor
+ * cores and their exp weights are rounded to bf16, like the output; the others
+ * are as in bw_attn_paged_decode.  What a shared position that some sequence
+ * sees holds must be finite; others may hold anything.  A visible score that
+ * is NaN or +infinity and scores that are all -infinity give NaN in that head.
+ *   shared_table int32 [n_shared_pages] device, 4-byte aligned (a row of the
+ *             page table, say); shared_len int32 [1] device, 4-byte aligned,
+ *             from 0 to n_shared_pages * page_size: read on the device.  A
+ *             length outside counts as 0, a used entry outside [0, n_pages) as
+ *             zeros; both set bit 256 of the device error word.
+ *   n_shared_pages >= 1, n_shared_pages * page_size <= BW_PAGED_MAX_LEN.
+ *   workspace as for bw_attn_paged_decode (zeroed once, shared one after the
+ *             other by calls over paged caches of any kind and shape),
+ *             bw_attn_paged_shared_workspace_bytes(n_seqs, H, Hkv, D) bytes.
+ *   All else as for bw_attn_paged_decode.  It pays off from a few hundred
+ *   shared positions and a few sequences on. */
+size_t bw_attn_paged_shared_workspace_bytes(int n_seqs, int H, int Hkv, int D);
+bw_status bw_attn_paged_shared(const bw_bf16 *q, int64_t q_ld, int H,
+                               const bw_paged_kv *kv, const int *shared_table,
+                               int n_shared_pages, const int *shared_len,
+                               float scale, bw_bf16 *out, int64_t out_ld,
+                               void *workspace, size_t workspace_bytes,
+                               bw_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * What stands between a layer's projections ([W2A8] §4.1: a norm in front of
+ * every projection; §六 item 3: 8-bit activations), for rows of any batch.
+ * Ordering of these calls: launched with programmatic dependent launch;
+ * everything is read and written after the preceding work on `stream` has
+ * completed.  Asynchronous; they allocate nothing.
+ *
+ * bw_add_rms_norm_quant -- the residual's addition, the RMS norm and the codes
+ * that the next projection takes, in one pass over the row:
+ *   v = h + x (or x, without h),     h_out = v,
+ *   t = v / sqrt(mean(v^2) + eps) * gamma,
+ *   s = 127 / max(max |t|, 1e-5),    q = round(t s) (as bw_quant_act).
+ * fp32 arithmetic; the norm holds over all of fp32's range.  A row in which a
+ * value is not finite (or |t| leaves fp32) gets s = NaN and codes of 0, so
+ * that what is computed from it is NaN; its h_out is the sum all the same.
+ *   x      fp32 or (x_bf16 nonzero) bf16 [M][x_ld] device, aligned to its
+ *          type, x_ld at least K and below 2^31.
+ *   h      fp32 [M][K] device, 4-byte aligned, with h_out [M][K], which may be
+ *          h itself; or NULL, both.  x must not overlap h_out.
+ *   gamma  fp32 [K] device, 4-byte aligned, finite.  eps >= 0 (host).
+ *   q      int8 [M][K], s fp32 [M] device (outputs).
+ *   1 <= M <= BW_MAX_M, 1 <= K <= BW_MAX_K.  Rows of whole 16-byte vectors (8
+ *   of bf16) and q on 4 bytes, K % 4 == 0 and K <= 16384, are read once;
+ *   others are read again for the codes.
+ * ---------------------------------------------------------------------- */
+bw_status bw_add_rms_norm_quant(const void *x, int x_bf16, int64_t x_ld,
+                                const float *h, float *h_out,
+                                const float *gamma, float eps, int M, int K,
+                                int8_t *q, float *s, bw_stream_t stream);
+
+/* bw_relu2_rms_norm_quant -- the same behind the gated product, for the down
+ * projection: v = relu(g)^2 u with g = gu[m][0 .. F) and u = gu[m][F .. 2 F)
+ * (the rows of a fused gate|up projection).  A product beyond fp32's range
+ * counts as a value that is not finite.
+ *   gu     bf16 [M][gu_ld] device, 2-byte aligned, gu_ld at least 2 F and below
+ *          2^31.
+ *   gamma fp32 [F], q int8 [M][F], s fp32 [M] as above; 1 <= F <= BW_MAX_K. */
+bw_status bw_relu2_rms_norm_quant(const bw_bf16 *gu, int64_t gu_ld,
+                                  const float *gamma, float eps, int M, int F,
+                                  int8_t *q, float *s, bw_stream_t stream);
+
+/* bw_lora_add -- low-rank adapters of many requests beside a shared
+ * projection: every row adds its own adapter's product to the projection's
+ * output (bw_gemv_w2a8 or bw_gemm_w2a8, whose x and s it takes),
+ *   out[m] = bf16( y[m] + scale[a] B[a] (A[a] x[m]) / s[m] ),  a = adapter[m].
+ * A row without an adapter (-1) gets y.  An adapter number outside [-1,
+ * n_adapters) counts as -1 and sets bit 512 of the device error word.  Both
+ * products sum in fp32; A x is kept to 16 bits between them (two bf16
+ * values), 2^-17 of it.  What is not finite in a row or in an adapter stays
+ * within the rows that have it.
+ *   x        int8 [M][K] device, 4-byte aligned; s fp32 [M] device.
+ *   A        bf16 [n_adapters][R][K] device, B bf16 [n_adapters][N][R] device,
+ *            16-byte aligned; adapters of smaller rank are padded with zeros
+ *            (in both).
+ *   scale    fp32 [n_adapters] device, 4-byte aligned, or NULL (1).
+ *   adapter  int32 [M] device, 4-byte aligned, in any order.
+ *   y, out   bf16 [M][y_ld], [M][out_ld] device, 2-byte aligned, strides at
+ *            least N and below 2^31 (columns of a fused projection, say); out
+ *            may be y itself with the same stride, else must not overlap it.
+ *   workspace device scratch of at least bw_lora_workspace_bytes(M, R) bytes,
+ *            16-byte aligned, owned by the caller; overwritten.  Calls that
+ *            share one (captured graphs too) must not overlap on the GPU.
+ *   1 <= M <= BW_MAX_M, 1 <= N <= BW_MAX_N, 4 <= K <= BW_MAX_K, K % 4 == 0,
+ *   R a multiple of 8 up to BW_LORA_MAX_RANK, 1 <= n_adapters <=
+ *   BW_LORA_MAX_ADAPTERS.  16-byte rows of y and out, and K % 8 == 0 with x on
+ *   8 bytes, are read in vectors. */
+#define BW_LORA_MAX_RANK 128
+#define BW_LORA_MAX_ADAPTERS 65536
+size_t bw_lora_workspace_bytes(int M, int R);
+bw_status bw_lora_add(const int8_t *x, const float *s, const bw_bf16 *A,
+                      const bw_bf16 *B, const float *scale, const int *adapter,
+                      int n_adapters, int M, int N, int K, int R,
+                      const bw_bf16 *y, int64_t y_ld, bw_bf16 *out,
+                      int64_t out_ld, void *workspace, size_t workspace_bytes,
+                      bw_stream_t stream);
+
 /* bw_device_error -- reads and clears the library's device error word.
  * Kernels that wait on an mbarrier or poll for another CTA's data bound
  * every wait (about one second); a wait that runs out sets a bit here and
@@ -658,8 +767,9 @@ bw_status bw_attn_paged_prefill(const bw_bf16 *q, int64_t q_ld, int n_tokens,
  * read a different position after its dependency wait than before it (the
  * promise was broken; the call used the later one).  Bit 256: a call over
  * a paged cache met a bad length, token range or page number, or a workspace
- * that was not zeroed.
- * Returns BW_ERR_TIMEOUT if any bit other than 16, 128 and 256 was set, else
+ * that was not zeroed.  Bit 512: bw_lora_add met an adapter number out of
+ * range.
+ * Returns BW_ERR_TIMEOUT if any bit other than 16, 128, 256 and 512 was set, else
  * BW_ERR_INVALID_ARG if one of these was, else BW_OK; *bits receives the
  * word.
  * SYNCHRONISES `stream`; not for the hot path. */
