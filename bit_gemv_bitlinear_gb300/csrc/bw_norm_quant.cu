@@ -26,12 +26,25 @@ namespace bw {
 namespace {
 
 constexpr int kNormMaxThreads = 1024;
+constexpr int norm_max_threads(int V) { return V <= 4 ? 1024 : 512; }
 
-__device__ __forceinline__ float4 load4(const float *p) {
-  return *reinterpret_cast<const float4 *>(p);
+// Four values as they lie in memory, and as fp32.
+template <typename T>
+struct Four;
+template <>
+struct Four<float> {
+  using Raw = float4;
+};
+template <>
+struct Four<__nv_bfloat16> {
+  using Raw = uint2;
+};
+template <typename T>
+__device__ __forceinline__ typename Four<T>::Raw load4(const T *p) {
+  return *reinterpret_cast<const typename Four<T>::Raw *>(p);
 }
-__device__ __forceinline__ float4 load4(const __nv_bfloat16 *p) {
-  const uint2 w = *reinterpret_cast<const uint2 *>(p);
+__device__ __forceinline__ float4 wide(const float4 &v) { return v; }
+__device__ __forceinline__ float4 wide(const uint2 &w) {
   return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u),
                      __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xffff0000u));
 }
@@ -40,7 +53,8 @@ __device__ __forceinline__ float load1(const __nv_bfloat16 *p) {
   return __bfloat162float(*p);
 }
 
-// The rows' values, four or one at a time.  kAdds: they are written back.
+// The rows' values, four (as loaded, then made of that) or one at a time.
+// kStores: they are written back.
 template <typename T, bool Residual>
 struct AddRows {
   static constexpr bool kStores = Residual;
@@ -49,13 +63,20 @@ struct AddRows {
   const float *h;
   float *h_out;
   int K;
-  __device__ __forceinline__ float4 get4(int m, int k) const {
-    float4 v = load4(x + m * x_ld + k);
-    if (Residual) {
-      const float4 r = load4(h + int64_t(m) * K + k);
-      v = make_float4(r.x + v.x, r.y + v.y, r.z + v.z, r.w + v.w);
-    }
-    return v;
+  struct Raw {
+    typename Four<T>::Raw x;
+    float4 h;
+  };
+  __device__ __forceinline__ Raw load(int m, int k) const {
+    Raw r;
+    r.x = load4(x + m * x_ld + k);
+    if (Residual) r.h = load4(h + int64_t(m) * K + k);
+    return r;
+  }
+  __device__ __forceinline__ float4 value(const Raw &r) const {
+    const float4 v = wide(r.x);
+    if (!Residual) return v;
+    return make_float4(r.h.x + v.x, r.h.y + v.y, r.h.z + v.z, r.h.w + v.w);
   }
   __device__ __forceinline__ float get1(int m, int k) const {
     const float v = load1(x + m * x_ld + k);
@@ -83,9 +104,14 @@ struct GateRows {
   const __nv_bfloat16 *gu;
   int64_t gu_ld;
   int K;
-  __device__ __forceinline__ float4 get4(int m, int k) const {
-    const float4 g = load4(gu + m * gu_ld + k);
-    const float4 u = load4(gu + m * gu_ld + K + k);
+  struct Raw {
+    uint2 g, u;
+  };
+  __device__ __forceinline__ Raw load(int m, int k) const {
+    return Raw{load4(gu + m * gu_ld + k), load4(gu + m * gu_ld + K + k)};
+  }
+  __device__ __forceinline__ float4 value(const Raw &r) const {
+    const float4 g = wide(r.g), u = wide(r.u);
     return make_float4(gated(g.x, u.x), gated(g.y, u.y), gated(g.z, u.z),
                        gated(g.w, u.w));
   }
@@ -119,144 +145,152 @@ __device__ __forceinline__ float2 block_sum_max(float2 v, float2 *s) {
   return v;
 }
 
-__device__ __forceinline__ int8_t code(float v) {
-  return static_cast<int8_t>(
-      static_cast<int>(fminf(fmaxf(rintf(v), -128.0f), 127.0f)));
+// round(v), to even, for |v| of a code (127 and a few roundings): 3 2^22 more is
+// a whole number of units, and its low byte the code.  (A quarter of the time of
+// a rounding and a conversion.)
+__device__ __forceinline__ uint32_t code(float v) {
+  return __float_as_uint(v + 12582912.0f) & 0xffu;
+}
+__device__ __forceinline__ uint32_t codes4(const float4 &v, float f) {
+  const uint32_t a = __byte_perm(__float_as_uint(fmaf(v.x, f, 12582912.0f)),
+                                 __float_as_uint(fmaf(v.y, f, 12582912.0f)), 0x0040);
+  const uint32_t b = __byte_perm(__float_as_uint(fmaf(v.z, f, 12582912.0f)),
+                                 __float_as_uint(fmaf(v.w, f, 12582912.0f)), 0x0040);
+  return __byte_perm(a, b, 0x5410);
 }
 
-// What a row's codes need: code = rint(v c gamma mul); s is its scale.
+// What a row's codes need: code = rint(v gamma mul c); s is its scale.
 struct RowScale {
   float c, mul, s;
   bool bad;  // NaN or an infinity in the row
 };
-// sums(c): this thread's (sum (c v)^2, max |c v gamma|); most(): its max |v|.
-template <typename Sums, typename Most>
-__device__ __forceinline__ RowScale row_scale(int K, float eps, float2 (*s)[32],
-                                              Sums sums, Most most) {
-  RowScale r{1.0f, 0.0f, 0.0f, false};
-  float2 t = block_sum_max(sums(1.0f), s[0]);
-  float e = eps;
-  // (false for NaN as well; the whole block branches alike)
-  if (!(t.x >= 0x1p-80f && t.x <= 0x1p126f)) {
-    const float2 top = block_sum_max(make_float2(0.0f, most()), s[1]);
-    // a power of two near 1 / largest, itself within range
-    int ex = 0;
-    if (top.y > 0.0f && top.y <= 3.402823466e38f) frexpf(top.y, &ex);
-    ex = min(max(ex, -120), 120);
-    r.c = ldexpf(1.0f, -ex);
-    t = block_sum_max(sums(r.c), s[0]);
-    r.bad = !(t.x <= 3.402823466e38f);
-    e = eps * r.c * r.c;  // +infinity where eps is all that counts
-  }
-  const float mean = t.x / float(K) + e;
+// From the sum t.x of (c v)^2 and the largest t.y |c v gamma|.
+__device__ __forceinline__ RowScale row_scale(float2 t, float c,
+                                              float inv_K, float eps) {
+  RowScale r{c, 0.0f, 0.0f, false};
+  const float e = eps * c * c;  // +infinity where eps is all that counts
+  const float mean = fmaf(t.x, inv_K, e);
   // rows of zeros with eps 0: codes of zero
-  float inv = mean > 0.0f ? 1.0f / sqrtf(mean) : 0.0f;
-  if (e > 3.402823466e38f) inv = (1.0f / sqrtf(eps)) / r.c;
+  float inv = mean > 0.0f ? rsqrtf(mean) : 0.0f;
+  if (e > 3.402823466e38f) inv = rsqrtf(eps) / c;
   const float top = inv * t.y;
-  r.bad |= !(top <= 3.402823466e38f);
-  r.s = 127.0f / fmaxf(top, 1e-5f);
+  r.bad = !(t.x <= 3.402823466e38f) || !(top <= 3.402823466e38f);
+  // (every thread makes these: the root and the quotient in a few operations,
+  // off by 2 units at most)
+  r.s = __fdividef(127.0f, fmaxf(top, 1e-5f));
   r.mul = inv * r.s;
   if (r.bad) r.s = __int_as_float(0x7fc00000);
   return r;
 }
+// Whether a row whose squares sum to this (with c = 1) is summed again; false
+// for NaN as well.
+__device__ __forceinline__ bool in_range(float sum) {
+  return sum >= 0x1p-80f && sum <= 0x1p126f;
+}
+// The row once more from memory, where the codes come from then too (rare: it
+// need not be fast).  h_out is written already.
+template <typename Rows>
+__device__ __noinline__ void again(const Rows &rows, const float *gamma,
+                                   float eps, float inv_K, int K, int8_t *q,
+                                   float *s_out, int m, float2 (*s_red)[32]) {
+  float2 t = make_float2(0.0f, 0.0f);
+  for (int k = threadIdx.x; k < K; k += blockDim.x)
+    t.y = fmaxf(t.y, fabsf(rows.again1(m, k)));
+  t = block_sum_max(t, s_red[1]);
+  int ex = 0;  // a power of two near 1 / largest, itself within range
+  if (t.y > 0.0f && t.y <= 3.402823466e38f) frexpf(t.y, &ex);
+  const float c = ldexpf(1.0f, -min(max(ex, -120), 120));
+  t = make_float2(0.0f, 0.0f);
+  for (int k = threadIdx.x; k < K; k += blockDim.x) {
+    const float v = c * rows.again1(m, k);
+    t.x = fmaf(v, v, t.x);
+    t.y = fmaxf(t.y, fabsf(v * gamma[k]));
+  }
+  const RowScale r = row_scale(block_sum_max(t, s_red[0]), c, inv_K, eps);
+  if (threadIdx.x == 0) s_out[m] = r.s;
+  for (int k = threadIdx.x; k < K; k += blockDim.x)
+    q[int64_t(m) * K + k] =
+        r.bad ? int8_t(0) : int8_t(code(c * rows.again1(m, k) * gamma[k] * r.mul));
+}
 
-// Rows of K % 4 == 0 values, aligned for vectors: V vectors a thread.
+// Rows of K % 4 == 0 values, aligned for vectors: V vectors a thread.  A value
+// is kept as its product with gamma.
 template <typename Rows, int V>
-__global__ void __launch_bounds__(kNormMaxThreads)
-norm_quant_kernel(const Rows rows, const float *gamma, float eps, int K,
-                  int8_t *q, float *s_out) {
+__global__ void __launch_bounds__(norm_max_threads(V))
+norm_quant_kernel(const Rows rows, const float *gamma, float eps, float inv_K,
+                  int K, int8_t *q, float *s_out) {
   __shared__ float2 s_red[2][32];
   pipe::pdl_wait();
   pipe::pdl_trigger();
   const int m = blockIdx.x, nv = K / 4;
-  float4 v[V], g[V];
+  // Every load without a branch around it (the last vector again where there is
+  // none): with one, the compiler waits for each load before it makes the next
+  // (2039 x 6912 gated: 32 us, and 20.7 so).
+  typename Rows::Raw raw[V];
+  float4 v[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+    raw[i] = rows.load(m, 4 * min(int(threadIdx.x + i * blockDim.x), nv - 1));
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+    v[i] = load4(gamma + 4 * min(int(threadIdx.x + i * blockDim.x), nv - 1));
+  float2 t = make_float2(0.0f, 0.0f);
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     const int k = threadIdx.x + i * blockDim.x;
-    v[i] = g[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    const float4 y = rows.value(raw[i]), g = v[i];
+    v[i] = make_float4(y.x * g.x, y.y * g.y, y.z * g.z, y.w * g.w);
     if (k < nv) {
-      v[i] = rows.get4(m, 4 * k);
-      g[i] = load4(gamma + 4 * k);
+      if (Rows::kStores) rows.put4(m, 4 * k, y);
+      t.x = fmaf(y.x, y.x, t.x);
+      t.x = fmaf(y.y, y.y, t.x);
+      t.x = fmaf(y.z, y.z, t.x);
+      t.x = fmaf(y.w, y.w, t.x);
     }
+    t.y = fmaxf(fmaxf(t.y, fmaxf(fabsf(v[i].x), fabsf(v[i].y))),
+                fmaxf(fabsf(v[i].z), fabsf(v[i].w)));
   }
-  if (Rows::kStores) {
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int k = threadIdx.x + i * blockDim.x;
-      if (k < nv) rows.put4(m, 4 * k, v[i]);
-    }
+  t = block_sum_max(t, s_red[0]);
+  if (!in_range(t.x)) {  // (the whole block)
+    again(rows, gamma, eps, inv_K, K, q, s_out, m, s_red);
+    return;
   }
-  const RowScale r = row_scale(
-      K, eps, s_red,
-      [&](float c) {
-        float2 t = make_float2(0.0f, 0.0f);
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-          const float a[4] = {c * v[i].x, c * v[i].y, c * v[i].z, c * v[i].w};
-          const float b[4] = {g[i].x, g[i].y, g[i].z, g[i].w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            t.x = fmaf(a[e], a[e], t.x);
-            t.y = fmaxf(t.y, fabsf(a[e] * b[e]));
-          }
-        }
-        return t;
-      },
-      [&] {
-        float t = 0.0f;
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-          t = fmaxf(fmaxf(t, fmaxf(fabsf(v[i].x), fabsf(v[i].y))),
-                    fmaxf(fabsf(v[i].z), fabsf(v[i].w)));
-        return t;
-      });
+  const RowScale r = row_scale(t, 1.0f, inv_K, eps);
   if (threadIdx.x == 0) s_out[m] = r.s;
-  char4 *qr = reinterpret_cast<char4 *>(q + int64_t(m) * K);
+  uint32_t *qr = reinterpret_cast<uint32_t *>(q + int64_t(m) * K);
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     const int k = threadIdx.x + i * blockDim.x;
-    if (k < nv)
-      qr[k] = r.bad ? make_char4(0, 0, 0, 0)
-                    : make_char4(code(r.c * v[i].x * g[i].x * r.mul),
-                                 code(r.c * v[i].y * g[i].y * r.mul),
-                                 code(r.c * v[i].z * g[i].z * r.mul),
-                                 code(r.c * v[i].w * g[i].w * r.mul));
+    if (k < nv) qr[k] = r.bad ? 0u : codes4(v[i], r.mul);
   }
 }
 
 // Any K and alignment: the row is read once for every pass over it.
 template <typename Rows>
 __global__ void __launch_bounds__(kNormMaxThreads)
-norm_quant_any_kernel(const Rows rows, const float *gamma, float eps, int K,
-                      int8_t *q, float *s_out) {
+norm_quant_any_kernel(const Rows rows, const float *gamma, float eps, float inv_K,
+                      int K, int8_t *q, float *s_out) {
   __shared__ float2 s_red[2][32];
   pipe::pdl_wait();
   pipe::pdl_trigger();
   const int m = blockIdx.x;
-  bool first = true;
-  const RowScale r = row_scale(
-      K, eps, s_red,
-      [&](float c) {
-        float2 t = make_float2(0.0f, 0.0f);
-        for (int k = threadIdx.x; k < K; k += blockDim.x) {
-          const float v = first ? rows.get1(m, k) : rows.again1(m, k);
-          if (Rows::kStores && first) rows.put1(m, k, v);
-          t.x = fmaf(c * v, c * v, t.x);
-          t.y = fmaxf(t.y, fabsf(c * v * gamma[k]));
-        }
-        first = false;
-        return t;
-      },
-      [&] {
-        float t = 0.0f;
-        for (int k = threadIdx.x; k < K; k += blockDim.x)
-          t = fmaxf(t, fabsf(rows.again1(m, k)));
-        return t;
-      });
+  float2 t = make_float2(0.0f, 0.0f);
+  for (int k = threadIdx.x; k < K; k += blockDim.x) {
+    const float v = rows.get1(m, k);
+    if (Rows::kStores) rows.put1(m, k, v);
+    t.x = fmaf(v, v, t.x);
+    t.y = fmaxf(t.y, fabsf(v * gamma[k]));
+  }
+  t = block_sum_max(t, s_red[0]);
+  if (!in_range(t.x)) {
+    again(rows, gamma, eps, inv_K, K, q, s_out, m, s_red);
+    return;
+  }
+  const RowScale r = row_scale(t, 1.0f, inv_K, eps);
   if (threadIdx.x == 0) s_out[m] = r.s;
   for (int k = threadIdx.x; k < K; k += blockDim.x)
     q[int64_t(m) * K + k] =
-        r.bad ? int8_t(0) : code(r.c * rows.again1(m, k) * gamma[k] * r.mul);
+        r.bad ? int8_t(0) : int8_t(code(rows.again1(m, k) * gamma[k] * r.mul));
 }
 
 bool aligned_to(const void *p, uintptr_t a) {
@@ -276,18 +310,25 @@ cudaError_t launch_rows(const Rows &rows, bool vec, const NormQuantLaunch &l,
   cfg.numAttrs = 1;
   vec = vec && l.K % 4 == 0 && aligned_to(l.gamma, 16) && aligned_to(l.q, 4);
   const int nv = l.K / 4;
-  auto go = [&](auto kernel, int v, int work) {
-    const int threads = (work + v - 1) / v;
-    cfg.blockDim = dim3(unsigned(std::min((threads + 31) / 32 * 32, kNormMaxThreads)));
-    return cudaLaunchKernelEx(&cfg, kernel, rows, l.gamma, l.eps, l.K, l.q, l.s);
+  const float inv_K = float(1.0 / l.K);
+  auto go = [&](auto kernel, int threads) {
+    cfg.blockDim = dim3(unsigned((threads + 31) / 32 * 32));
+    return cudaLaunchKernelEx(&cfg, kernel, rows, l.gamma, l.eps, inv_K, l.K,
+                              l.q, l.s);
   };
-  if (vec && nv <= kNormMaxThreads)
-    return go(norm_quant_kernel<Rows, 1>, 1, nv);
-  if (vec && nv <= 2 * kNormMaxThreads)
-    return go(norm_quant_kernel<Rows, 2>, 2, nv);
-  if (vec && nv <= 4 * kNormMaxThreads)
-    return go(norm_quant_kernel<Rows, 4>, 4, nv);
-  return go(norm_quant_any_kernel<Rows>, 4, l.K);
+  // Up to 320 threads: a CTA's loads are under way while others' sums are
+  // exchanged (us with 2, 4 and 8 vectors a thread: 4096 x 2560 with residual
+  // 18.3, 18.7, 26; 2039 x 6912 gated 19.3, 20.7, 16.5).  Where every row has an
+  // SM to itself, the shortest chain (64 x 6912: 2.1, 2.1, 2.5).
+  const bool few = l.M <= device_sm_count();
+  if (vec && nv <= (few ? 2048 : 640))
+    return go(norm_quant_kernel<Rows, 2>, (nv + 1) / 2);
+  if (vec && nv <= (few ? 4096 : 1280))
+    return go(norm_quant_kernel<Rows, 4>, (nv + 3) / 4);
+  if (vec && nv <= 8 * norm_max_threads(8))
+    return go(norm_quant_kernel<Rows, 8>, (nv + 7) / 8);
+  return go(norm_quant_any_kernel<Rows>,
+            std::min((l.K + 3) / 4, kNormMaxThreads));
 }
 
 }  // namespace
