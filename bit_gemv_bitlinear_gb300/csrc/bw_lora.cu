@@ -11,9 +11,9 @@
 // two bf16 values (2^-17 of it is lost, against bf16's 2^-8 in the output), so
 // the second product runs on the tensor cores too and sums in fp32.
 //
-// Bound by bytes: the adapters that a call uses, and y.  mma.sync and not
-// tcgen05: a call has few rows of each adapter, and 16 rows by 8 columns are the
-// smallest tile there is.  Layout:
+// Bound by bytes: the adapters that a call uses, and y.  Few rows run on mma.sync:
+// they may well all have other adapters, and 16 rows by 8 columns are the smallest
+// tile there is.  Layout:
 //  * 16 rows are a tile.  Its distinct adapters are found with ballots, in any
 //    order of rows; each is multiplied with the whole tile, and rows of others
 //    are left out (shrink: not stored; expand: zeros for u).
@@ -22,13 +22,18 @@
 //    codes, made bf16 by four operations a pair), straight from global memory;
 //    and the columns of the second product, so a lane stores 16 bytes of out.
 //  * shrink: a CTA takes a tile, one (or every J-th) of its adapters and 16 or
-//    all of its R rows; the warps cut the K axis and add up in shared memory.
-//  * expand: a CTA takes 32 columns and the adapters of a tile (few rows: the
-//    warps deal them out and add up in shared memory), or 256 columns and four
-//    tiles, a warp 32 columns (many rows: B is loaded when the adapter changes).
+//    more of its R rows; the warps cut the K axis and add up in shared memory.
+//    (Prompts: J = 2, or a tile that two requests share holds up the rest.)
+//  * expand, few rows: a CTA takes 32 columns and the adapters of a tile; the
+//    warps deal them out and add up in shared memory.
+//  * expand, many rows: on tcgen05, 128 rows by 128 columns (below).
+// 2011 rows of 5 adapters of rank 64, 13824 x 2560: 34 us, 0.56 of the measured copy
+// rate; with mma.sync and y in registers the second product alone was 40 (500
+// instructions a warp for 32 x 32 outputs, 10 cycles each).
 #include <algorithm>
 
 #include "bw_serve.cuh"
+#include "bw_tc.cuh"
 
 namespace bw {
 namespace {
@@ -38,7 +43,8 @@ constexpr int kLoraWarps = 8;
 constexpr int kLoraThreads = kLoraWarps * 32;
 // Up to this many rows a tile may well hold another adapter in every row.
 constexpr int kLoraFewRows = 256;
-constexpr int kLoraTiles = 4;  // tiles of 16 rows a CTA of the second product
+// From this many rows on the second product runs on tcgen05.
+constexpr int kLoraTcRows = 513;
 
 struct LoraArgs {
   const int8_t *x;
@@ -51,7 +57,10 @@ struct LoraArgs {
   int64_t y_ld;
   __nv_bfloat16 *out;
   int64_t out_ld;
-  __nv_bfloat16 *u_hi, *u_lo;  // [M][R16]
+  // u as two bf16 values, rows u_ld apart: [M][R16] each, or (tcgen05) [M][2 R16]
+  // of hi | lo.
+  __nv_bfloat16 *u_hi, *u_lo;
+  int u_ld;
   unsigned int *err;
 };
 
@@ -145,11 +154,15 @@ lora_shrink_kernel(const LoraArgs a) {
   unsigned left = __ballot_sync(0xffffffffu, mine >= 0), rows;
   const int8_t *x0 = a.x + int64_t(min(row0 + fr, a.M - 1)) * a.K;
   const int8_t *x1 = a.x + int64_t(min(row0 + fr + 8, a.M - 1)) * a.K;
+  // the row of the values that this thread adds up
+  const int out_row = ((threadIdx.x >> 3) & 7) + 8 * (threadIdx.x & 1);
   int id;
   for (int j = 0; next_adapter(mine, left, id, rows); ++j) {
     if (j % int(gridDim.z) != int(blockIdx.z)) continue;
     const __nv_bfloat16 *A =
         a.A + (int64_t(id) * a.R + r0 + fr) * a.K;  // row 8 t + fr of tile t
+    const float scale = a.scale ? __ldcg(a.scale + id) : 1.0f;
+    const float row_s = __ldcg(a.s + min(row0 + out_row, a.M - 1));
     float c[NT][4] = {};
 #pragma unroll 1
     for (int k0 = warp * 32; k0 < a.K; k0 += kWarps * 32 * kAhead) {
@@ -186,10 +199,9 @@ lora_shrink_kernel(const LoraArgs a) {
           make_float4(c[t][0], c[t][1], c[t][2], c[t][3]);
     __syncthreads();
     // element e of lane l, tile t: row l / 4 (+ 8), column 8 t + 2 (l mod 4) + ..
-    const float scale = a.scale ? __ldcg(a.scale + id) : 1.0f;
-    for (int i = threadIdx.x; i < NT * 32 * 2; i += kWarps * 32) {
-      const int half = i & 1, l = (i >> 1) & 31, t = i >> 6;
-      const int row = (l >> 2) + 8 * half, col = r0 + 8 * t + 2 * (l & 3);
+    for (int t = threadIdx.x >> 6; t < NT; t += kWarps / 2) {
+      const int half = threadIdx.x & 1, l = (threadIdx.x >> 1) & 31;
+      const int row = out_row, col = r0 + 8 * t + 2 * (l & 3);
       if (!(rows >> row & 1u) || col >= a.R16) continue;
       float v0 = 0.0f, v1 = 0.0f;
 #pragma unroll
@@ -197,13 +209,13 @@ lora_shrink_kernel(const LoraArgs a) {
         v0 += s_sum[w][t][l][2 * half];
         v1 += s_sum[w][t][l][2 * half + 1];
       }
-      const float f = scale / __ldcg(a.s + row0 + row);
+      const float f = scale / row_s;
       v0 *= f;
       v1 *= f;
       const __nv_bfloat162 hi = __floats2bfloat162_rn(v0, v1);
       const __nv_bfloat162 lo = __floats2bfloat162_rn(
           v0 - __low2float(hi), v1 - __high2float(hi));
-      const int64_t at = int64_t(row0 + row) * a.R16 + col;
+      const int64_t at = int64_t(row0 + row) * a.u_ld + col;
       *reinterpret_cast<__nv_bfloat162 *>(a.u_hi + at) = hi;
       *reinterpret_cast<__nv_bfloat162 *>(a.u_lo + at) = lo;
     }
@@ -235,34 +247,6 @@ __device__ __forceinline__ void load_b(const LoraArgs &a, int id, int n0,
             a.B + (int64_t(id) * a.N + col) * a.R + r));
     }
 }
-// p = u B for a tile: row fr of u at hi and lo, row fr + 8 `step` values on.
-// (Rows of other adapters are multiplied too: a row's u makes its own row alone.)
-template <int KK, typename Load>
-__device__ __forceinline__ void multiply(const LoraArgs &a,
-                                         const uint2 (&b)[KK][4],
-                                         const __nv_bfloat16 *hi,
-                                         const __nv_bfloat16 *lo, int step,
-                                         Load load, float (&p)[4][4]) {
-  const int r0 = 4 * (threadIdx.x & 3);
-#pragma unroll
-  for (int t = 0; t < 4; ++t)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) p[t][e] = 0.0f;
-#pragma unroll
-  for (int k = 0; k < KK; ++k) {
-    if (16 * k >= a.R16) break;
-    const int r = 16 * k + r0;
-    const uint2 h0 = load(hi + r), h1 = load(hi + step + r);
-    const uint2 l0 = load(lo + r), l1 = load(lo + step + r);
-    const uint32_t fh[4] = {h0.x, h1.x, h0.y, h1.y};
-    const uint32_t fl[4] = {l0.x, l1.x, l0.y, l1.y};
-#pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      mma16816(p[t], fl, b[k][t].x, b[k][t].y);
-      mma16816(p[t], fh, b[k][t].x, b[k][t].y);
-    }
-  }
-}
 // What a product adds to the rows that are the adapter's.  (To those alone: 0
 // times a weight that is not finite would not vanish in another's row.)
 __device__ __forceinline__ void keep_rows(unsigned rows, const float (&p)[4][4],
@@ -290,26 +274,27 @@ __device__ __forceinline__ uint4 load_y(const LoraArgs &a, int row, int col) {
       p[e >> 1] |= uint32_t(__bfloat16_as_ushort(y[e])) << (16 * (e & 1));
   return w;
 }
+// A pair of bf16 as fp32, and back.
+__device__ __forceinline__ float low_of(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float high_of(uint32_t w) {
+  return __uint_as_float(w & 0xffff0000u);
+}
+__device__ __forceinline__ uint32_t pair_of(float lo, float hi) {
+  const __nv_bfloat162 t = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t *>(&t);
+}
 template <bool Vec>
 __device__ __forceinline__ void store_row(const LoraArgs &a, int row, int col,
-                                          uint4 w, const float (&c)[8]) {
+                                          const uint32_t (&w)[4]) {
   if (row >= a.M) return;
-  uint32_t *p = reinterpret_cast<uint32_t *>(&w);
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const __nv_bfloat162 t =
-        __floats2bfloat162_rn(__uint_as_float(p[e] << 16) + c[2 * e],
-                              __uint_as_float(p[e] & 0xffff0000u) + c[2 * e + 1]);
-    p[e] = *reinterpret_cast<const uint32_t *>(&t);
-  }
   __nv_bfloat16 *o = a.out + row * a.out_ld + col;
   if (Vec && col + 8 <= a.N) {
-    *reinterpret_cast<uint4 *>(o) = w;
+    *reinterpret_cast<uint4 *>(o) = make_uint4(w[0], w[1], w[2], w[3]);
   } else {
 #pragma unroll
     for (int e = 0; e < 8; ++e)
       if (col + e < a.N)
-        o[e] = __ushort_as_bfloat16(uint16_t(p[e >> 1] >> (16 * (e & 1))));
+        o[e] = __ushort_as_bfloat16(uint16_t(w[e >> 1] >> (16 * (e & 1))));
   }
 }
 
@@ -345,19 +330,32 @@ lora_expand_few_kernel(const LoraArgs a) {
     if (rows[u]) load_b<KK>(a, ids[u], n0, b[u]);
   pipe::pdl_wait();
   pipe::pdl_trigger();
-  const int r0 = min(row0 + fr, a.M - 1), r1 = min(row0 + fr + 8, a.M - 1);
-  const int64_t at = int64_t(r0) * a.R16;
+  // (rows of other adapters are multiplied too: a row's u makes its own row alone)
+  const int64_t at0 = int64_t(min(row0 + fr, a.M - 1)) * a.u_ld;
+  const int64_t at1 = int64_t(min(row0 + fr + 8, a.M - 1)) * a.u_ld;
   float c[4][4] = {};
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
     if (!rows[u]) continue;
     if (u >= kHeld) load_b<KK>(a, ids[u], n0, b[u % kHeld]);
-    float p[4][4];
-    multiply<KK>(a, b[u % kHeld], a.u_hi + at, a.u_lo + at, (r1 - r0) * a.R16,
-                 [](const __nv_bfloat16 *q) {
-                   return __ldcg(reinterpret_cast<const uint2 *>(q));
-                 },
-                 p);
+    float p[4][4] = {};
+#pragma unroll
+    for (int k = 0; k < KK; ++k) {
+      if (16 * k >= a.R16) break;
+      const int r = 16 * k + 4 * fc;
+      auto piece = [&](const __nv_bfloat16 *x, int64_t row_at) {
+        return __ldcg(reinterpret_cast<const uint2 *>(x + row_at + r));
+      };
+      const uint2 h0 = piece(a.u_hi, at0), h1 = piece(a.u_hi, at1);
+      const uint2 l0 = piece(a.u_lo, at0), l1 = piece(a.u_lo, at1);
+      const uint32_t hi[4] = {h0.x, h1.x, h0.y, h1.y};
+      const uint32_t lo[4] = {l0.x, l1.x, l0.y, l1.y};
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        mma16816(p[t], lo, b[u % kHeld][k][t].x, b[u % kHeld][k][t].y);
+        mma16816(p[t], hi, b[u % kHeld][k][t].x, b[u % kHeld][k][t].y);
+      }
+    }
     keep_rows(rows[u], p, c);
   }
 #pragma unroll
@@ -367,91 +365,351 @@ lora_expand_few_kernel(const LoraArgs a) {
   __syncthreads();
   if (row >= kLoraRows) return;
   const int half = row >> 3, l = (row & 7) * 4 + fc;
-  float v[8] = {};
+  uint32_t w[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-  for (int t = 0; t < 4; ++t)
+  for (int t = 0; t < 4; ++t) {
+    float v0 = 0.0f, v1 = 0.0f;
 #pragma unroll
-    for (int w = 0; w < kLoraWarps; ++w) {
-      v[2 * t] += s_sum[w][t][l][2 * half];
-      v[2 * t + 1] += s_sum[w][t][l][2 * half + 1];
+    for (int k = 0; k < kLoraWarps; ++k) {
+      v0 += s_sum[k][t][l][2 * half];
+      v1 += s_sum[k][t][l][2 * half + 1];
     }
-  store_row<Vec>(a, row0 + row, n0 + 8 * fc, y, v);
+    w[t] = pair_of(low_of(w[t]) + v0, high_of(w[t]) + v1);
+  }
+  store_row<Vec>(a, row0 + row, n0 + 8 * fc, w);
 }
 
-// Many rows: four tiles and 256 columns a CTA, a warp 32 columns of all tiles.
-// u of the tiles lies in shared memory, rows an odd number of 32 bytes apart (so
-// that the 16 lanes of a fragment's load meet 32 banks); y is asked for before
-// the wait.
-__host__ __device__ constexpr int u_stride(int R16) {
-  return R16 + (R16 / 16 % 2 ? 0 : 16);
-}
-template <int KK, bool Vec>
-__global__ void __launch_bounds__(kLoraThreads, KK <= 4 ? 2 : 1)
-lora_expand_kernel(const LoraArgs a) {
-  constexpr int kRows = kLoraTiles * kLoraRows;
-  __shared__ __align__(16) __nv_bfloat16 s_u[2][kRows * u_stride(16 * KK)];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int n0 = (blockIdx.x * kLoraWarps + warp) * 32;
-  const int row0 = blockIdx.y * kRows;
-  const int fr = lane >> 2, fc = lane & 3;
-  int mine[kLoraTiles];
-  uint4 y[kLoraTiles][2];
-#pragma unroll
-  for (int i = 0; i < kLoraTiles; ++i) {
-    mine[i] = lane_adapter(a, row0 + i * kLoraRows);
-#pragma unroll
-    for (int half = 0; half < 2; ++half)
-      y[i][half] = load_y<Vec>(a, row0 + i * kLoraRows + fr + 8 * half, n0 + 8 * fc);
+// ---- the second product for many rows, on tcgen05 ----
+// A CTA takes tiles of 128 rows by 128 columns in turn; a tile's distinct adapters
+// are its rounds (one for most tiles of prompts).  A round's U (hi | lo, 128 rows)
+// and B (128 columns) come by tiled copies, two rounds ahead; U B^T goes to one of
+// two accumulators in tensor memory (U's two halves against the same B); y comes
+// into shared memory by tiled copies too, eight warps add the accumulator to it, a
+// thread to a row's 64 columns, where the row is the round's, and a tiled copy
+// writes it out.  Every role finds the rounds by itself, from the adapter numbers.
+constexpr int kExRows = 128, kExCols = 128;
+constexpr int kExSoftWarps = 8;
+constexpr int kExThreads = (kExSoftWarps + 3) * 32;  // and copies in, products, out
+template <int KK>  // R16 <= 16 KK
+struct ExpandCfg {
+  static constexpr int kUBlocks = (2 * 16 * KK + 63) / 64;  // of 64 values
+  static constexpr int kBBlocks = (16 * KK + 63) / 64;
+  static constexpr uint32_t kBlock = 128 * 128;             // 128 rows of them
+  static constexpr uint32_t kRound = (kUBlocks + kBBlocks) * kBlock;
+  static constexpr uint32_t kY = 2 * kBlock;
+  static constexpr int kRounds = KK <= 4 ? 2 : 1;  // in flight
+  static constexpr int kTiles = 4;
+  static constexpr uint32_t kYAt = kRounds * kRound;
+  static constexpr uint32_t kBars = kYAt + kTiles * kY;
+  // barriers
+  static constexpr int kFullR = 0, kEmptyR = kRounds;       // U and B
+  static constexpr int kFullD = 2 * kRounds, kEmptyD = kFullD + 2;
+  static constexpr int kFullY = kEmptyD + 2, kEmptyY = kFullY + kTiles;
+  static constexpr int kDoneY = kEmptyY + kTiles;            // all sums are in y
+  static constexpr int kNumBars = kDoneY + kTiles;
+  __device__ static int count(int i) {
+    return (i >= kEmptyD && i < kFullY) || i >= kDoneY ? kExSoftWarps : 1;
   }
-  uint2 b[KK][4];
-  int held = __shfl_sync(0xffffffffu, mine[0], 0);
-  if (held >= 0) load_b<KK>(a, held, n0, b);
-  pipe::pdl_wait();
-  pipe::pdl_trigger();
-  const int step = u_stride(a.R16);
-  const int pieces = a.R16 / 8;  // of 16 bytes a row
-  for (int i = threadIdx.x; i < min(kRows, a.M - row0) * pieces; i += kLoraThreads) {
-    const int r = i / pieces, c = (i - r * pieces) * 8;
-    const int64_t from = int64_t(row0 + r) * a.R16 + c;
-    *reinterpret_cast<uint4 *>(&s_u[0][r * step + c]) =
-        __ldcg(reinterpret_cast<const uint4 *>(a.u_hi + from));
-    *reinterpret_cast<uint4 *>(&s_u[1][r * step + c]) =
-        __ldcg(reinterpret_cast<const uint4 *>(a.u_lo + from));
-  }
-  __syncthreads();
-  if (n0 >= a.N) return;
+  static constexpr uint32_t kTmem = kBars + kNumBars * 8;
+  static constexpr uint32_t kSmem = kTmem + 16 + 1024;
+  static_assert(kSmem <= 227 * 1024, "shared memory");
+};
+
+// The rounds of a tile: its distinct adapters in the order of their first rows.
+// The numbers are asked for a tile ahead.
+struct Rounds {
+  int ids[4], ahead[4];  // of rows lane, lane + 32, ..
+  unsigned left[4];
+  __device__ __forceinline__ void load(const LoraArgs &a, int row0) {
 #pragma unroll
-  for (int i = 0; i < kLoraTiles; ++i) {
-    unsigned left = __ballot_sync(0xffffffffu, mine[i] >= 0), rows;
-    const int at = (i * kLoraRows + fr) * step;
-    float c[4][4] = {};
-    int id;
-    while (next_adapter(mine[i], left, id, rows)) {
-      if (id != held) {
-        load_b<KK>(a, id, n0, b);
-        held = id;
+    for (int j = 0; j < 4; ++j) {
+      const int row = row0 + 32 * j + int(threadIdx.x & 31);
+      ahead[j] = row < a.M ? __ldcg(a.adapter + row) : -1;
+    }
+  }
+  // those that load() asked for; `next`: the next tile's first row
+  __device__ __forceinline__ void begin(const LoraArgs &a, int next, bool report) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      ids[j] = ahead[j];
+      if (ids[j] < -1 || ids[j] >= a.n_adapters) {
+        if (report) atomicOr(a.err, kLoraErr);
+        ids[j] = -1;
       }
-      float p[4][4];
-      multiply<KK>(a, b, s_u[0] + at, s_u[1] + at, 8 * step,
-                   [](const __nv_bfloat16 *q) {
-                     return *reinterpret_cast<const uint2 *>(q);
-                   },
-                   p);
-      keep_rows(rows, p, c);
+      left[j] = __ballot_sync(0xffffffffu, ids[j] >= 0);
     }
+    load(a, next);
+  }
+  __device__ __forceinline__ bool next(int &id) {
+    int j = 0;
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      const float v[8] = {c[0][2 * half], c[0][2 * half + 1], c[1][2 * half],
-                          c[1][2 * half + 1], c[2][2 * half], c[2][2 * half + 1],
-                          c[3][2 * half], c[3][2 * half + 1]};
-      store_row<Vec>(a, row0 + i * kLoraRows + fr + 8 * half, n0 + 8 * fc,
-                     y[i][half], v);
+    for (int k = 3; k >= 0; --k)
+      if (left[k]) j = k;
+    unsigned first = left[0];
+    int mine = ids[0];
+#pragma unroll
+    for (int k = 1; k < 4; ++k)
+      if (j == k) first = left[k], mine = ids[k];
+    if (!first) return false;
+    id = __shfl_sync(0xffffffffu, mine, __ffs(int(first)) - 1);
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      left[k] &= ~__ballot_sync(0xffffffffu, ids[k] == id);
+    return true;
+  }
+};
+
+__device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *map,
+                                            int c0, int c1, int c2,
+                                            uint64_t *bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_"
+      "tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_addr(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2),
+      "r"(smem_addr(bar))
+      : "memory");
+}
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap *map, int c0,
+                                             int c1, const void *src) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group "
+      "[%0, {%1, %2}], [%3];" ::"l"(reinterpret_cast<uint64_t>(map)),
+      "r"(c0), "r"(c1), "r"(smem_addr(src))
+      : "memory");
+}
+// Operands in bf16, fp32 accumulators, M = 128, N = kExCols, both K-major.
+constexpr uint32_t kExIdesc = (1u << 4) | (1u << 7) | (1u << 10) |
+                              (uint32_t(kExCols >> 3) << 17) |
+                              (uint32_t(128 >> 4) << 24);
+
+template <int KK>
+__global__ void __launch_bounds__(kExThreads, 1)
+lora_expand_kernel(const LoraArgs a, const __grid_constant__ CUtensorMap umap,
+                   const __grid_constant__ CUtensorMap bmap,
+                   const __grid_constant__ CUtensorMap ymap,
+                   const __grid_constant__ CUtensorMap omap) {
+  using C = ExpandCfg<KK>;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t *smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
+  uint64_t *bar = reinterpret_cast<uint64_t *>(smem + C::kBars);
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::kTmem);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr int kCopyWarp = kExSoftWarps, kMmaWarp = kExSoftWarps + 1,
+                kOutWarp = kExSoftWarps + 2;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < C::kNumBars; ++i)
+      mbar_init(&bar[i], C::count(i));
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == kMmaWarp) tmem_alloc(tmem_slot, 2 * kExCols);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const int col_tiles = (a.N + kExCols - 1) / kExCols;
+  const int tiles = (a.M + kExRows - 1) / kExRows * col_tiles;  // below 2^23
+  // After a wait that runs out (never expected; reported) a role waits no more,
+  // issues nothing more and leaves.
+  bool ok = true;
+  auto wait = [&](int b, int phase) {
+    if (ok && !warp_wait(&bar[b], uint32_t(phase) & 1u)) {
+      if (lane == 0) atomicOr(a.err, 4u);
+      ok = false;
     }
+    return ok;
+  };
+  int round = 0, tile_k = 0;  // so far
+  Rounds rounds;
+  int id;
+  auto row_of = [&](int t) { return t / col_tiles * kExRows; };
+  rounds.load(a, row_of(blockIdx.x));
+
+  if (warp == kCopyWarp) {
+    bool waited = false;
+    for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x, ++tile_k) {
+      const int row0 = row_of(t), n0 = t % col_tiles * kExCols;
+      const int yb = tile_k % C::kTiles, yr = tile_k / C::kTiles;
+      if (yr > 0 && !wait(C::kEmptyY + yb, yr - 1)) break;
+      if (lane == 0) {
+        // (whole boxes count, what lies outside reads as zeros)
+        mbar_arrive_expect_tx(&bar[C::kFullY + yb], C::kY);
+        for (int h = 0; h < 2; ++h)
+          tma_load_2d(smem + C::kYAt + yb * C::kY + h * C::kBlock, &ymap,
+                      n0 + 64 * h, row0, &bar[C::kFullY + yb]);
+      }
+      __syncwarp();
+      rounds.begin(a, row_of(t + gridDim.x), true);
+      while (rounds.next(id)) {
+        const int s = round % C::kRounds, r = round / C::kRounds;
+        if (r > 0 && !wait(C::kEmptyR + s, r - 1)) break;
+        if (!waited) {  // for u
+          pdl_wait();
+          pdl_trigger();
+          waited = true;
+        }
+        if (lane == 0) {
+          uint8_t *to = smem + s * C::kRound;
+          const int u_blocks = (2 * a.R16 + 63) / 64, b_blocks = (a.R + 63) / 64;
+          mbar_arrive_expect_tx(&bar[C::kFullR + s],
+                                uint32_t(u_blocks + b_blocks) * C::kBlock);
+          for (int h = 0; h < u_blocks; ++h)
+            tma_load_2d(to + h * C::kBlock, &umap, 64 * h, row0, &bar[C::kFullR + s]);
+          for (int h = 0; h < b_blocks; ++h)
+            tma_load_3d(to + (C::kUBlocks + h) * C::kBlock, &bmap, 64 * h, n0, id,
+                        &bar[C::kFullR + s]);
+        }
+        __syncwarp();
+        ++round;
+      }
+    }
+    if (!waited) pdl_wait();
+    if (!ok) {  // what is in flight lands first
+      bool landed = true;
+      for (int i = max(0, tile_k - C::kTiles); i < tile_k; ++i)
+        landed &= warp_wait(&bar[C::kFullY + i % C::kTiles],
+                            uint32_t(i / C::kTiles) & 1u);
+      for (int i = max(0, round - C::kRounds); i < round; ++i)
+        landed &= warp_wait(&bar[C::kFullR + i % C::kRounds],
+                            uint32_t(i / C::kRounds) & 1u);
+      if (!landed && lane == 0) atomicOr(a.err, 2u);
+    }
+  } else if (warp == kMmaWarp) {
+    for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
+      rounds.begin(a, row_of(t + gridDim.x), false);
+      while (ok && rounds.next(id)) {
+        const int s = round % C::kRounds, d = round & 1;
+        if (round >= 2) wait(C::kEmptyD + d, (round >> 1) - 1);
+        if (!wait(C::kFullR + s, round / C::kRounds)) break;
+        tc_fence_after();
+        if (elect_one()) {
+          const uint32_t base = smem_addr(smem + s * C::kRound);
+          const int steps = a.R16 / 16;
+#pragma unroll 1
+          for (int k = 0; k < 2 * steps; ++k) {
+            // U's step k against B's step k mod `steps`
+            const int kb = k < steps ? k : k - steps;
+            tc_mma_ss(tmem + d * kExCols,
+                      sw128_desc(base + (k >> 2) * C::kBlock) + uint64_t((k & 3) * 2),
+                      sw128_desc(base + (C::kUBlocks + (kb >> 2)) * C::kBlock) +
+                          uint64_t((kb & 3) * 2),
+                      kExIdesc, k > 0);
+          }
+          tc_commit(&bar[C::kEmptyR + s]);
+          tc_commit(&bar[C::kFullD + d]);
+        }
+        __syncwarp();
+        ++round;
+      }
+    }
+    // (the accumulators are not given back before the last products are done)
+    for (int i = max(0, round - 2); i < round; ++i)
+      wait(C::kFullD + (i & 1), i >> 1);
+  } else if (warp == kOutWarp) {
+    for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x, ++tile_k) {
+      const int n0 = t % col_tiles * kExCols, yb = tile_k % C::kTiles;
+      if (!wait(C::kDoneY + yb, tile_k / C::kTiles)) break;
+      if (lane == 0) {
+        for (int h = 0; h < 2; ++h)
+          if (n0 + 64 * h < a.N)
+            tma_store_2d(&omap, n0 + 64 * h, row_of(t),
+                         smem + C::kYAt + yb * C::kY + h * C::kBlock);
+        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+        asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+        mbar_arrive(&bar[C::kEmptyY + yb]);
+      }
+      __syncwarp();
+    }
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    __syncwarp();
+  } else {
+    const int quarter = warp & 3, half = warp >> 2;  // of rows, of columns
+    const int r = quarter * 32 + lane;
+    const uint32_t t_lane = tmem + (uint32_t(quarter * 32) << 16) + half * 64;
+    for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x, ++tile_k) {
+      const int yb = tile_k % C::kTiles;
+      uint8_t *row = smem + C::kYAt + yb * C::kY + half * C::kBlock + r * 128;
+      rounds.begin(a, row_of(t + gridDim.x), false);
+      const int mine = quarter == 0 ? rounds.ids[0] : quarter == 1 ? rounds.ids[1]
+                       : quarter == 2 ? rounds.ids[2] : rounds.ids[3];
+      wait(C::kFullY + yb, tile_k / C::kTiles);
+      while (ok && rounds.next(id)) {
+        const int d = round & 1;
+        wait(C::kFullD + d, round >> 1);
+        tc_fence_after();
+        if (ok && __any_sync(0xffffffffu, mine == id)) {
+          float v[64];
+          tmem_ld32_issue(t_lane + d * kExCols, v);
+          tmem_ld32_issue(t_lane + d * kExCols + 32, v + 32);
+          tmem_landed(v);
+          tmem_landed(v + 32);
+          if (mine == id) {
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+              uint4 *at = reinterpret_cast<uint4 *>(row + ((c ^ (r & 7)) << 4));
+              const uint4 w = *at;
+              const float *p = v + 8 * c;
+              *at = make_uint4(pair_of(low_of(w.x) + p[0], high_of(w.x) + p[1]),
+                               pair_of(low_of(w.y) + p[2], high_of(w.y) + p[3]),
+                               pair_of(low_of(w.z) + p[4], high_of(w.z) + p[5]),
+                               pair_of(low_of(w.w) + p[6], high_of(w.w) + p[7]));
+            }
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar[C::kEmptyD + d]);
+        ++round;
+      }
+      if (!ok) break;
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar[C::kDoneY + yb]);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();  // every tensor-memory access is done
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 2 * kExCols);
   }
 }
 
 bool aligned_to(const void *p, uintptr_t a) {
   return reinterpret_cast<uintptr_t>(p) % a == 0;
+}
+
+template <int KK>
+cudaError_t launch_expand(const LoraArgs &a, cudaLaunchConfig_t &cfg) {
+  using C = ExpandCfg<KK>;
+  CUtensorMap umap, bmap, ymap, omap;
+  const auto bf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  const auto sw = CU_TENSOR_MAP_SWIZZLE_128B;
+  PFN_cuTensorMapEncodeTiled_v12000 fn = tensor_map_encoder();
+  if (!fn) return cudaErrorInvalidValue;
+  const cuuint64_t dims[3] = {cuuint64_t(a.R), cuuint64_t(a.N),
+                              cuuint64_t(a.n_adapters)};
+  const cuuint64_t strides[2] = {cuuint64_t(a.R) * 2,
+                                 cuuint64_t(a.R) * 2 * cuuint64_t(a.N)};
+  const cuuint32_t box[3] = {64, kExCols, 1}, elem[3] = {1, 1, 1};
+  if (!encode_2d(&umap, bf16, a.u_hi, uint64_t(a.u_ld), uint64_t(a.M),
+                 uint64_t(a.u_ld) * 2, 64, kExRows, sw) ||
+      !encode_2d(&ymap, bf16, a.y, uint64_t(a.N), uint64_t(a.M),
+                 uint64_t(a.y_ld) * 2, 64, kExRows, sw) ||
+      !encode_2d(&omap, bf16, a.out, uint64_t(a.N), uint64_t(a.M),
+                 uint64_t(a.out_ld) * 2, 64, kExRows, sw) ||
+      fn(&bmap, bf16, 3, const_cast<__nv_bfloat16 *>(a.B), dims, strides, box, elem,
+         CU_TENSOR_MAP_INTERLEAVE_NONE, sw, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    return cudaErrorInvalidValue;
+  const cudaError_t e = cudaFuncSetAttribute(
+      lora_expand_kernel<KK>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+      int(C::kSmem));
+  if (e != cudaSuccess) return e;
+  const int tiles = (a.M + kExRows - 1) / kExRows * ((a.N + kExCols - 1) / kExCols);
+  cfg.gridDim = dim3(unsigned(std::min(tiles, std::max(1, device_sm_count()))));
+  cfg.blockDim = dim3(kExThreads);
+  cfg.dynamicSmemBytes = C::kSmem;
+  return cudaLaunchKernelEx(&cfg, lora_expand_kernel<KK>, a, umap, bmap, ymap, omap);
 }
 
 }  // namespace
@@ -478,8 +736,13 @@ cudaError_t launch_lora(const LoraLaunch &l, cudaStream_t stream) {
   a.y_ld = l.y_ld;
   a.out = l.out;
   a.out_ld = l.out_ld;
+  // (strides below 2^40 bytes are the tiled copies' limit)
+  const bool vec = l.y_ld % 8 == 0 && l.out_ld % 8 == 0 &&
+                   aligned_to(l.y, 16) && aligned_to(l.out, 16);
+  const bool tc = vec && l.M >= kLoraTcRows && int64_t(a.R) * l.N < (int64_t(1) << 38);
   a.u_hi = static_cast<__nv_bfloat16 *>(l.workspace);
-  a.u_lo = a.u_hi + int64_t(l.M) * a.R16;
+  a.u_lo = tc ? a.u_hi + a.R16 : a.u_hi + int64_t(l.M) * a.R16;
+  a.u_ld = tc ? 2 * a.R16 : a.R16;
   a.err = device_error_word();
   if (!a.err) return cudaErrorInvalidSymbol;
   cudaLaunchConfig_t cfg = {};
@@ -509,15 +772,13 @@ cudaError_t launch_lora(const LoraLaunch &l, cudaStream_t stream) {
                     : shrink(lora_shrink_kernel<8, 8, 2, true>,
                              lora_shrink_kernel<8, 8, 2, false>, 8, 8, 2u);
   if (e != cudaSuccess) return e;
-  const bool vec = l.y_ld % 8 == 0 && l.out_ld % 8 == 0 &&
-                   aligned_to(l.y, 16) && aligned_to(l.out, 16);
   auto expand = [&](auto whole, auto any) {
     return vec ? cudaLaunchKernelEx(&cfg, whole, a)
                : cudaLaunchKernelEx(&cfg, any, a);
   };
   cfg.blockDim = dim3(kLoraThreads);
   const int kk = a.R16 / 16;
-  if (few) {
+  if (!tc) {
     cfg.gridDim = dim3(unsigned((l.N + 31) / 32), tiles);
     if (kk <= 1)
       return expand(lora_expand_few_kernel<1, true>, lora_expand_few_kernel<1, false>);
@@ -527,13 +788,9 @@ cudaError_t launch_lora(const LoraLaunch &l, cudaStream_t stream) {
       return expand(lora_expand_few_kernel<4, true>, lora_expand_few_kernel<4, false>);
     return expand(lora_expand_few_kernel<8, true>, lora_expand_few_kernel<8, false>);
   }
-  cfg.gridDim = dim3(unsigned((l.N + 32 * kLoraWarps - 1) / (32 * kLoraWarps)),
-                     (tiles + kLoraTiles - 1) / kLoraTiles);
-  if (kk <= 2)
-    return expand(lora_expand_kernel<2, true>, lora_expand_kernel<2, false>);
-  if (kk <= 4)
-    return expand(lora_expand_kernel<4, true>, lora_expand_kernel<4, false>);
-  return expand(lora_expand_kernel<8, true>, lora_expand_kernel<8, false>);
+  return kk <= 2   ? launch_expand<2>(a, cfg)
+         : kk <= 4 ? launch_expand<4>(a, cfg)
+                   : launch_expand<8>(a, cfg);
 }
 
 }  // namespace bw

@@ -148,18 +148,6 @@ __host__ __device__ constexpr uint32_t pf_idesc(int n, bool b_transposed) {
          (uint32_t(128 >> 4) << 24);
 }
 
-// D (tmem) (+)= A (smem) B (smem).
-__device__ __forceinline__ void tc_mma_ss(uint32_t d, uint64_t adesc,
-                                          uint64_t bdesc, uint32_t idesc,
-                                          uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-
 // Transposed B in the 128-byte swizzle: 64 n by 8 k blocks of 1024 bytes,
 // the next 8 k 1024 bytes on, the next 64 n `half` bytes on.
 __device__ __forceinline__ uint64_t sw128_desc_t(uint32_t addr, uint32_t half) {
@@ -169,39 +157,6 @@ __device__ __forceinline__ uint64_t sw128_desc_t(uint32_t addr, uint32_t half) {
   d |= uint64_t(1) << 46;
   d |= uint64_t(2) << 61;
   return d;
-}
-
-// 32 columns of this warp's lanes; the values may be used only after
-// tmem_landed on them.
-__device__ __forceinline__ void tmem_ld32_issue(uint32_t taddr, float *v) {
-  uint32_t *r = reinterpret_cast<uint32_t *>(v);
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, "
-      "%30, %31}, [%32];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]),
-        "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
-        "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
-        "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
-        "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]),
-        "=r"(r[30]), "=r"(r[31])
-      : "r"(taddr)
-      : "memory");
-}
-// Waits for this thread's tensor-memory loads; v is tied to the wait.
-__device__ __forceinline__ void tmem_landed(float *v) {
-  uint32_t *r = reinterpret_cast<uint32_t *>(v);
-  asm volatile(
-      "tcgen05.wait::ld.sync.aligned;"
-      : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]),
-        "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]),
-        "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
-        "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]),
-        "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]),
-        "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
-        "+r"(r[30]), "+r"(r[31])::"memory");
 }
 
 // Bits 0 .. n - 1 (none for n <= 0, all for n >= 32).

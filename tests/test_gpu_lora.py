@@ -98,6 +98,10 @@ CASES = [
     (300, 1021, 68, 40, 20),
     (333, 513, 1028, 128, 3),
     (1000, 256, 512, 16, 2),
+    (513, 8, 64, 8, 3),
+    (640, 136, 260, 24, 40),
+    (700, 200, 132, 128, 9),
+    (1025, 2568, 512, 64, 3),
 ]
 
 
@@ -111,14 +115,14 @@ def test_mixed_rows(bw, M, N, K, R, n, scaled):
     assert bw.bw_device_error() == 0
 
 
-@pytest.mark.parametrize("M", [64, 512, 4096])
+@pytest.mark.parametrize("M", [64, 512, 600, 4096])
 def test_rows_by_request(bw, M):
     """Requests one after the other, as prompts lie in a batch."""
     c = Case(M, M, 200, 128, 32, 6, ids=np.arange(M) * 6 // M)
     c.check(c.run(bw, out=torch.empty_like(c.y)))
 
 
-@pytest.mark.parametrize("M", [40, 400])
+@pytest.mark.parametrize("M", [40, 400, 530])
 @pytest.mark.parametrize("off,pad", [(0, 24), (8, 0), (3, 2)])
 def test_columns_of_a_fused_projection(bw, M, off, pad):
     """In place and into columns of a wider buffer; the others stay."""
@@ -135,7 +139,7 @@ def test_columns_of_a_fused_projection(bw, M, off, pad):
     assert (out[:, 72:] == 5.0).all()
 
 
-@pytest.mark.parametrize("M", [20, 300])
+@pytest.mark.parametrize("M", [20, 300, 520])
 def test_rows_without_an_adapter(bw, M):
     c = Case(M, M, 64, 64, 16, 4, ids=np.full(M, -1))
     out = torch.zeros_like(c.y)
@@ -146,7 +150,7 @@ def test_rows_without_an_adapter(bw, M):
     assert torch.equal(c.y, kept)
 
 
-@pytest.mark.parametrize("M", [20, 300])
+@pytest.mark.parametrize("M", [20, 300, 520])
 def test_bad_adapter_numbers(bw, M):
     """Reported, and those rows are as without one."""
     c = Case(M, M, 64, 64, 16, 4)
@@ -162,7 +166,7 @@ def test_bad_adapter_numbers(bw, M):
     assert torch.equal(out[[0, 3, M - 1, 7]], c.y[[0, 3, M - 1, 7]])
 
 
-@pytest.mark.parametrize("M", [20, 300])
+@pytest.mark.parametrize("M", [20, 300, 520])
 def test_what_is_not_finite_stays_in_its_rows(bw, M):
     c = Case(M, M, 64, 64, 16, 4, ids=np.arange(M) % 4)
     c.A[1, 3, 5] = float("nan")
@@ -186,23 +190,24 @@ def test_inputs_at_odd_places(bw):
     c.check(c.run(bw, out=torch.empty_like(c.y)))
 
 
-def test_far_adapters(bw):
+@pytest.mark.parametrize("M", [18, 520])
+def test_far_adapters(bw, M):
     """Offsets beyond 32 bits: 40000 adapters of 128 x 516."""
     n, R, K, N = 40000, 128, 516, 8
     torch.cuda.empty_cache()
-    c = Case(5, 18, N, K, R, 1, ids=np.zeros(18))
+    c = Case(5, M, N, K, R, 1, ids=np.zeros(M))
     A = torch.empty((n, R, K), dtype=torch.bfloat16, device="cuda")
     B = torch.empty((n, N, R), dtype=torch.bfloat16, device="cuda")
     A[n - 1], B[n - 1] = c.A[0], c.B[0]
     scale = torch.zeros(n, device="cuda")
     scale[n - 1] = c.scale[0]
-    ids = torch.full((18,), n - 1, dtype=torch.int32, device="cuda")
+    ids = torch.full((M,), n - 1, dtype=torch.int32, device="cuda")
     out = bw.bw_lora_add(c.y, c.x, c.s, A, B, ids, scale=scale,
                          out=torch.empty_like(c.y))
     c.check(out)
 
 
-@pytest.mark.parametrize("M", [30, 300])
+@pytest.mark.parametrize("M", [30, 300, 600])
 def test_captured_and_on_another_stream(bw, M):
     """A replayed graph follows the adapter numbers on the device."""
     c = Case(M, M, 96, 128, 16, 9)
