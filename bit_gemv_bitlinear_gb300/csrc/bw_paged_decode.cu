@@ -76,6 +76,8 @@ struct DecodeArgs {
   int box_rows;
   const int *shared_len;  // positions that are not visited here; or null
   int shared_pages;
+  int shared_items;
+  SharedRates rates;  // how the prefix shares the SMs
   // (the view that their number is checked against)
   __device__ PagedView shared_v() const {
     PagedView s = v;
@@ -177,12 +179,18 @@ __device__ __forceinline__ TilePlan seq_plan(int len, int window, int sinks,
   return tile_plan(len - 1, len - 1, window, sinks, kDcTile);
 }
 
-// A (sequence, head) and its tiles.
+// A (sequence, head) and its tiles.  Behind a shared prefix (shared >= 0) items
+// are short, and one takes a CTA about as long to begin and to end as a tile:
+// it counts one tile more, its first, which is not visited.  (64 sequences of up
+// to 500 positions: CTAs of 8 tiles took 12 to 22 us by their 1 to 6 items.)
 struct Item {
   int b, g, len;
   TilePlan plan;
   int64_t first;  // first tile of the item
 };
+__device__ __forceinline__ int counted(const TilePlan &p, int shared) {
+  return p.n > 0 && shared >= 0 ? p.n + 1 : p.n;
+}
 
 // Where the sequences begin, for one warp: entry t = 32 k + lane is the first
 // tile of sequences t per and on, and the first one's length.
@@ -212,10 +220,11 @@ __device__ __forceinline__ bool item_at(const DecodeArgs &a, const Begins &bg,
   for (it.b = b0; it.b < a.v.n_seqs; ++it.b) {
     it.len = it.b == b0 ? len : seq_len(a.v, it.b);
     it.plan = seq_plan(it.len, a.window, a.sinks, shared);
-    const int64_t tiles = int64_t(it.plan.n) * a.v.hkv;
+    const int n = counted(it.plan, shared);
+    const int64_t tiles = int64_t(n) * a.v.hkv;
     if (at < base + tiles) {
-      it.g = int(at - base) / it.plan.n;  // below 2^24
-      it.first = base + int64_t(it.g) * it.plan.n;
+      it.g = int(at - base) / n;  // below 2^24
+      it.first = base + int64_t(it.g) * n;
       return true;
     }
     base += tiles;
@@ -224,7 +233,7 @@ __device__ __forceinline__ bool item_at(const DecodeArgs &a, const Begins &bg,
 }
 __device__ __forceinline__ bool item_next(const DecodeArgs &a, int shared,
                                           Item &it) {
-  it.first += it.plan.n;
+  it.first += counted(it.plan, shared);
   if (++it.g < a.v.hkv) return true;
   it.g = 0;
   for (++it.b; it.b < a.v.n_seqs; ++it.b) {
@@ -282,7 +291,7 @@ decode_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap kmap,
   for (int b = b_lo; b < b_hi; ++b) {
     const int len = seq_len(a.v, b);
     if (b == b_lo) s_len0[tid] = len;
-    const int tiles = seq_plan(len, a.window, a.sinks, shared).n;
+    const int tiles = counted(seq_plan(len, a.window, a.sinks, shared), shared);
     mine += int64_t(tiles) * a.v.hkv;
     if (tiles == 0 && b % int(gridDim.x) == int(blockIdx.x)) {
       for (int g = 0; g < a.v.hkv; ++g)
@@ -316,7 +325,14 @@ decode_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap kmap,
     total += s_sum[w];
   }
   s_before[tid] = before;
-  const Dealing dl = deal(total, int(gridDim.x), GH == 1);
+  int ctas = gridDim.x;
+  if constexpr (Shared) {
+    // the SMs that the prefix leaves (CTAs begin in their order)
+    const int n = shared_split(
+        a.shared_items, shared, float(total), a.rates);
+    if (n > 0) ctas = min(ctas, max(1, (a.rates.sms - n) * C::kCtas));
+  }
+  const Dealing dl = deal(total, ctas, GH == 1);
   if (int(blockIdx.x) >= dl.n_ctas) {  // the whole CTA
     if (Shared) pdl_wait();
     return;
@@ -343,6 +359,7 @@ decode_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap kmap,
     auto stage_free = [&] {
       return round == 0 || warp_wait(&empty[stage], (round - 1) & 1u);
     };
+    constexpr int kMore = Shared ? 1 : 0;  // tiles of an item that are not visited
     Begins bg;
 #pragma unroll
     for (int k = 0; k < Begins::kPer; ++k) {
@@ -371,7 +388,7 @@ decode_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap kmap,
       unit_range(dl, unit, &w.t, &w.end);
       if (w.t >= dl.total) return 0;
       if (!item_at(a, bg, w.t, shared, w.it)) return -1;
-      load_pages(w, tile_pos(w.it.plan, int(w.t - w.it.first), kDcTile) >>
+      load_pages(w, tile_pos(w.it.plan, max(0, int(w.t - w.it.first) - kMore), kDcTile) >>
                         a.v.page_shift);
       return 1;
     };
@@ -397,59 +414,61 @@ decode_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap kmap,
       };
       int unit0 = 0, parts = 0;  // of the item
       auto count_parts = [&] {
-        unit0 = unit_of(dl, w.it.first);
-        parts = unit_of(dl, w.it.first + w.it.plan.n - 1) - unit0 + 1;
+        unit0 = unit_of(dl, w.it.first + kMore);
+        parts = unit_of(dl, w.it.first + kMore + w.it.plan.n - 1) - unit0 + 1;
       };
       count_parts();
       bool new_part = true;
       for (;;) {
         if (dynamic && w.t == claim_at && lane == 0) claimed = atomicAdd(a.claim, 1u);
-        const int pos = tile_pos(w.it.plan, int(w.t - w.it.first), kDcTile);
-        const int p0 = pos >> a.v.page_shift;
-        if (w.pg_b != w.it.b || p0 < w.pg0 ||
-            ((pos + kDcTile - 1) >> a.v.page_shift) >= w.pg0 + 32)
-          load_pages(w, p0);
-        // A box that nobody sees and a bad page read as zeros (a page past the
-        // pool); only an entry that is used is looked at.
-        int page = __shfl_sync(0xffffffffu, w.pg,
-                               ((pos + r0) >> a.v.page_shift) - w.pg0);
-        const bool used = pos + r0 < w.it.plan.s1 ||
-                          (pos + r0 < w.it.len && pos + r0 + a.box_rows > w.it.plan.lo);
-        if (page < 0 || page >= a.v.n_pages || !used) {
-          if (used && mine_box) atomicOr(a.v.err, kPagedErr);
-          page = a.v.n_pages;
-        }
-        ok = stage_free() &&
-             (!new_part || part == 0 || warp_wait(q_read, uint32_t(part - 1) & 1u));
-        if (!ok) break;
-        if (lane == 0) {
-          info[stage] = DcTileInfo{w.unit, w.it.b, w.it.g, w.it.len, pos,
-                                   w.t == w.it.first, w.it.plan.s1, w.it.plan.lo,
-                                   unit0, parts, {}};
-          const uint32_t q_bytes = new_part ? uint32_t(a.G) * D * 2 : 0u;
-          mbar_arrive_expect_tx(&full[stage], C::kStage + q_bytes);
-          // The queries come with the part's first tile, once for the CTA: read
-          // by every warp of every CTA, the one row of a long sequence was a
-          // hot spot that doubled the call's time.
-          if (new_part)
-            bulk_copy_g2s(smem + C::kQ,
-                          a.q + int64_t(w.it.b) * a.q_ld + int64_t(w.it.g) * a.G * D,
-                          q_bytes, &full[stage]);
-        }
-        part += new_part;
-        new_part = false;
-        __syncwarp();
-        if (mine_box)
-          tma_load_4d_once(smem + stage * C::kStage + dst, is_v ? &vmap : &kmap,
-                           half * 64, (pos + r0) & ((1 << a.v.page_shift) - 1),
-                           w.it.g, page, &full[stage], once);
-        if (++stage == C::kStages) {
-          stage = 0;
-          ++round;
+        if (!Shared || w.t != w.it.first) {
+          const int pos = tile_pos(w.it.plan, int(w.t - w.it.first) - kMore, kDcTile);
+          const int p0 = pos >> a.v.page_shift;
+          if (w.pg_b != w.it.b || p0 < w.pg0 ||
+              ((pos + kDcTile - 1) >> a.v.page_shift) >= w.pg0 + 32)
+            load_pages(w, p0);
+          // A box that nobody sees and a bad page read as zeros (a page past the
+          // pool); only an entry that is used is looked at.
+          int page = __shfl_sync(0xffffffffu, w.pg,
+                                 ((pos + r0) >> a.v.page_shift) - w.pg0);
+          const bool used = pos + r0 < w.it.plan.s1 ||
+                            (pos + r0 < w.it.len && pos + r0 + a.box_rows > w.it.plan.lo);
+          if (page < 0 || page >= a.v.n_pages || !used) {
+            if (used && mine_box) atomicOr(a.v.err, kPagedErr);
+            page = a.v.n_pages;
+          }
+          ok = stage_free() &&
+               (!new_part || part == 0 || warp_wait(q_read, uint32_t(part - 1) & 1u));
+          if (!ok) break;
+          if (lane == 0) {
+            info[stage] = DcTileInfo{w.unit, w.it.b, w.it.g, w.it.len, pos,
+                                     w.t == w.it.first + kMore, w.it.plan.s1, w.it.plan.lo,
+                                     unit0, parts, {}};
+            const uint32_t q_bytes = new_part ? uint32_t(a.G) * D * 2 : 0u;
+            mbar_arrive_expect_tx(&full[stage], C::kStage + q_bytes);
+            // The queries come with the part's first tile, once for the CTA: read
+            // by every warp of every CTA, the one row of a long sequence was a
+            // hot spot that doubled the call's time.
+            if (new_part)
+              bulk_copy_g2s(smem + C::kQ,
+                            a.q + int64_t(w.it.b) * a.q_ld + int64_t(w.it.g) * a.G * D,
+                            q_bytes, &full[stage]);
+          }
+          part += new_part;
+          new_part = false;
+          __syncwarp();
+          if (mine_box)
+            tma_load_4d_once(smem + stage * C::kStage + dst, is_v ? &vmap : &kmap,
+                             half * 64, (pos + r0) & ((1 << a.v.page_shift) - 1),
+                             w.it.g, page, &full[stage], once);
+          if (++stage == C::kStages) {
+            stage = 0;
+            ++round;
+          }
         }
         if (dynamic && w.t == claim_at + 1) find_next();
         if (++w.t == w.end) break;
-        if (w.t >= w.it.first + w.it.plan.n) {
+        if (w.t >= w.it.first + w.it.plan.n + kMore) {
           if (!item_next(a, shared, w.it)) {
             ok = false;
             break;
@@ -990,6 +1009,11 @@ cudaError_t launch_paged_decode(const PagedView &v, const PagedAttnLaunch &l,
       rest + dc_part_bytes(a.G, l.D, l.shared_len ? size_t(v.n_seqs) * v.hkv : 0));
   a.shared_len = l.shared_len;
   a.shared_pages = l.shared_pages;
+  if (l.shared_len) {
+    const SharedCut cut = shared_cut(v.n_seqs, a.G, v.hkv);
+    a.shared_items = cut.items;
+    a.rates = shared_rates(l.D, cut.seqs > kPfRows / a.G, device_sm_count());
+  }
   a.scale2 = l.scale * kLog2e;
   a.window = l.window;
   a.sinks = l.sinks;

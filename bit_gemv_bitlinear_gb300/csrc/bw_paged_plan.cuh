@@ -8,6 +8,7 @@
 // §六 item 2 (a preallocated KV cache, the position read on the device).
 #pragma once
 
+#include <cmath>
 #include <cstdint>
 
 #ifdef __CUDACC__
@@ -175,27 +176,115 @@ BW_PLAN_FN SharedCut shared_cut(int n_seqs, int G, int Hkv) {
 BW_PLAN_FN int shared_tiles(int shared) {
   return (shared + kPfTile - 1) / kPfTile;
 }
-// All items' tiles in one order, in equal contiguous shares of `n` CTAs.  The
-// part of item i that CTA c makes lies in slot i + c: along the order either
-// grows from part to part.
+// How the items' tiles are dealt to CTAs.  Where there are CTAs for all items,
+// each item is cut into `parts` (a CTA that begins a second item waits 6 us for
+// its first scores and makes a second part); else all items' tiles are dealt in
+// one order, in contiguous shares, as equal as whole tiles are.  A part lies in
+// slot c of its CTA in the one case, and in slot i + c of item i in the other:
+// along the order either grows from part to part.  (At most 2^31 tiles.)
 struct SharedDeal {
-  int64_t total;
-  int tiles, n;  // of an item; CTAs that have a share
-  BW_PLAN_FN_IN void share(int c, int64_t *lo, int64_t *hi) const {
-    *lo = c < n ? c * total / n : total;
-    *hi = c < n ? (c + 1) * total / n : total;
+  int tiles, n;         // of an item; CTAs that have a share
+  int parts;            // 0: in one order
+  uint32_t total, per, more;  // `more` CTAs have per + 1, the others per
+  // The first tile and the number of tiles of CTA c's share, tiles of all items
+  // counted in one order.
+  BW_PLAN_FN_IN void share(int c, uint32_t *lo, uint32_t *hi) const {
+    *lo = *hi = total;
+    if (c >= n) return;
+    const uint32_t u = uint32_t(c);
+    if (parts > 0) {
+      const uint32_t item = u / uint32_t(parts), s = u - item * uint32_t(parts);
+      const uint32_t t = uint32_t(tiles), p = uint32_t(parts);
+      const uint32_t each = t / p, big = t - each * p;
+      *lo = item * t + s * each + (s < big ? s : big);
+      *hi = *lo + each + (s < big);
+    } else {
+      *lo = u * per + (u < more ? u : more);
+      *hi = *lo + per + (u < more);
+    }
   }
-  // The CTA that has a tile.
-  BW_PLAN_FN_IN int owner(int64_t tile) const {
-    return int(((tile + 1) * n - 1) / total);
+  // The slots of item i's parts: first and number.
+  BW_PLAN_FN_IN void slots(int i, int *first, int *count) const {
+    if (parts > 0) {
+      *first = i * parts;
+      *count = parts;
+    } else {
+      const uint32_t t0 = uint32_t(i) * uint32_t(tiles);
+      const int c = owner(t0);
+      *first = i + c;
+      *count = owner(t0 + uint32_t(tiles) - 1) - c + 1;
+    }
+  }
+  BW_PLAN_FN_IN int slot(int i, int c) const { return parts > 0 ? c : i + c; }
+  // (in one order) the CTA that has a tile
+  BW_PLAN_FN_IN int owner(uint32_t tile) const {
+    const uint32_t large = more * (per + 1);
+    return int(tile < large ? tile / (per + 1) : more + (tile - large) / per);
   }
 };
-BW_PLAN_FN SharedDeal shared_deal(int items, int shared, int grid) {
+// For n CTAs at most; all of them have a share where n is shared_split's.
+BW_PLAN_FN SharedDeal shared_deal(int items, int shared, int n) {
   SharedDeal d{};
   d.tiles = shared_tiles(shared);
-  d.total = int64_t(items) * d.tiles;
-  d.n = d.total < grid ? int(d.total) : grid;
+  d.total = uint32_t(items) * uint32_t(d.tiles);
+  d.n = d.total < uint32_t(n) ? int(d.total) : n;
+  if (d.n >= items && d.n > 0) {
+    d.parts = d.n / items < d.tiles ? d.n / items : d.tiles;
+    d.n = d.parts * items;
+  } else if (d.n > 0) {
+    d.per = d.total / uint32_t(d.n);
+    d.more = d.total - d.per * uint32_t(d.n);
+  }
   return d;
+}
+// Key tiles of the positions behind the prefix of a sequence of `len`, for each
+// key-value head, as the decode kernel visits them.
+constexpr int kSharedOwnTile = 64;
+BW_PLAN_FN int shared_own_tiles(int len, int shared) {
+  return len > shared ? (len - 1) / kSharedOwnTile + 1 - shared / kSharedOwnTile : 0;
+}
+// The SMs that the prefix gets, of `sms`; the others are the decode kernel's, so
+// that both run at the same time.  Of a key tile of the prefix an SM has pre_us,
+// of what the decode kernel does (its tiles, and a beginning for each sequence's)
+// own_us; the prefix takes late_us longer to begin and to end.
+struct SharedRates {
+  int sms;
+  float pre_us, own_us, late_us;
+};
+BW_PLAN_FN float shared_time(const SharedRates &r, uint32_t turns, float own, int n) {
+  const float a = r.late_us + float(turns) * r.pre_us;
+  const float b = own * r.own_us / float(r.sms - n);
+  return a > b ? a : b;
+}
+BW_PLAN_FN int shared_split(int items, int shared, float own, const SharedRates &r) {
+  const uint32_t tiles = uint32_t(shared_tiles(shared));
+  const uint32_t pre = uint32_t(items) * tiles;
+  if (pre == 0) return 0;
+  if (own <= 0.0f || r.sms < 2) return pre < uint32_t(r.sms) ? int(pre) : r.sms;
+  // n with late + pre pre_us / n = own own_us / (sms - n)
+  const float a = float(pre) * r.pre_us, b = own * r.own_us, s = float(r.sms);
+  const float h = (a + b - r.late_us * s) / (2.0f * r.late_us);
+  const float x = sqrtf(h * h + a * s / r.late_us) - h;
+  int n = int(x + 0.5f);
+  n = n < 1 ? 1 : n > r.sms - 1 ? r.sms - 1 : n;
+  if (items > r.sms - 1 || items > n + n / 2) {
+    // in one order: as few as do it in the same number of turns
+    const uint32_t turns = (pre + uint32_t(n) - 1) / uint32_t(n);
+    n = int((pre + turns - 1) / turns);
+    return n < items ? n : items;
+  }
+  // whole parts: as many an item as that, or one more
+  const uint32_t most = uint32_t((r.sms - 1) / items) < tiles ? uint32_t((r.sms - 1) / items) : tiles;
+  uint32_t best = 0;
+  float least = 0.0f;
+  for (int k = n / items; k <= n / items + 1; ++k) {
+    uint32_t parts = k < 1 ? 1u : uint32_t(k) < most ? uint32_t(k) : most;
+    const uint32_t turns = (tiles + parts - 1) / parts;
+    parts = (tiles + turns - 1) / turns;
+    const float t = shared_time(r, turns, own, int(parts) * items);
+    if (best == 0 || t < least) best = parts, least = t;
+  }
+  return int(best) * items;
 }
 BW_PLAN_FN int shared_slots(const SharedCut &c, int grid) {
   return c.items + grid;

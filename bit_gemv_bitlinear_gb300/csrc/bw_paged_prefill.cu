@@ -79,7 +79,10 @@ struct PrefillArgs {
   int box_rows;
   int split;
   const int *shared_len;  // of a shared prefix (v.table: its pages); else null
-  int n_items;            // of a shared prefix, all key-value heads'
+  // of a shared prefix: all key-value heads' items, how it shares the SMs
+  int n_items, max_len;
+  SharedRates rates;
+  int *ctas;
 };
 
 template <int D>
@@ -372,9 +375,29 @@ prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap qmap,
   // (few sequences, the scheduler: one a lane)
   SeqTokens kept{0, 0, 0, false, false};
   int shared = 0;
+  // a shared prefix: this CTA's share of the tiles
+  SharedDeal deal{};
+  uint32_t at = 0, share_end = 0;
   if constexpr (Shared) {
+    // all sequences' tiles behind the prefix: how many SMs the decode kernel gets
     shared = shared_positions(a.v, a.shared_len);
     void_call = false;
+    int own = 0;
+    for (int b = tid; b < a.v.n_seqs; b += kPfThreads) {
+      const int len = __ldcg(a.v.len + b);
+      const int t = len <= a.max_len ? shared_own_tiles(len, shared) : 0;
+      own += t + (t > 0);  // below 2^24
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) own += __shfl_xor_sync(0xffffffffu, own, o);
+    if (lane == 0) before[warp] = own;
+    __syncthreads();
+    float all = 0.0f;
+    for (int w = 0; w < kPfThreads / 32; ++w) all += float(before[w]);
+    const int n = shared_split(a.n_items, shared, all * float(a.v.hkv), a.rates);
+    deal = shared_deal(a.n_items, shared, n);
+    deal.share(int(blockIdx.x), &at, &share_end);
+    if (blockIdx.x == 0 && tid == 0) *a.ctas = n;
   } else {
     const int b_lo = tid < kPfScan ? min(tid * per, a.v.n_seqs) : a.v.n_seqs;
     const int b_hi = min(b_lo + per, a.v.n_seqs);
@@ -414,8 +437,24 @@ prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap qmap,
       return pf_work(a, it);
   };
   // The next item, by every role but the scheduler: item k lies in slot k & 1.
+  // (Of a shared prefix every role finds them by itself: what is left of the
+  // share, to the end of its key-value head's tiles.)
   int k_item = 0;
   auto next_item = [&](PfItem &it) {
+    if constexpr (Shared) {
+      if (at >= share_end) return false;
+      const int item = int(at / uint32_t(deal.tiles));
+      const int x = item / a.v.hkv;
+      it.b = 0;
+      it.g = item - x * a.v.hkv;
+      it.s = deal.slot(item, int(blockIdx.x));
+      it.row0 = x * a.TI;
+      it.n_tok = min(a.TI, a.n_tokens - it.row0);
+      it.pos0 = int(at - uint32_t(item) * uint32_t(deal.tiles));
+      it.bad = int(min(uint32_t(deal.tiles - it.pos0), share_end - at));
+      at += uint32_t(it.bad);
+      return true;
+    }
     const int slot = k_item & 1;
     if (!warp_wait(&bar[C::kFullItem + slot], uint32_t(k_item >> 1) & 1u)) {
       if (lane == 0) atomicOr(a.v.err, 4u);
@@ -440,27 +479,9 @@ prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap qmap,
       if constexpr (!Shared)
         for (int w = 0; w < kPfScan / 32; ++w) total += s_sum[w];
       if (void_call) total = 0;
-      // (a shared prefix: this CTA's share of the tiles)
-      const SharedDeal deal = shared_deal(a.n_items, shared, int(gridDim.x));
-      int64_t at = 0, share_end = 0;
-      if constexpr (Shared) deal.share(int(blockIdx.x), &at, &share_end);
       const int n_items = total * a.v.hkv * a.split;  // below 2^23
       auto find = [&](int k, PfItem &it) {
         it = PfItem{-1, 0, 0, 0, 0, 0, 0};
-        if constexpr (Shared) {
-          if (at >= share_end) return;
-          const int item = int(at / deal.tiles);
-          const int x = item / a.v.hkv;
-          it.b = 0;
-          it.g = item - x * a.v.hkv;
-          it.s = item + int(blockIdx.x);
-          it.row0 = x * a.TI;
-          it.n_tok = min(a.TI, a.n_tokens - it.row0);
-          it.pos0 = int(at - int64_t(item) * deal.tiles);
-          it.bad = int(min(int64_t(deal.tiles - it.pos0), share_end - at));
-          at += it.bad;
-          return;
-        }
         const int c = (k & 1) ? int(gridDim.x) - 1 - int(blockIdx.x) : int(blockIdx.x);
         const int idx = k * int(gridDim.x) + c;
         if (idx >= n_items) return;
@@ -517,11 +538,18 @@ prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap qmap,
       };
       int vs = 0, vr = 0;
       PfItem it, next;
-      find(0, it);
-      bool ok = give(0, it);
-      for (int k = 1; ok && it.b >= 0; ++k) {
-        find(k, next);
-        ok = give(k, next);
+      bool ok = true, more = true;
+      if constexpr (Shared) {
+        more = next_item(it);
+      } else {
+        find(0, it);
+        ok = give(0, it);
+      }
+      for (int k = 1; ok && more && it.b >= 0; ++k) {
+        if constexpr (!Shared) {
+          find(k, next);
+          ok = give(k, next);
+        }
         const PfWork w = work_of(it);
         for (int j = 0; ok && j < w.n; ++j) {
           ok = warp_wait(&bar[C::kFullV + vs], uint32_t(vr) & 1u);
@@ -547,7 +575,10 @@ prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap qmap,
           if (lane == 0) mbar_arrive(&bar[C::kReadyV + vs]);
           if (++vs == C::kVStages) vs = 0, ++vr;
         }
-        it = next;
+        if constexpr (Shared)
+          more = next_item(it);
+        else
+          it = next;
       }
       if (!ok && lane == 0) atomicOr(a.v.err, 4u);
     } else if (warp == kPfLoadWarp) {
@@ -972,7 +1003,8 @@ prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap qmap,
           // nothing branches in between, so nothing touches its registers)
           tmem_ld32_issue(t_s + 64, s + 64);
           tmem_ld32_issue(t_s + 96, s + 96);
-          weights64(s, a.scale2, m, wt, sum);
+          // (Shared: not against an m that the next line looks for anyway)
+          if (!Shared || !unseen) weights64(s, a.scale2, m, wt, sum);
           tmem_landed(s + 64);
           tmem_landed(s + 96);
           if (!all) mask();
@@ -1282,6 +1314,9 @@ cudaError_t launch_shared_prefix(const PagedView &v, const PagedAttnLaunch &l,
   a.n_items = x.cut.items;
   a.part = x.part;
   a.ml = x.ml;
+  a.ctas = x.ctas;
+  a.max_len = x.max_len;
+  a.rates = x.rates;
   if (l.D == 64) return launch_items<64, false, true>(a, l, grid, stream);
   return a.TI == a.TQ ? launch_items<128, true, true>(a, l, grid, stream)
                       : launch_items<128, false, true>(a, l, grid, stream);

@@ -7,14 +7,22 @@
 //
 // Mathematics: attention over two sets of positions, each with m = max s_j,
 // l = sum 2^(s_j - m) and o = sum 2^(s_j - m) v_j, joins as in
-// bw_paged_decode.cu.  Three launches:
+// bw_paged_decode.cu.
+//
+// Bound by the bytes of the keys and values and, for many sequences, by the
+// tensor cores.  Three launches:
 //  * the prefix (bw_paged_prefill.cu): all sequences' query heads of a key-value
 //    head are rows of 128-row tiles against the same keys, on the tensor cores;
-//    the key axis is dealt to all SMs in equal shares;
-//  * the positions behind it (bw_paged_decode.cu), by sequence.  It does not wait
-//    for the first launch until its own work is done, so its CTAs fill the SMs
-//    that the first one's leave;
+//  * the positions behind it (bw_paged_decode.cu), by sequence, at the same time:
+//    from the lengths on the device both kernels work out how many SMs each
+//    gets, the first one's other CTAs leave at once, and the second does not wait
+//    for the first until its own work is done;
 //  * here, the join of a query head's parts of both, a warp per head or several.
+// 64 sequences of up to 500 positions behind 8209, 20 + 2 x 5 heads of 128: 29 us,
+// of which the prefix's CTAs run from 3.5 to 24 (8 to the first scores, 2 a pair of
+// 128-row tiles, 2 to write the parts), the others' from 8 to 24, the join from 29
+// to 32 (the ends of two launches, 1.4 each, and two rounds of loads); 48 behind
+// 100001: 68, 0.60 of the measured copy rate, 720 TFLOP/s.
 #include <algorithm>
 
 #include "bw_paged_shared.cuh"
@@ -30,7 +38,7 @@ struct SharedJoinArgs {
   const int *shared_len;
   int shared_pages;
   SharedCut cut;
-  int grid;             // CTAs of the prefix's launch
+  const int *ctas;      // that have a share of the prefix
   const float *pre;     // [slots][cut.seqs G][D]
   const float2 *pre_ml;
   const float *part;    // the decode kernel's parts
@@ -70,6 +78,7 @@ shared_join_kernel(const SharedJoinArgs a) {
   prefix.max_pages = a.shared_pages;
   // (asked for together; reported by the launches before)
   const int shared_n = __ldcg(a.shared_len), len_n = __ldcg(a.v.len + b);
+  const int ctas = min(max(__ldcg(a.ctas), 0), kPfMostCtas);
   DcParts own = a.parts[int64_t(b) * a.v.hkv + g];
   const int shared =
       shared_n >= 0 && shared_n <= (a.shared_pages << a.v.page_shift) ? shared_n : 0;
@@ -80,12 +89,11 @@ shared_join_kernel(const SharedJoinArgs a) {
   if (own.unit0 < 0 || own.parts < 0 || own.parts > most ||
       own.unit0 > most - own.parts)
     own.parts = 0;
-  const SharedDeal deal = shared_deal(a.cut.items, shared, a.grid);
+  const SharedDeal deal = shared_deal(a.cut.items, shared, ctas);
   const int x = b / a.cut.seqs, item = x * a.v.hkv + g;
   int first = 0, n_pre = 0;
-  if (deal.total > 0) {
-    first = deal.owner(int64_t(item) * deal.tiles);
-    n_pre = deal.owner(int64_t(item + 1) * deal.tiles - 1) - first + 1;
+  if (deal.n > 0) {
+    deal.slots(item, &first, &n_pre);
   }
   const int n = there ? n_pre + own.parts : 0;
   const int row = (b - x * a.cut.seqs) * a.G + h;
@@ -97,7 +105,7 @@ shared_join_kernel(const SharedJoinArgs a) {
     const float *o;
     const float2 *m;
     if (i < n_pre) {
-      const int64_t r = int64_t(item + first + i) * slot_rows + row;
+      const int64_t r = int64_t(first + i) * slot_rows + row;
       o = a.pre + r * D;
       m = a.pre_ml + r;
     } else {
@@ -234,6 +242,9 @@ cudaError_t launch_paged_shared(const PagedView &v, const PagedAttnLaunch &l,
   uint8_t *ws = static_cast<uint8_t *>(l.workspace);
   x.part = reinterpret_cast<float *>(ws + at.part);
   x.ml = reinterpret_cast<float2 *>(ws + at.ml);
+  x.ctas = reinterpret_cast<int *>(ws + kPagedSharedAt);
+  x.max_len = v.max_pages << v.page_shift;
+  x.rates = shared_rates(l.D, x.cut.seqs > kPfRows / (l.H / v.hkv), sms);
   PagedView prefix = v;
   prefix.table = shared_table;
   prefix.max_pages = l.shared_pages;
@@ -246,7 +257,7 @@ cudaError_t launch_paged_shared(const PagedView &v, const PagedAttnLaunch &l,
   a.shared_len = l.shared_len;
   a.shared_pages = l.shared_pages;
   a.cut = x.cut;
-  a.grid = grid;
+  a.ctas = x.ctas;
   a.pre = x.part;
   a.pre_ml = x.ml;
   // (as launch_paged_decode lays them out)
@@ -259,11 +270,15 @@ cudaError_t launch_paged_shared(const PagedView &v, const PagedAttnLaunch &l,
   a.out_ld = l.out_ld;
   a.H = l.H;
   a.G = l.H / v.hkv;
-  // Few heads have many parts each.
-  const bool few = v.n_seqs * l.H <= 8 * sms;
+  // As many warps a head as leave all CTAs room at once.
+  const int heads = v.n_seqs * l.H, room = 32 * sms;
   if (l.D == 64)
-    return few ? launch_join<64, 4>(a, stream) : launch_join<64, 1>(a, stream);
-  return few ? launch_join<128, 4>(a, stream) : launch_join<128, 1>(a, stream);
+    return heads * 4 <= room   ? launch_join<64, 4>(a, stream)
+           : heads * 2 <= room ? launch_join<64, 2>(a, stream)
+                               : launch_join<64, 1>(a, stream);
+  return heads * 4 <= room   ? launch_join<128, 4>(a, stream)
+         : heads * 2 <= room ? launch_join<128, 2>(a, stream)
+                             : launch_join<128, 1>(a, stream);
 }
 
 }  // namespace bw

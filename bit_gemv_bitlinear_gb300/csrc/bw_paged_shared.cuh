@@ -49,6 +49,21 @@ inline size_t dc_parts_bytes(size_t items) {
 }
 
 // ---- the shared prefix ----
+// What things take, in us (shared_split), measured in calls of 48 to 230
+// sequences: a key tile of the prefix 1.65 with two query tiles of 128 dims (a
+// document of 100001 positions: 28 tiles a CTA in 48), 1.1 with one, 1.3 and 1.0
+// for 64 dims; a tile of the decode kernel 0.65, of which an SM has two at a time,
+// and 0.47 of three for 64 dims.  The prefix's first scores come about 3 later,
+// and its sums take 2 to write.  (64 sequences behind 8209 positions: 29.1 us; 41
+// without a split, the decode kernel's CTAs behind the prefix's.)
+inline SharedRates shared_rates(int D, bool two, int sms) {
+  SharedRates r{};
+  r.sms = sms < kPfMostCtas ? sms : kPfMostCtas;
+  r.pre_us = D == 64 ? (two ? 1.3f : 1.0f) : (two ? 1.65f : 1.1f);
+  r.own_us = D == 64 ? 0.47f : 0.65f;
+  r.late_us = D == 64 ? 6.0f : 8.0f;
+  return r;
+}
 struct SharedPrefix {
   const int *table;  // its pages
   const int *len;    // its positions (one)
@@ -56,7 +71,12 @@ struct SharedPrefix {
   SharedCut cut;
   float *part;       // [slots][cut.seqs G][D]
   float2 *ml;        // [slots][cut.seqs G]
+  int *ctas;         // those that have a share, for the join
+  int max_len;       // of a sequence
+  SharedRates rates;
 };
+// Where the workspace's first 256 bytes keep it.
+constexpr size_t kPagedSharedAt = 160;
 // CTAs of the prefix's launch, of which those with tiles have a share.
 inline int shared_grid(int sms, const SharedCut &c, int64_t longest) {
   const int64_t tiles = c.items * ((longest + kPfTile - 1) / kPfTile);

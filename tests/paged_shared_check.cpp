@@ -22,39 +22,45 @@ int main() {
             if (int64_t(c.items / Hkv) * c.seqs < n ||
                 int64_t(c.items / Hkv - 1) * c.seqs >= n)
               return 3;
-            const SharedDeal d = shared_deal(c.items, shared, most);
-            std::vector<char> used(shared_slots(c, most), 0);
-            int64_t at = 0;
-            for (int cta = 0; cta < most; ++cta) {
-              int64_t lo, hi;
-              d.share(cta, &lo, &hi);
-              if (lo != at || hi < lo) return 4;
-              if (cta < d.n && d.total > 0 && hi == lo) return 5;
-              // pieces, as the scheduler makes them
-              for (int64_t t = lo; t < hi;) {
-                const int item = int(t / d.tiles);
-                const int64_t end = (int64_t(item) + 1) * d.tiles < hi
-                                        ? (int64_t(item) + 1) * d.tiles
-                                        : hi;
-                if (item >= c.items) return 6;
-                const int slot = item + cta;
-                if (slot >= int(used.size()) || used[slot]) return 7;
-                used[slot] = 1;
-                // as the join looks for them
-                const int first = d.owner(int64_t(item) * d.tiles);
-                const int last = d.owner(int64_t(item + 1) * d.tiles - 1);
-                if (cta < first || cta > last) return 8;
-                if (d.owner(t) != cta || d.owner(end - 1) != cta) return 9;
-                t = end;
+            for (float own : {0.0f, 1.0f, 300.0f, 5000.0f, 4e6f}) {
+              const SharedRates r{most, 1.65f, 0.83f, 4.0f};
+              const int n = shared_split(c.items, shared, own, r);
+              if (n < 0 || n > most || (shared > 0) != (n > 0)) return 12;
+              if (own > 0 && most > 1 && n > most - 1) return 13;
+              const SharedDeal d = shared_deal(c.items, shared, n);
+              if (d.n > n || (d.n > 0) != (n > 0)) return 14;
+              std::vector<char> used(shared_slots(c, most), 0);
+              std::vector<int> seen(c.items, 0);
+              uint32_t at = 0;
+              for (int cta = 0; cta < most; ++cta) {
+                uint32_t lo, hi;
+                d.share(cta, &lo, &hi);
+                if (lo != at || hi < lo) return 4;
+                if (cta < d.n && hi == lo) return 5;
+                // pieces, as the CTA takes them
+                for (uint32_t t = lo; t < hi;) {
+                  const int item = int(t / uint32_t(d.tiles));
+                  const uint32_t all = uint32_t(item + 1) * uint32_t(d.tiles);
+                  const uint32_t end = all < hi ? all : hi;
+                  if (item >= c.items) return 6;
+                  const int slot = d.slot(item, cta);
+                  if (slot >= int(used.size()) || used[slot]) return 7;
+                  used[slot] = 1;
+                  // as the join looks for them
+                  int first, count;
+                  d.slots(item, &first, &count);
+                  if (slot != first + seen[item]++ || seen[item] > count) return 8;
+                  t = end;
+                }
+                at = hi;
               }
-              at = hi;
+              if (at != d.total) return 10;
+              for (int item = 0; d.total > 0 && item < c.items; ++item) {
+                int first, count;
+                d.slots(item, &first, &count);
+                if (count != seen[item]) return 11;
+              }
             }
-            if (at != d.total) return 10;
-            // and every part that the join looks for is there
-            for (int item = 0; d.total > 0 && item < c.items; ++item)
-              for (int u = d.owner(int64_t(item) * d.tiles);
-                   u <= d.owner(int64_t(item + 1) * d.tiles - 1); ++u)
-                if (!used[item + u]) return 11;
             ++checked;
           }
   std::printf("%d plans\n", checked);
