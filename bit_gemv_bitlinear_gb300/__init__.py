@@ -587,7 +587,7 @@ def _where(dev: int, stream):
     if stream is None:
         s = torch.cuda.current_stream(dev).cuda_stream \
             if _raw_stream is None else _raw_stream(dev)
-        if torch.cuda.current_device() == dev:
+        if _current_device() == dev:
             return _NO_CONTEXT, s
         return torch.cuda.device(dev), s
     s = _stream(stream)
@@ -601,6 +601,10 @@ def _where(dev: int, stream):
 # The current stream's handle without making a stream object, where this
 # PyTorch has it.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+# torch.cuda.current_device() without its look at whether CUDA is initialised (a
+# CUDA tensor is at hand where this is called), where this PyTorch has it.
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or \
+    torch.cuda.current_device
 
 
 def bw_qk_norm_rope_append(qkv: torch.Tensor, k_pages: torch.Tensor,
@@ -801,15 +805,6 @@ def _whole(t, dtype, dev: int, shape, name: str) -> int:
             + "".join(f"[{n}]" for n in shape))
 
 
-def _codes(q, s, dev: int, M: int, K: int, like):
-    """The outputs q [M][K] and s [M], made where they are not given."""
-    if q is None:
-        q = torch.empty((M, K), dtype=_I8, device=like.device)
-    if s is None:
-        s = torch.empty((M,), dtype=_F32, device=like.device)
-    return q, s, _whole(q, _I8, dev, (M, K), "q"), _whole(s, _F32, dev, (M,), "s")
-
-
 def bw_add_rms_norm_quant(x: torch.Tensor, gamma: torch.Tensor,
                           h: torch.Tensor | None = None, eps: float = 1e-5,
                           h_out: torch.Tensor | None = None,
@@ -820,27 +815,50 @@ def bw_add_rms_norm_quant(x: torch.Tensor, gamma: torch.Tensor,
     None -> (int8 q [M][K], fp32 s [M]) of (h + x) / rms * gamma, as
     bw_quant_act's.  h + x goes to h_out (h itself if None)."""
     try:
-        (M, K), dev = x.shape, x.get_device()
+        shape, dev = x.shape, x.get_device()
+        M, K = shape
         ok = dev >= 0
     except (AttributeError, ValueError):
         ok = False
     if not ok:
         _refuse(x, (_BF16, _F32), -1, "x must be [M][K]")
-    ptr, ld = _row_view(x, (_BF16, _F32), dev, M, K, "x")
-    g = _whole(gamma, _F32, dev, (K,), "gamma")
+    bf16 = x.dtype is _BF16
+    st = x.stride()
+    if not bf16 and x.dtype is not _F32 or st[1] != 1 and K > 1:
+        _refuse(x, (_BF16, _F32), dev, f"x must be [{M}][{K}] with contiguous rows")
     hp = ho = None
     if h is not None:
-        hp = ho = _whole(h, _F32, dev, (M, K), "h")
+        hp = ho = _whole(h, _F32, dev, shape, "h")
         if h_out is not None:
-            ho = _whole(h_out, _F32, dev, (M, K), "h_out")
+            ho = _whole(h_out, _F32, dev, shape, "h_out")
     elif h_out is not None:
         raise ValueError("h_out without h")
+    return _norm_quant(_lib.bw_add_rms_norm_quant,
+                       (x.data_ptr(), bf16, st[0] if M > 1 else K, hp, ho),
+                       dev, shape, gamma, eps, q, s, stream,
+                       "bw_add_rms_norm_quant")
+
+
+def _norm_quant(call, first, dev, shape, gamma, eps, q, s, stream, what):
+    """The part that both norms have in common: q and s, made where they are
+    not given, and the call behind its `first` arguments."""
+    M, K = shape
+    g = _vector(gamma, _F32, dev, K, "gamma")
     context, st = _where(dev, stream)
-    with context:
-        q, s, qp, sp = _codes(q, s, dev, M, K, x)
-        _check(_lib.bw_add_rms_norm_quant(ptr, x.dtype is _BF16, ld, hp, ho, g,
-                                          eps, M, K, qp, sp, st),
-               "bw_add_rms_norm_quant")
+    if q is None or s is None:
+        with context:
+            if q is None:
+                q = torch.empty(shape, dtype=_I8, device=gamma.device)
+            if s is None:
+                s = torch.empty((M,), dtype=_F32, device=gamma.device)
+    qp, sp = _whole(q, _I8, dev, shape, "q"), _vector(s, _F32, dev, M, "s")
+    if context is _NO_CONTEXT:
+        status = call(*first, g, eps, M, K, qp, sp, st)
+    else:
+        with context:
+            status = call(*first, g, eps, M, K, qp, sp, st)
+    if status:
+        _check(status, what)
     return q, s
 
 
@@ -857,15 +875,13 @@ def bw_relu2_rms_norm_quant(gu: torch.Tensor, gamma: torch.Tensor,
         ok = False
     if not ok:
         _refuse(gu, (_BF16,), -1, "gu must be [M][2 F]")
-    F = width // 2
-    ptr, ld = _row_view(gu, (_BF16,), dev, M, width, "gu")
-    g = _whole(gamma, _F32, dev, (F,), "gamma")
-    context, st = _where(dev, stream)
-    with context:
-        q, s, qp, sp = _codes(q, s, dev, M, F, gu)
-        _check(_lib.bw_relu2_rms_norm_quant(ptr, ld, g, eps, M, F, qp, sp, st),
-               "bw_relu2_rms_norm_quant")
-    return q, s
+    st = gu.stride()
+    if gu.dtype is not _BF16 or st[1] != 1:
+        _refuse(gu, (_BF16,), dev, f"gu must be [{M}][{width}] with contiguous rows")
+    return _norm_quant(_lib.bw_relu2_rms_norm_quant,
+                       (gu.data_ptr(), st[0] if M > 1 else width), dev,
+                       (M, width // 2), gamma, eps, q, s, stream,
+                       "bw_relu2_rms_norm_quant")
 
 
 def bw_lora_workspace_bytes(M: int, R: int) -> int:
@@ -899,22 +915,28 @@ def bw_lora_add(y: torch.Tensor, x: torch.Tensor, s: torch.Tensor,
     Ap = _whole(A, _BF16, dev, (n, R, K), "A")
     Bp = _whole(B, _BF16, dev, (n, N, R), "B")
     xp = _whole(x, _I8, dev, (M, K), "x")
-    sp = _whole(s, _F32, dev, (M,), "s")
-    ap = _whole(adapter, _I32, dev, (M,), "adapter")
-    cp = None if scale is None else _whole(scale, _F32, dev, (n,), "scale")
+    sp = _vector(s, _F32, dev, M, "s")
+    ap = _vector(adapter, _I32, dev, M, "adapter")
+    cp = None if scale is None else _vector(scale, _F32, dev, n, "scale")
     if out is None:
         out, op, out_ld = y, yp, y_ld
     else:
         op, out_ld = _row_view(out, (_BF16,), dev, M, N, "out")
     context, st = _where(dev, stream)
-    with context:
-        if workspace is None:
+    if workspace is None:
+        with context:
             workspace = torch.empty((max(16, bw_lora_workspace_bytes(M, R)),),
                                     dtype=torch.uint8, device=y.device)
-        _check(_lib.bw_lora_add(
-            xp, sp, Ap, Bp, cp, ap, n, M, N, K, R, yp, y_ld, op, out_ld,
-            _vector(workspace, torch.uint8, dev, 0, "workspace"),
-            workspace.numel(), st), "bw_lora_add")
+    wp, size = _vector(workspace, torch.uint8, dev, 0, "workspace"), workspace.numel()
+    if context is _NO_CONTEXT:
+        status = _lib.bw_lora_add(xp, sp, Ap, Bp, cp, ap, n, M, N, K, R, yp, y_ld,
+                                  op, out_ld, wp, size, st)
+    else:
+        with context:
+            status = _lib.bw_lora_add(xp, sp, Ap, Bp, cp, ap, n, M, N, K, R, yp,
+                                      y_ld, op, out_ld, wp, size, st)
+    if status:
+        _check(status, "bw_lora_add")
     return out
 
 
