@@ -15,21 +15,25 @@
 // they may well all have other adapters, and 16 rows by 8 columns are the smallest
 // tile there is.  Layout:
 //  * 16 rows are a tile.  Its distinct adapters are found with ballots, in any
-//    order of rows; each is multiplied with the whole tile, and rows of others
-//    are left out (shrink: not stored; expand: zeros for u).
+//    order of rows; each is multiplied with the whole tile, and what comes out for
+//    rows of others is left out.
 //  * The reduction axis may be permuted alike in both factors, so a lane takes
 //    16 consecutive bytes of an adapter's row for two products' fragments (and 8
 //    codes, made bf16 by four operations a pair), straight from global memory;
 //    and the columns of the second product, so a lane stores 16 bytes of out.
-//  * shrink: a CTA takes a tile, one (or every J-th) of its adapters and 16 or
-//    more of its R rows; the warps cut the K axis and add up in shared memory.
-//    (Prompts: J = 2, or a tile that two requests share holds up the rest.)
-//  * expand, few rows: a CTA takes 32 columns and the adapters of a tile; the
-//    warps deal them out and add up in shared memory.
-//  * expand, many rows: on tcgen05, 128 rows by 128 columns (below).
+//  * few rows: one launch, a cluster of 16 CTAs a tile (lora_few_kernel).  Two
+//    launches with u in memory between them took 4.7 us for one row of 2560 x 2560
+//    at rank 16 and 9.1 for 61 of 48 adapters, 3840 x 2560; so it is 4.3 and 8.6,
+//    of which the exchanges (loads of the numbers, of A, of the sums, of B) are
+//    most: 82 + 82 KB of weights come in well under 1.
+//  * many rows: u first, a CTA a tile, its adapters (two CTAs in turn, or a tile
+//    that two requests share holds up the rest) and up to 64 of its R rows, the
+//    warps cut the K axis and add up in shared memory; then the second product on
+//    tcgen05, 128 rows by 128 columns.
 // 2011 rows of 5 adapters of rank 64, 13824 x 2560: 34 us, 0.56 of the measured copy
-// rate; with mma.sync and y in registers the second product alone was 40 (500
-// instructions a warp for 32 x 32 outputs, 10 cycles each).
+// rate (7 for u, 26 for the rest, which waits for y: with mma.sync and y in
+// registers that was 40, 500 instructions a warp for 32 x 32 outputs, 10 cycles
+// each).
 #include <algorithm>
 
 #include "bw_serve.cuh"
@@ -41,8 +45,6 @@ namespace {
 constexpr int kLoraRows = 16;
 constexpr int kLoraWarps = 8;
 constexpr int kLoraThreads = kLoraWarps * 32;
-// Up to this many rows a tile may well hold another adapter in every row.
-constexpr int kLoraFewRows = 256;
 // From this many rows on the second product runs on tcgen05.
 constexpr int kLoraTcRows = 513;
 
@@ -57,10 +59,7 @@ struct LoraArgs {
   int64_t y_ld;
   __nv_bfloat16 *out;
   int64_t out_ld;
-  // u as two bf16 values, rows u_ld apart: [M][R16] each, or (tcgen05) [M][2 R16]
-  // of hi | lo.
-  __nv_bfloat16 *u_hi, *u_lo;
-  int u_ld;
+  __nv_bfloat16 *u;  // as two bf16 values: [M][2 R16], hi | lo
   unsigned int *err;
 };
 
@@ -84,11 +83,11 @@ __device__ __forceinline__ uint32_t codes2(uint32_t w) {
   return *reinterpret_cast<const uint32_t *>(&d);
 }
 
-// The adapter of this lane's row (lanes 0..15: row0 + lane), -1 for none.
-__device__ __forceinline__ int lane_adapter(const LoraArgs &a, int row0) {
+// The adapter of this lane's row (lanes 0 .. n - 1: row0 + lane), -1 for none.
+__device__ __forceinline__ int lane_adapter(const LoraArgs &a, int row0, int n) {
   const int lane = threadIdx.x & 31;
   int id = -1;
-  if (lane < kLoraRows && row0 + lane < a.M) {
+  if (lane < n && row0 + lane < a.M) {
     id = __ldcg(a.adapter + row0 + lane);
     if (id < -1 || id >= a.n_adapters) {
       atomicOr(a.err, kLoraErr);
@@ -141,16 +140,16 @@ __device__ __forceinline__ uint2 load_x8(const int8_t *p, int n) {
 
 // u of a tile's rows for adapters z, z + gridDim.z, ... of the tile, rows
 // [8 NT y, 8 NT (y + 1)) of A; kAhead blocks of 32 values of K in flight a warp.
-template <int NT, int kWarps, int kAhead, bool Vec>
-__global__ void __launch_bounds__(kWarps * 32, 1)
+template <int NT, int kAhead, bool Vec>
+__global__ void __launch_bounds__(kLoraThreads, 1)
 lora_shrink_kernel(const LoraArgs a) {
-  __shared__ float s_sum[kWarps][NT][32][4];
+  __shared__ float s_sum[kLoraWarps][NT][32][4];
   pipe::pdl_wait();
   pipe::pdl_trigger();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int row0 = blockIdx.x * kLoraRows, r0 = blockIdx.y * 8 * NT;
   const int fr = lane >> 2, fc = lane & 3;
-  const int mine = lane_adapter(a, row0);
+  const int mine = lane_adapter(a, row0, kLoraRows);
   unsigned left = __ballot_sync(0xffffffffu, mine >= 0), rows;
   const int8_t *x0 = a.x + int64_t(min(row0 + fr, a.M - 1)) * a.K;
   const int8_t *x1 = a.x + int64_t(min(row0 + fr + 8, a.M - 1)) * a.K;
@@ -165,12 +164,12 @@ lora_shrink_kernel(const LoraArgs a) {
     const float row_s = __ldcg(a.s + min(row0 + out_row, a.M - 1));
     float c[NT][4] = {};
 #pragma unroll 1
-    for (int k0 = warp * 32; k0 < a.K; k0 += kWarps * 32 * kAhead) {
+    for (int k0 = warp * 32; k0 < a.K; k0 += kLoraWarps * 32 * kAhead) {
       uint2 xa[kAhead], xb[kAhead];
       uint4 b[kAhead][NT];
 #pragma unroll
       for (int h = 0; h < kAhead; ++h) {
-        const int k = k0 + h * kWarps * 32 + 8 * fc;
+        const int k = k0 + h * kLoraWarps * 32 + 8 * fc;
         const int n = min(a.K - k, 8);
         xa[h] = load_x8<Vec>(x0 + k, n);
         xb[h] = load_x8<Vec>(x1 + k, n);
@@ -199,13 +198,13 @@ lora_shrink_kernel(const LoraArgs a) {
           make_float4(c[t][0], c[t][1], c[t][2], c[t][3]);
     __syncthreads();
     // element e of lane l, tile t: row l / 4 (+ 8), column 8 t + 2 (l mod 4) + ..
-    for (int t = threadIdx.x >> 6; t < NT; t += kWarps / 2) {
+    for (int t = threadIdx.x >> 6; t < NT; t += kLoraWarps / 2) {
       const int half = threadIdx.x & 1, l = (threadIdx.x >> 1) & 31;
       const int row = out_row, col = r0 + 8 * t + 2 * (l & 3);
       if (!(rows >> row & 1u) || col >= a.R16) continue;
       float v0 = 0.0f, v1 = 0.0f;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
+      for (int w = 0; w < kLoraWarps; ++w) {
         v0 += s_sum[w][t][l][2 * half];
         v1 += s_sum[w][t][l][2 * half + 1];
       }
@@ -215,9 +214,9 @@ lora_shrink_kernel(const LoraArgs a) {
       const __nv_bfloat162 hi = __floats2bfloat162_rn(v0, v1);
       const __nv_bfloat162 lo = __floats2bfloat162_rn(
           v0 - __low2float(hi), v1 - __high2float(hi));
-      const int64_t at = int64_t(row0 + row) * a.u_ld + col;
-      *reinterpret_cast<__nv_bfloat162 *>(a.u_hi + at) = hi;
-      *reinterpret_cast<__nv_bfloat162 *>(a.u_lo + at) = lo;
+      __nv_bfloat16 *to = a.u + int64_t(row0 + row) * 2 * a.R16 + col;
+      *reinterpret_cast<__nv_bfloat162 *>(to) = hi;
+      *reinterpret_cast<__nv_bfloat162 *>(to + a.R16) = lo;
     }
   }
 }
@@ -262,9 +261,10 @@ __device__ __forceinline__ void keep_rows(unsigned rows, const float (&p)[4][4],
 // y's columns col .. col + 7 of a row, and out = y + c.  Vec: 16-byte aligned
 // rows; ends of rows and others go value by value.
 template <bool Vec>
-__device__ __forceinline__ uint4 load_y(const LoraArgs &a, int row, int col) {
+__device__ __forceinline__ uint4 load_y(const LoraArgs &a, int row, int end,
+                                        int col) {
   uint4 w = make_uint4(0u, 0u, 0u, 0u);
-  if (row >= a.M) return w;
+  if (row >= end) return w;
   const __nv_bfloat16 *y = a.y + row * a.y_ld + col;
   if (Vec && col + 8 <= a.N) return *reinterpret_cast<const uint4 *>(y);
   uint32_t *p = reinterpret_cast<uint32_t *>(&w);
@@ -284,9 +284,9 @@ __device__ __forceinline__ uint32_t pair_of(float lo, float hi) {
   return *reinterpret_cast<const uint32_t *>(&t);
 }
 template <bool Vec>
-__device__ __forceinline__ void store_row(const LoraArgs &a, int row, int col,
-                                          const uint32_t (&w)[4]) {
-  if (row >= a.M) return;
+__device__ __forceinline__ void store_row(const LoraArgs &a, int row, int end,
+                                          int col, const uint32_t (&w)[4]) {
+  if (row >= end) return;
   __nv_bfloat16 *o = a.out + row * a.out_ld + col;
   if (Vec && col + 8 <= a.N) {
     *reinterpret_cast<uint4 *>(o) = make_uint4(w[0], w[1], w[2], w[3]);
@@ -298,85 +298,216 @@ __device__ __forceinline__ void store_row(const LoraArgs &a, int row, int col,
   }
 }
 
-// Few rows: a tile and 32 columns a CTA, the tile's adapters dealt to the warps
-// (at most two each).
-template <int KK, bool Vec>
+// ---- few rows: both products in one launch ----
+// A cluster of 16 CTAs takes a tile of 16 rows, or of 8 where there is room for
+// twice as many clusters.  First each CTA multiplies its
+// sixteenth of the K axis, a warp 16 of an adapter's R rows at a time; the sums
+// meet in every CTA, read out of the others' shared memory in one order.  Then
+// each CTA has a sixteenth of the columns, a warp 32 at a time, and adds the
+// tile's adapters in turn; B's first fragments are asked for before the sums
+// meet.
+constexpr int kClCtas = 16;
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// 16 bytes at `p`'s place in another CTA's shared memory.
+__device__ __forceinline__ float4 load_of_cta(const float *p, uint32_t rank) {
+  uint32_t at;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
+               : "=r"(at)
+               : "r"(pipe::smem_addr(p)), "r"(rank));
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(at)
+               : "memory");
+  return v;
+}
+// Where u's value r lies in its row: the second product's reduction takes four
+// consecutive values of B's row a lane (c), as 2 c, 2 c + 1, 8 + 2 c and 9 + 2 c of
+// its 16, so u's are laid out in that order.
+__device__ __forceinline__ int place_of(int r) {
+  return (r & ~15) + 2 * ((r >> 2) & 3) + (r & 1) + ((r & 2) << 2);
+}
+
+template <int KK, bool VecK>
 __global__ void __launch_bounds__(kLoraThreads)
-lora_expand_few_kernel(const LoraArgs a) {
-  __shared__ float s_sum[kLoraWarps][4][32][4];
+lora_few_kernel(const LoraArgs a, int vec, int tile) {
+  constexpr int kAhead = 5;            // blocks of 32 of K in flight
+  constexpr int kHeld = KK <= 4 ? 8 / KK : 1;  // adapters' B in flight
+  constexpr int kStride = 16 * KK + 8;  // odd in 16 bytes: eight rows meet all banks
+  __shared__ __align__(16) float s_part[kLoraRows][16 * KK];
+  __shared__ __align__(16) __nv_bfloat16 s_u[2][kLoraRows][kStride];  // hi, lo
+  __shared__ int s_id[kLoraRows], s_count;
+  __shared__ unsigned s_rows[kLoraRows];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int row0 = blockIdx.y * kLoraRows, n0 = blockIdx.x * 32;
+  const int rank = blockIdx.x, row0 = blockIdx.y * tile;
+  const int end = min(row0 + tile, a.M);
   const int fr = lane >> 2, fc = lane & 3;
-  const int mine = lane_adapter(a, row0);
-  unsigned left = __ballot_sync(0xffffffffu, mine >= 0), rows[2] = {0u, 0u};
-  int ids[2] = {0, 0}, id;
-  unsigned of_id;
-  for (int j = 0; next_adapter(mine, left, id, of_id); ++j)
-#pragma unroll
-    for (int u = 0; u < 2; ++u)
-      if (j == warp + u * kLoraWarps) {
-        ids[u] = id;
-        rows[u] = of_id;
-      }
-  // thread i of the first 64: row i / 4, eight columns
-  const int row = threadIdx.x >> 2;
-  uint4 y = make_uint4(0u, 0u, 0u, 0u);
-  if (row < kLoraRows) y = load_y<Vec>(a, row0 + row, n0 + 8 * fc);
-  // what both adapters need is asked for at once where there is room for it
-  constexpr int kHeld = KK <= 2 ? 2 : 1;
-  uint2 b[kHeld][KK][4];
-#pragma unroll
-  for (int u = 0; u < kHeld; ++u)
-    if (rows[u]) load_b<KK>(a, ids[u], n0, b[u]);
   pipe::pdl_wait();
   pipe::pdl_trigger();
-  // (rows of other adapters are multiplied too: a row's u makes its own row alone)
-  const int64_t at0 = int64_t(min(row0 + fr, a.M - 1)) * a.u_ld;
-  const int64_t at1 = int64_t(min(row0 + fr + 8, a.M - 1)) * a.u_ld;
-  float c[4][4] = {};
+  const int mine = lane_adapter(a, row0, tile);
+  unsigned left = __ballot_sync(0xffffffffu, mine >= 0);
+  const unsigned with = left;
+  if (warp == 0) {
+    int id, n = 0;
+    unsigned rows;
+    for (; next_adapter(mine, left, id, rows); ++n)
+      if (lane == 0) s_id[n] = id, s_rows[n] = rows;
+    if (lane == 0) s_count = n;
+  }
+  __syncthreads();
+  const int count = s_count;
+
+  // ---- u: this CTA's blocks of K ----
+  const int blocks = (a.K + 31) / 32, groups = a.R16 / 16;
+  const int b_lo = rank * blocks / kClCtas, b_hi = (rank + 1) * blocks / kClCtas;
+  const int8_t *x0 = a.x + int64_t(min(row0 + fr, a.M - 1)) * a.K;
+  const int8_t *x1 = a.x + int64_t(min(row0 + fr + 8, a.M - 1)) * a.K;
+  for (int task = warp; task < count * groups; task += kLoraWarps) {
+    const int j = task / groups, r0 = (task - j * groups) * 16;
+    const __nv_bfloat16 *A = a.A + (int64_t(s_id[j]) * a.R + r0 + fr) * a.K;
+    float c[2][4] = {};
+#pragma unroll 1
+    for (int k0 = b_lo; k0 < b_hi; k0 += kAhead) {
+      uint2 xa[kAhead], xb[kAhead];
+      uint4 b[kAhead][2];
 #pragma unroll
-  for (int u = 0; u < 2; ++u) {
-    if (!rows[u]) continue;
-    if (u >= kHeld) load_b<KK>(a, ids[u], n0, b[u % kHeld]);
-    float p[4][4] = {};
+      for (int h = 0; h < kAhead; ++h) {
+        const int k = (k0 + h) * 32 + 8 * fc;
+        const int n = k0 + h < b_hi ? min(a.K - k, 8) : 0;
+        xa[h] = load_x8<VecK>(x0 + k, n);
+        xb[h] = load_x8<VecK>(x1 + k, n);
 #pragma unroll
-    for (int k = 0; k < KK; ++k) {
-      if (16 * k >= a.R16) break;
-      const int r = 16 * k + 4 * fc;
-      auto piece = [&](const __nv_bfloat16 *x, int64_t row_at) {
-        return __ldcg(reinterpret_cast<const uint2 *>(x + row_at + r));
-      };
-      const uint2 h0 = piece(a.u_hi, at0), h1 = piece(a.u_hi, at1);
-      const uint2 l0 = piece(a.u_lo, at0), l1 = piece(a.u_lo, at1);
-      const uint32_t hi[4] = {h0.x, h1.x, h0.y, h1.y};
-      const uint32_t lo[4] = {l0.x, l1.x, l0.y, l1.y};
+        for (int t = 0; t < 2; ++t)
+          b[h][t] = load_a8<VecK>(A + int64_t(8 * t) * a.K + k,
+                                  r0 + 8 * t < a.R ? n : 0);
+      }
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        mma16816(p[t], lo, b[u % kHeld][k][t].x, b[u % kHeld][k][t].y);
-        mma16816(p[t], hi, b[u % kHeld][k][t].x, b[u % kHeld][k][t].y);
+      for (int h = 0; h < kAhead; ++h) {
+        const uint32_t f0[4] = {codes2<0>(xa[h].x), codes2<0>(xb[h].x),
+                                codes2<1>(xa[h].x), codes2<1>(xb[h].x)};
+        const uint32_t f1[4] = {codes2<0>(xa[h].y), codes2<0>(xb[h].y),
+                                codes2<1>(xa[h].y), codes2<1>(xb[h].y)};
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          mma16816(c[t], f0, b[h][t].x, b[h][t].y);
+          mma16816(c[t], f1, b[h][t].z, b[h][t].w);
+        }
       }
     }
-    keep_rows(rows[u], p, c);
+    const unsigned rows = s_rows[j];
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int half = 0; half < 2; ++half)
+        if (rows >> (fr + 8 * half) & 1u)
+          *reinterpret_cast<float2 *>(&s_part[fr + 8 * half][r0 + 8 * t + 2 * fc]) =
+              make_float2(c[t][2 * half], c[t][2 * half + 1]);
   }
+  cluster_arrive();
+
+  // ---- what the second product needs meanwhile ----
+  const int col_groups = (a.N + 31) / 32;
+  int cg = rank + kClCtas * warp;
+  uint2 b[kHeld][KK][4];
+  uint4 y[2];
+  auto ask = [&] {
+    if (cg >= col_groups) return;
 #pragma unroll
-  for (int t = 0; t < 4; ++t)
-    *reinterpret_cast<float4 *>(s_sum[warp][t][lane]) =
-        make_float4(c[t][0], c[t][1], c[t][2], c[t][3]);
-  __syncthreads();
-  if (row >= kLoraRows) return;
-  const int half = row >> 3, l = (row & 7) * 4 + fc;
-  uint32_t w[4] = {y.x, y.y, y.z, y.w};
+    for (int half = 0; half < 2; ++half)
+      y[half] = vec ? load_y<true>(a, row0 + fr + 8 * half, end, 32 * cg + 8 * fc)
+                    : load_y<false>(a, row0 + fr + 8 * half, end, 32 * cg + 8 * fc);
 #pragma unroll
-  for (int t = 0; t < 4; ++t) {
-    float v0 = 0.0f, v1 = 0.0f;
+    for (int u = 0; u < kHeld; ++u)
+      if (u < count) load_b<KK>(a, s_id[u], 32 * cg, b[u]);
+  };
+  ask();
+  cluster_wait();
+
+  // ---- u: the sums of all CTAs ----
+  for (int i = threadIdx.x; i < kLoraRows * a.R16 / 4; i += kLoraThreads) {
+    const int row = i / (a.R16 / 4), r = (i - row * (a.R16 / 4)) * 4;
+    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (with >> row & 1u) {
+      float4 p[kClCtas];
 #pragma unroll
-    for (int k = 0; k < kLoraWarps; ++k) {
-      v0 += s_sum[k][t][l][2 * half];
-      v1 += s_sum[k][t][l][2 * half + 1];
+      for (int k = 0; k < kClCtas; ++k) p[k] = load_of_cta(&s_part[row][r], k);
+#pragma unroll
+      for (int k = 0; k < kClCtas; ++k)
+        v.x += p[k].x, v.y += p[k].y, v.z += p[k].z, v.w += p[k].w;
+      const int id = __ldcg(a.adapter + row0 + row);
+      const float f = (a.scale ? __ldcg(a.scale + id) : 1.0f) / __ldcg(a.s + row0 + row);
+      v.x *= f, v.y *= f, v.z *= f, v.w *= f;
     }
-    w[t] = pair_of(low_of(w[t]) + v0, high_of(w[t]) + v1);
+    const uint32_t h0 = pair_of(v.x, v.y), h1 = pair_of(v.z, v.w);
+    const int at = place_of(r);  // and r + 2: 8 on
+    *reinterpret_cast<uint32_t *>(&s_u[0][row][at]) = h0;
+    *reinterpret_cast<uint32_t *>(&s_u[0][row][at + 8]) = h1;
+    *reinterpret_cast<uint32_t *>(&s_u[1][row][at]) =
+        pair_of(v.x - low_of(h0), v.y - high_of(h0));
+    *reinterpret_cast<uint32_t *>(&s_u[1][row][at + 8]) =
+        pair_of(v.z - low_of(h1), v.w - high_of(h1));
   }
-  store_row<Vec>(a, row0 + row, n0 + 8 * fc, w);
+  cluster_arrive();  // the others' sums have been read
+  __syncthreads();
+
+  // ---- out: 32 columns a warp at a time ----
+  const uint32_t u_at =
+      pipe::smem_addr(&s_u[0][lane & 15][8 * (lane >> 4)]);
+  constexpr uint32_t kLo = kLoraRows * kStride * 2;
+  while (cg < col_groups) {
+    float c[4][4] = {{low_of(y[0].x), high_of(y[0].x), low_of(y[1].x), high_of(y[1].x)},
+                     {low_of(y[0].y), high_of(y[0].y), low_of(y[1].y), high_of(y[1].y)},
+                     {low_of(y[0].z), high_of(y[0].z), low_of(y[1].z), high_of(y[1].z)},
+                     {low_of(y[0].w), high_of(y[0].w), low_of(y[1].w), high_of(y[1].w)}};
+    for (int j0 = 0; j0 < count; j0 += kHeld) {
+      if (j0 > 0)
+#pragma unroll
+        for (int u = 0; u < kHeld; ++u)
+          if (j0 + u < count) load_b<KK>(a, s_id[j0 + u], 32 * cg, b[u]);
+#pragma unroll
+      for (int u = 0; u < kHeld; ++u) {
+        if (j0 + u >= count) break;
+        float p[4][4] = {};
+#pragma unroll
+        for (int k = 0; k < KK; ++k) {
+          if (16 * k >= a.R16) break;
+          uint32_t f[2][4];
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            asm volatile(
+                "ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                : "=r"(f[e][0]), "=r"(f[e][1]), "=r"(f[e][2]), "=r"(f[e][3])
+                : "r"(u_at + e * kLo + 32 * k)
+                : "memory");
+#pragma unroll
+          for (int t = 0; t < 4; ++t) {
+            mma16816(p[t], f[1], b[u][k][t].x, b[u][k][t].y);
+            mma16816(p[t], f[0], b[u][k][t].x, b[u][k][t].y);
+          }
+        }
+        keep_rows(s_rows[j0 + u], p, c);
+      }
+    }
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      const uint32_t w[4] = {pair_of(c[0][2 * half], c[0][2 * half + 1]),
+                             pair_of(c[1][2 * half], c[1][2 * half + 1]),
+                             pair_of(c[2][2 * half], c[2][2 * half + 1]),
+                             pair_of(c[3][2 * half], c[3][2 * half + 1])};
+      if (vec)
+        store_row<true>(a, row0 + fr + 8 * half, end, 32 * cg + 8 * fc, w);
+      else
+        store_row<false>(a, row0 + fr + 8 * half, end, 32 * cg + 8 * fc, w);
+    }
+    cg += kClCtas * kLoraWarps;
+    ask();
+  }
+  cluster_wait();  // (a CTA's sums stay until all have read them)
 }
 
 // ---- the second product for many rows, on tcgen05 ----
@@ -678,6 +809,33 @@ bool aligned_to(const void *p, uintptr_t a) {
   return reinterpret_cast<uintptr_t>(p) % a == 0;
 }
 
+// Sets a kernel's attribute, once a device.
+template <typename Kernel>
+cudaError_t once(std::atomic<bool> *done, Kernel kernel, cudaFuncAttribute what,
+                 int value) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (done[dev].load(std::memory_order_relaxed)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, what, value);
+  if (e == cudaSuccess) done[dev].store(true, std::memory_order_relaxed);
+  return e;
+}
+
+template <int KK>
+cudaError_t launch_few(const LoraArgs &a, bool vec, bool vec_k, int tile,
+                       cudaLaunchConfig_t &cfg) {
+  static std::atomic<bool> done[2][64];
+  auto go = [&](auto kernel, std::atomic<bool> *d) {
+    const cudaError_t e =
+        once(d, kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    return e != cudaSuccess ? e : cudaLaunchKernelEx(&cfg, kernel, a, int(vec), tile);
+  };
+  return vec_k ? go(lora_few_kernel<KK, true>, done[0])
+               : go(lora_few_kernel<KK, false>, done[1]);
+}
+
 template <int KK>
 cudaError_t launch_expand(const LoraArgs &a, cudaLaunchConfig_t &cfg) {
   using C = ExpandCfg<KK>;
@@ -691,8 +849,8 @@ cudaError_t launch_expand(const LoraArgs &a, cudaLaunchConfig_t &cfg) {
   const cuuint64_t strides[2] = {cuuint64_t(a.R) * 2,
                                  cuuint64_t(a.R) * 2 * cuuint64_t(a.N)};
   const cuuint32_t box[3] = {64, kExCols, 1}, elem[3] = {1, 1, 1};
-  if (!encode_2d(&umap, bf16, a.u_hi, uint64_t(a.u_ld), uint64_t(a.M),
-                 uint64_t(a.u_ld) * 2, 64, kExRows, sw) ||
+  if (!encode_2d(&umap, bf16, a.u, uint64_t(2 * a.R16), uint64_t(a.M),
+                 uint64_t(a.R16) * 4, 64, kExRows, sw) ||
       !encode_2d(&ymap, bf16, a.y, uint64_t(a.N), uint64_t(a.M),
                  uint64_t(a.y_ld) * 2, 64, kExRows, sw) ||
       !encode_2d(&omap, bf16, a.out, uint64_t(a.N), uint64_t(a.M),
@@ -701,9 +859,9 @@ cudaError_t launch_expand(const LoraArgs &a, cudaLaunchConfig_t &cfg) {
          CU_TENSOR_MAP_INTERLEAVE_NONE, sw, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
     return cudaErrorInvalidValue;
-  const cudaError_t e = cudaFuncSetAttribute(
-      lora_expand_kernel<KK>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-      int(C::kSmem));
+  static std::atomic<bool> done[64];
+  const cudaError_t e = once(done, lora_expand_kernel<KK>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, int(C::kSmem));
   if (e != cudaSuccess) return e;
   const int tiles = (a.M + kExRows - 1) / kExRows * ((a.N + kExCols - 1) / kExCols);
   cfg.gridDim = dim3(unsigned(std::min(tiles, std::max(1, device_sm_count()))));
@@ -736,58 +894,51 @@ cudaError_t launch_lora(const LoraLaunch &l, cudaStream_t stream) {
   a.y_ld = l.y_ld;
   a.out = l.out;
   a.out_ld = l.out_ld;
-  // (strides below 2^40 bytes are the tiled copies' limit)
-  const bool vec = l.y_ld % 8 == 0 && l.out_ld % 8 == 0 &&
-                   aligned_to(l.y, 16) && aligned_to(l.out, 16);
-  const bool tc = vec && l.M >= kLoraTcRows && int64_t(a.R) * l.N < (int64_t(1) << 38);
-  a.u_hi = static_cast<__nv_bfloat16 *>(l.workspace);
-  a.u_lo = tc ? a.u_hi + a.R16 : a.u_hi + int64_t(l.M) * a.R16;
-  a.u_ld = tc ? 2 * a.R16 : a.R16;
+  a.u = static_cast<__nv_bfloat16 *>(l.workspace);
   a.err = device_error_word();
   if (!a.err) return cudaErrorInvalidSymbol;
   cudaLaunchConfig_t cfg = {};
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = kClCtas;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
   const unsigned tiles = unsigned((l.M + kLoraRows - 1) / kLoraRows);
-  const bool few = l.M <= kLoraFewRows;
   const bool vec_k = l.K % 8 == 0 && aligned_to(l.x, 8);
-  auto shrink = [&](auto whole, auto any, int nt, int warps, unsigned z) {
-    cfg.blockDim = dim3(unsigned(32 * warps));
-    cfg.gridDim = dim3(tiles, unsigned((a.R16 + 8 * nt - 1) / (8 * nt)), z);
+  const bool vec = l.y_ld % 8 == 0 && l.out_ld % 8 == 0 &&
+                   aligned_to(l.y, 16) && aligned_to(l.out, 16);
+  const int kk = a.R16 / 16;
+  // (tensor maps' strides are below 2^40 bytes)
+  if (!vec || l.M < kLoraTcRows || int64_t(a.R) * l.N >= (int64_t(1) << 38)) {
+    cfg.numAttrs = 2;
+    // Tiles of 8 where all of them run at once (61 rows of 48 adapters, 3840 x
+    // 2560: 8.6 us, 10.8 with tiles of 16).
+    const int tile = 2 * tiles * kClCtas <= 2u * unsigned(device_sm_count()) ? 8 : kLoraRows;
+    cfg.gridDim = dim3(kClCtas, unsigned((l.M + tile - 1) / tile));
+    cfg.blockDim = dim3(kLoraThreads);
+    if (kk <= 1) return launch_few<1>(a, vec, vec_k, tile, cfg);
+    if (kk <= 2) return launch_few<2>(a, vec, vec_k, tile, cfg);
+    if (kk <= 4) return launch_few<4>(a, vec, vec_k, tile, cfg);
+    return launch_few<8>(a, vec, vec_k, tile, cfg);
+  }
+  cfg.numAttrs = 1;
+  auto shrink = [&](auto whole, auto any, int nt) {
+    cfg.blockDim = dim3(kLoraThreads);
+    cfg.gridDim = dim3(tiles, unsigned((a.R16 + 8 * nt - 1) / (8 * nt)), 2);
     return vec_k ? cudaLaunchKernelEx(&cfg, whole, a)
                  : cudaLaunchKernelEx(&cfg, any, a);
   };
   const cudaError_t e =
-      few ? shrink(lora_shrink_kernel<2, 16, 5, true>,
-                   lora_shrink_kernel<2, 16, 5, false>, 2, 16,
-                   unsigned(std::min(l.M, kLoraRows)))
-      : a.R16 <= 16 ? shrink(lora_shrink_kernel<2, 8, 5, true>,
-                             lora_shrink_kernel<2, 8, 5, false>, 2, 8, 2u)
-      : a.R16 <= 32 ? shrink(lora_shrink_kernel<4, 8, 3, true>,
-                             lora_shrink_kernel<4, 8, 3, false>, 4, 8, 2u)
-                    : shrink(lora_shrink_kernel<8, 8, 2, true>,
-                             lora_shrink_kernel<8, 8, 2, false>, 8, 8, 2u);
+      a.R16 <= 16   ? shrink(lora_shrink_kernel<2, 5, true>,
+                             lora_shrink_kernel<2, 5, false>, 2)
+      : a.R16 <= 32 ? shrink(lora_shrink_kernel<4, 3, true>,
+                             lora_shrink_kernel<4, 3, false>, 4)
+                    : shrink(lora_shrink_kernel<8, 2, true>,
+                             lora_shrink_kernel<8, 2, false>, 8);
   if (e != cudaSuccess) return e;
-  auto expand = [&](auto whole, auto any) {
-    return vec ? cudaLaunchKernelEx(&cfg, whole, a)
-               : cudaLaunchKernelEx(&cfg, any, a);
-  };
-  cfg.blockDim = dim3(kLoraThreads);
-  const int kk = a.R16 / 16;
-  if (!tc) {
-    cfg.gridDim = dim3(unsigned((l.N + 31) / 32), tiles);
-    if (kk <= 1)
-      return expand(lora_expand_few_kernel<1, true>, lora_expand_few_kernel<1, false>);
-    if (kk <= 2)
-      return expand(lora_expand_few_kernel<2, true>, lora_expand_few_kernel<2, false>);
-    if (kk <= 4)
-      return expand(lora_expand_few_kernel<4, true>, lora_expand_few_kernel<4, false>);
-    return expand(lora_expand_few_kernel<8, true>, lora_expand_few_kernel<8, false>);
-  }
   return kk <= 2   ? launch_expand<2>(a, cfg)
          : kk <= 4 ? launch_expand<4>(a, cfg)
                    : launch_expand<8>(a, cfg);

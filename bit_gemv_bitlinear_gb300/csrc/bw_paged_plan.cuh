@@ -261,6 +261,9 @@ BW_PLAN_FN int shared_split(int items, int shared, float own, const SharedRates 
   const uint32_t pre = uint32_t(items) * tiles;
   if (pre == 0) return 0;
   if (own <= 0.0f || r.sms < 2) return pre < uint32_t(r.sms) ? int(pre) : r.sms;
+  // room for a CTA a tile, and as much for each of the others
+  if (pre < uint32_t(r.sms) && float(pre) + own <= 1.25f * float(r.sms))
+    return int(pre);
   // n with late + pre pre_us / n = own own_us / (sms - n)
   const float a = float(pre) * r.pre_us, b = own * r.own_us, s = float(r.sms);
   const float h = (a + b - r.late_us * s) / (2.0f * r.late_us);

@@ -380,11 +380,13 @@ prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap qmap,
   uint32_t at = 0, share_end = 0;
   if constexpr (Shared) {
     // all sequences' tiles behind the prefix: how many SMs the decode kernel gets
+    // (the first length is asked for along with the prefix's)
+    int len = tid < a.v.n_seqs ? __ldcg(a.v.len + tid) : 0;
     shared = shared_positions(a.v, a.shared_len);
     void_call = false;
     int own = 0;
     for (int b = tid; b < a.v.n_seqs; b += kPfThreads) {
-      const int len = __ldcg(a.v.len + b);
+      if (b != tid) len = __ldcg(a.v.len + b);
       const int t = len <= a.max_len ? shared_own_tiles(len, shared) : 0;
       own += t + (t > 0);  // below 2^24
     }
