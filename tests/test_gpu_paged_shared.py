@@ -353,6 +353,57 @@ def test_long_prefix(bw):  # noqa: F811
         assert ((got[b].double() - want).abs() <= tol).all()
 
 
+@pytest.mark.parametrize("n,shared,own,H,Hkv,D", [
+    (64, 200, 9000, 20, 5, 128),     # units claimed while the call runs
+    (200, 5000, 2500, 32, 4, 64),
+    (1500, 300, 120, 32, 8, 64),     # more items than SMs: all tiles in one order
+    (4096, 150, 70, 8, 8, 128),
+    (600, 4000, 3, 64, 64, 64),
+    (3, 60000, 30000, 16, 1, 128),
+])
+def test_against_the_decode_call(bw, n, shared, own, H, Hkv, D):  # noqa: F811
+    """Large batches: the decode call over tables that hold the shared pages too
+    (fp32 output, which has tests of its own against 64 bits).  The prefix's
+    weights are rounded to bf16, 2^-8 of the mean of |v| at most; their
+    roundings are independent, and normal values' mean of |v| is below 1."""
+    page = 64
+    gen = torch.Generator(device="cuda").manual_seed(n)
+    lens = [0 if b % 97 == 5 else shared + (own * (b * 0.618 % 1.0)).__int__()
+            for b in range(n)]
+    first, common = shared // page, -(-shared // page)
+    mine = [max(0, -(-x // page) - first) for x in lens]
+    total = common + sum(mine)
+    kp = torch.randn((total, Hkv, page, D), device="cuda", generator=gen).bfloat16()
+    vp = torch.randn((total, Hkv, page, D), device="cuda", generator=gen).bfloat16()
+    order = torch.randperm(total, device="cuda", generator=gen).int()
+    table = torch.full((n, first + max(mine)), -1, dtype=torch.int32)
+    at = common
+    for b in range(n):
+        table[b, first:first + mine[b]] = order[at:at + mine[b]].cpu()
+        at += mine[b]
+    table = table.cuda()
+    whole = table.clone()
+    whole[:, :first] = order[:first]
+    part = shared - first * page  # the page that the prefix ends in, copied
+    if part:
+        for b in range(n):
+            if lens[b] > first * page:
+                for pool in (kp, vp):
+                    pool[int(whole[b, first]), :, :part] = pool[int(order[first]), :, :part]
+    q = (0.7 * torch.randn((n, H, D), device="cuda", generator=gen)).bfloat16()
+    kv_len = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    ws = torch.zeros(bw.bw_attn_paged_shared_workspace_bytes(n, H, Hkv, D),
+                     dtype=torch.uint8, device="cuda")
+    want = bw.bw_attn_paged_decode(q, kp, vp, whole, kv_len)
+    for _ in range(2):
+        got = bw.bw_attn_paged_shared(
+            q, kp, vp, table, kv_len, order[:common].contiguous(),
+            torch.tensor([shared], dtype=torch.int32, device="cuda"), workspace=ws)
+        off = (got.float() - want).abs()
+        assert float((off - 2.0 ** -8 * want.abs()).max()) <= 2.0 ** -8
+    assert bw.bw_device_error() == 0
+
+
 def test_refusals(bw):  # noqa: F811
     c = Batch(14, 64, [3, 4], 8, 2, 64, 16)
 
