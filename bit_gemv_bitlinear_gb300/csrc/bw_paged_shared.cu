@@ -51,19 +51,25 @@ struct SharedJoinArgs {
 
 // kWarps warps a query head: warp w takes parts w, w + kWarps, ...
 template <int D, int kWarps>
-__global__ void __launch_bounds__(kShThreads)
+__global__ void __launch_bounds__(kShThreads, kWarps > 1 ? 1 : D == 64 ? 6 : 5)
 shared_join_kernel(const SharedJoinArgs a) {
   constexpr int kE = D / 32;  // dims a lane
   constexpr int kHeads = kShThreads / 32 / kWarps;
-  constexpr int kAhead = 8;
+  // Alone a warp has few parts, and all CTAs should be there at once (7360 heads
+  // of 64 dims: a call of 30.0 us, 30.9 with 8 parts in flight, half of the CTAs
+  // waiting for the others' registers).
+  constexpr int kAhead = kWarps == 1 ? 3 : 8;
   struct alignas(kE * 4) Piece {
     float v[kE];
   };
   __shared__ float s_max[kShThreads / 32], s_sum[kShThreads / 32];
   __shared__ Piece s_acc[kShThreads / 32][32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int head = blockIdx.x * kHeads + warp / kWarps;
+  const int b = min(head / a.H, a.v.n_seqs - 1), hh = head % a.H;
+  const int g = hh / a.G, h = hh - g * a.G;
   pdl_wait();
   pdl_trigger();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // the claims' two words, as the decode call's join
   uint2 claims = make_uint2(0u, 0u);
   if (blockIdx.x == 0 && threadIdx.x == 0) {
@@ -71,11 +77,6 @@ shared_join_kernel(const SharedJoinArgs a) {
     *reinterpret_cast<uint2 *>(a.claim) = make_uint2(0u, 0u);
     if (claims.x != 0u && claims.y != kDcFirst) atomicOr(a.v.err, kPagedErr);
   }
-  const int head = blockIdx.x * kHeads + warp / kWarps;
-  const int b = min(head / a.H, a.v.n_seqs - 1), hh = head % a.H;
-  const int g = hh / a.G, h = hh - g * a.G;
-  PagedView prefix = a.v;
-  prefix.max_pages = a.shared_pages;
   // (asked for together; reported by the launches before)
   const int shared_n = __ldcg(a.shared_len), len_n = __ldcg(a.v.len + b);
   const int ctas = min(max(__ldcg(a.ctas), 0), kPfMostCtas);
