@@ -46,7 +46,7 @@ constexpr int kLoraRows = 16;
 constexpr int kLoraWarps = 8;
 constexpr int kLoraThreads = kLoraWarps * 32;
 // From this many rows on the second product runs on tcgen05.
-constexpr int kLoraTcRows = 513;
+constexpr int kLoraTcRows = 257;
 
 struct LoraArgs {
   const int8_t *x;
@@ -83,11 +83,11 @@ __device__ __forceinline__ uint32_t codes2(uint32_t w) {
   return *reinterpret_cast<const uint32_t *>(&d);
 }
 
-// The adapter of this lane's row (lanes 0 .. n - 1: row0 + lane), -1 for none.
-__device__ __forceinline__ int lane_adapter(const LoraArgs &a, int row0, int n) {
+// The adapter of this lane's row (lanes 0..15: row0 + lane), -1 for none.
+__device__ __forceinline__ int lane_adapter(const LoraArgs &a, int row0) {
   const int lane = threadIdx.x & 31;
   int id = -1;
-  if (lane < n && row0 + lane < a.M) {
+  if (lane < kLoraRows && row0 + lane < a.M) {
     id = __ldcg(a.adapter + row0 + lane);
     if (id < -1 || id >= a.n_adapters) {
       atomicOr(a.err, kLoraErr);
@@ -149,7 +149,7 @@ lora_shrink_kernel(const LoraArgs a) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int row0 = blockIdx.x * kLoraRows, r0 = blockIdx.y * 8 * NT;
   const int fr = lane >> 2, fc = lane & 3;
-  const int mine = lane_adapter(a, row0, kLoraRows);
+  const int mine = lane_adapter(a, row0);
   unsigned left = __ballot_sync(0xffffffffu, mine >= 0), rows;
   const int8_t *x0 = a.x + int64_t(min(row0 + fr, a.M - 1)) * a.K;
   const int8_t *x1 = a.x + int64_t(min(row0 + fr + 8, a.M - 1)) * a.K;
@@ -230,16 +230,17 @@ lora_shrink_kernel(const LoraArgs a) {
 __device__ __forceinline__ int column_of(int t, int j) {
   return 8 * (j >> 1) + 2 * t + (j & 1);
 }
-// B's fragments of 32 columns: 16 values of R a step, 4 consecutive ones a lane.
-template <int KK>
-__device__ __forceinline__ void load_b(const LoraArgs &a, int id, int n0,
-                                       uint2 (&b)[KK][4]) {
-  const int lane = threadIdx.x & 31, r0 = 4 * (lane & 3);
+// B's fragments of 32 columns, from value r0 of R on: 16 values a step, 4
+// consecutive ones a lane.
+template <int kSteps>
+__device__ __forceinline__ void load_b(const LoraArgs &a, int id, int n0, int r0,
+                                       uint2 (&b)[kSteps][4]) {
+  const int lane = threadIdx.x & 31;
 #pragma unroll
-  for (int k = 0; k < KK; ++k)
+  for (int k = 0; k < kSteps; ++k)
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
-      const int col = n0 + column_of(t, lane >> 2), r = 16 * k + r0;
+      const int col = n0 + column_of(t, lane >> 2), r = r0 + 16 * k + 4 * (lane & 3);
       b[k][t] = make_uint2(0u, 0u);
       if (col < a.N && r < a.R)
         b[k][t] = __ldg(reinterpret_cast<const uint2 *>(
@@ -258,13 +259,12 @@ __device__ __forceinline__ void keep_rows(unsigned rows, const float (&p)[4][4],
     if (r1) c[t][2] += p[t][2], c[t][3] += p[t][3];
   }
 }
-// y's columns col .. col + 7 of a row, and out = y + c.  Vec: 16-byte aligned
+// y's columns col .. col + 7 of a row (-1: none), and out = y + c.  Vec: 16-byte aligned
 // rows; ends of rows and others go value by value.
 template <bool Vec>
-__device__ __forceinline__ uint4 load_y(const LoraArgs &a, int row, int end,
-                                        int col) {
+__device__ __forceinline__ uint4 load_y(const LoraArgs &a, int row, int col) {
   uint4 w = make_uint4(0u, 0u, 0u, 0u);
-  if (row >= end) return w;
+  if (row < 0) return w;
   const __nv_bfloat16 *y = a.y + row * a.y_ld + col;
   if (Vec && col + 8 <= a.N) return *reinterpret_cast<const uint4 *>(y);
   uint32_t *p = reinterpret_cast<uint32_t *>(&w);
@@ -284,9 +284,9 @@ __device__ __forceinline__ uint32_t pair_of(float lo, float hi) {
   return *reinterpret_cast<const uint32_t *>(&t);
 }
 template <bool Vec>
-__device__ __forceinline__ void store_row(const LoraArgs &a, int row, int end,
-                                          int col, const uint32_t (&w)[4]) {
-  if (row >= end) return;
+__device__ __forceinline__ void store_row(const LoraArgs &a, int row, int col,
+                                          const uint32_t (&w)[4]) {
+  if (row < 0) return;
   __nv_bfloat16 *o = a.out + row * a.out_ld + col;
   if (Vec && col + 8 <= a.N) {
     *reinterpret_cast<uint4 *>(o) = make_uint4(w[0], w[1], w[2], w[3]);
@@ -299,14 +299,16 @@ __device__ __forceinline__ void store_row(const LoraArgs &a, int row, int end,
 }
 
 // ---- few rows: both products in one launch ----
-// A cluster of 16 CTAs takes a tile of 16 rows, or of 8 where there is room for
-// twice as many clusters.  First each CTA multiplies its
-// sixteenth of the K axis, a warp 16 of an adapter's R rows at a time; the sums
-// meet in every CTA, read out of the others' shared memory in one order.  Then
-// each CTA has a sixteenth of the columns, a warp 32 at a time, and adds the
-// tile's adapters in turn; B's first fragments are asked for before the sums
-// meet.
-constexpr int kClCtas = 16;
+// A cluster of 8 or 16 CTAs takes a tile of 16 rows, or of 8 where there is room for
+// twice as many clusters.  Where there are several tiles, rows are taken in the
+// order of their adapters, so that a tile has few of them.  First each CTA
+// multiplies its share of the K axis, a warp 16 of an adapter's R rows at a time;
+// the sums meet in every CTA, read out of the others' shared memory in one order.
+// Then each CTA has a share of the columns, a warp 32 at a time, and adds the tile's
+// adapters in turn; B's first fragments are asked for before the sums meet.  Wide
+// projections have several clusters a tile, each with its share of the columns (u
+// is made by all of them).
+constexpr int kSortMost = 512;  // rows that are put in order
 __device__ __forceinline__ void cluster_arrive() {
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
 }
@@ -333,23 +335,96 @@ __device__ __forceinline__ int place_of(int r) {
   return (r & ~15) + 2 * ((r >> 2) & 3) + (r & 1) + ((r & 2) << 2);
 }
 
+struct FewCut {
+  int tile, ctas;  // rows, CTAs of a cluster
+  bool sort, vec;  // vec: rows of y and out are aligned for vectors
+};
+
+// The row and the adapter of lane l (0..15) of tile t, -1 where there is none.  A
+// row's place in the order of the adapters (rows without one last) is the number of
+// rows before it: keys of 16 bits of adapter and 9 of row, counted by all threads.
+__device__ __forceinline__ void tile_rows(const LoraArgs &a, const FewCut &cut,
+                                          int t, int *s_row, int *s_of,
+                                          uint4 *s_key, int &row, int &id) {
+  static_assert(BW_LORA_MAX_ADAPTERS <= 1 << 16 && kSortMost <= 1 << 9, "keys");
+  const int lane = threadIdx.x & 31, first = t * cut.tile;
+  auto adapter_of = [&](int i) {
+    int x = __ldcg(a.adapter + i);
+    if (x < -1 || x >= a.n_adapters) {
+      atomicOr(a.err, kLoraErr);
+      x = -1;
+    }
+    return x;
+  };
+  row = id = -1;
+  if (!cut.sort) {
+    if (lane < cut.tile && first + lane < a.M) {
+      row = first + lane;
+      id = adapter_of(row);
+    }
+    if (threadIdx.x < kLoraRows) {
+      s_row[threadIdx.x] = row;
+      s_of[threadIdx.x] = id;
+    }
+    return;
+  }
+  uint32_t *key = reinterpret_cast<uint32_t *>(s_key);
+  const int n4 = (a.M + 3) / 4;
+  uint32_t mine[kSortMost / kLoraThreads];
+  int before[kSortMost / kLoraThreads] = {};
+#pragma unroll
+  for (int k = 0; k < kSortMost / kLoraThreads; ++k) {
+    const int i = threadIdx.x + k * kLoraThreads;
+    mine[k] = 0xffffffffu;
+    if (i < a.M) {
+      const int x = adapter_of(i);
+      mine[k] = uint32_t(x < 0 ? 1 << 16 : x) << 9 | uint32_t(i);
+    }
+    if (i < 4 * n4) key[i] = mine[k];
+  }
+  if (threadIdx.x < kLoraRows) s_row[threadIdx.x] = s_of[threadIdx.x] = -1;
+  __syncthreads();
+  for (int j = 0; j < n4; ++j) {
+    const uint4 o = s_key[j];
+#pragma unroll
+    for (int k = 0; k < kSortMost / kLoraThreads; ++k)
+      before[k] += (o.x < mine[k]) + (o.y < mine[k]) + (o.z < mine[k]) + (o.w < mine[k]);
+  }
+#pragma unroll
+  for (int k = 0; k < kSortMost / kLoraThreads; ++k) {
+    const int at = before[k] - first;
+    if (mine[k] != 0xffffffffu && at >= 0 && at < cut.tile) {
+      s_row[at] = int(mine[k] & 511u);
+      s_of[at] = mine[k] >> 25 ? -1 : int(mine[k] >> 9);
+    }
+  }
+  __syncthreads();
+  if (lane < kLoraRows) {
+    row = s_row[lane];
+    id = s_of[lane];
+  }
+}
+
 template <int KK, bool VecK>
-__global__ void __launch_bounds__(kLoraThreads)
-lora_few_kernel(const LoraArgs a, int vec, int tile) {
-  constexpr int kAhead = 5;            // blocks of 32 of K in flight
-  constexpr int kHeld = KK <= 4 ? 8 / KK : 1;  // adapters' B in flight
+__global__ void __launch_bounds__(kLoraThreads, 2)
+lora_few_kernel(const LoraArgs a, const FewCut cut) {
+  constexpr int kAhead = 5;                   // blocks of 32 of K in flight
+  constexpr int kSteps = KK <= 4 ? KK : 4;    // of 16 of R in a piece of B
+  constexpr int kPieces = KK / kSteps;        // of an adapter
+  constexpr int kHeld = 8 / kSteps;           // in flight
   constexpr int kStride = 16 * KK + 8;  // odd in 16 bytes: eight rows meet all banks
   __shared__ __align__(16) float s_part[kLoraRows][16 * KK];
   __shared__ __align__(16) __nv_bfloat16 s_u[2][kLoraRows][kStride];  // hi, lo
-  __shared__ int s_id[kLoraRows], s_count;
+  __shared__ uint4 s_key[kSortMost / 4];
+  __shared__ int s_row[kLoraRows], s_of[kLoraRows], s_id[kLoraRows], s_count;
   __shared__ unsigned s_rows[kLoraRows];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rank = blockIdx.x, row0 = blockIdx.y * tile;
-  const int end = min(row0 + tile, a.M);
+  const int rank = blockIdx.x, ctas = cut.ctas;
   const int fr = lane >> 2, fc = lane & 3;
   pipe::pdl_wait();
   pipe::pdl_trigger();
-  const int mine = lane_adapter(a, row0, tile);
+  int my_row, mine;
+  tile_rows(a, cut, blockIdx.y, s_row, s_of, s_key, my_row, mine);
   unsigned left = __ballot_sync(0xffffffffu, mine >= 0);
   const unsigned with = left;
   if (warp == 0) {
@@ -361,12 +436,14 @@ lora_few_kernel(const LoraArgs a, int vec, int tile) {
   }
   __syncthreads();
   const int count = s_count;
+  const int rows_of[2] = {__shfl_sync(0xffffffffu, my_row, fr),
+                          __shfl_sync(0xffffffffu, my_row, fr + 8)};
 
   // ---- u: this CTA's blocks of K ----
   const int blocks = (a.K + 31) / 32, groups = a.R16 / 16;
-  const int b_lo = rank * blocks / kClCtas, b_hi = (rank + 1) * blocks / kClCtas;
-  const int8_t *x0 = a.x + int64_t(min(row0 + fr, a.M - 1)) * a.K;
-  const int8_t *x1 = a.x + int64_t(min(row0 + fr + 8, a.M - 1)) * a.K;
+  const int b_lo = rank * blocks / ctas, b_hi = (rank + 1) * blocks / ctas;
+  const int8_t *x0 = a.x + int64_t(max(rows_of[0], 0)) * a.K;
+  const int8_t *x1 = a.x + int64_t(max(rows_of[1], 0)) * a.K;
   for (int task = warp; task < count * groups; task += kLoraWarps) {
     const int j = task / groups, r0 = (task - j * groups) * 16;
     const __nv_bfloat16 *A = a.A + (int64_t(s_id[j]) * a.R + r0 + fr) * a.K;
@@ -411,19 +488,26 @@ lora_few_kernel(const LoraArgs a, int vec, int tile) {
   cluster_arrive();
 
   // ---- what the second product needs meanwhile ----
-  const int col_groups = (a.N + 31) / 32;
-  int cg = rank + kClCtas * warp;
-  uint2 b[kHeld][KK][4];
+  const int col_groups = (a.N + 31) / 32, step = int(gridDim.z) * ctas * kLoraWarps;
+  int cg = (int(blockIdx.z) * kLoraWarps + warp) * ctas + rank;
+  uint2 b[kHeld][kSteps][4];
   uint4 y[2];
+  auto ask_b = [&](int piece0) {
+#pragma unroll
+    for (int u = 0; u < kHeld; ++u) {
+      const int piece = piece0 + u;
+      if (piece < count * kPieces)
+        load_b<kSteps>(a, s_id[piece / kPieces], 32 * cg,
+                       piece % kPieces * kSteps * 16, b[u]);
+    }
+  };
   auto ask = [&] {
     if (cg >= col_groups) return;
 #pragma unroll
     for (int half = 0; half < 2; ++half)
-      y[half] = vec ? load_y<true>(a, row0 + fr + 8 * half, end, 32 * cg + 8 * fc)
-                    : load_y<false>(a, row0 + fr + 8 * half, end, 32 * cg + 8 * fc);
-#pragma unroll
-    for (int u = 0; u < kHeld; ++u)
-      if (u < count) load_b<KK>(a, s_id[u], 32 * cg, b[u]);
+      y[half] = cut.vec ? load_y<true>(a, rows_of[half], 32 * cg + 8 * fc)
+                        : load_y<false>(a, rows_of[half], 32 * cg + 8 * fc);
+    ask_b(0);
   };
   ask();
   cluster_wait();
@@ -433,14 +517,16 @@ lora_few_kernel(const LoraArgs a, int vec, int tile) {
     const int row = i / (a.R16 / 4), r = (i - row * (a.R16 / 4)) * 4;
     float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     if (with >> row & 1u) {
-      float4 p[kClCtas];
+      for (int k0 = 0; k0 < ctas; k0 += 8) {
+        float4 p[8];
 #pragma unroll
-      for (int k = 0; k < kClCtas; ++k) p[k] = load_of_cta(&s_part[row][r], k);
+        for (int k = 0; k < 8; ++k) p[k] = load_of_cta(&s_part[row][r], k0 + k);
 #pragma unroll
-      for (int k = 0; k < kClCtas; ++k)
-        v.x += p[k].x, v.y += p[k].y, v.z += p[k].z, v.w += p[k].w;
-      const int id = __ldcg(a.adapter + row0 + row);
-      const float f = (a.scale ? __ldcg(a.scale + id) : 1.0f) / __ldcg(a.s + row0 + row);
+        for (int k = 0; k < 8; ++k)
+          v.x += p[k].x, v.y += p[k].y, v.z += p[k].z, v.w += p[k].w;
+      }
+      const float f = (a.scale ? __ldcg(a.scale + s_of[row]) : 1.0f) /
+                      __ldcg(a.s + s_row[row]);
       v.x *= f, v.y *= f, v.z *= f, v.w *= f;
     }
     const uint32_t h0 = pair_of(v.x, v.y), h1 = pair_of(v.z, v.w);
@@ -464,25 +550,23 @@ lora_few_kernel(const LoraArgs a, int vec, int tile) {
                      {low_of(y[0].y), high_of(y[0].y), low_of(y[1].y), high_of(y[1].y)},
                      {low_of(y[0].z), high_of(y[0].z), low_of(y[1].z), high_of(y[1].z)},
                      {low_of(y[0].w), high_of(y[0].w), low_of(y[1].w), high_of(y[1].w)}};
-    for (int j0 = 0; j0 < count; j0 += kHeld) {
-      if (j0 > 0)
-#pragma unroll
-        for (int u = 0; u < kHeld; ++u)
-          if (j0 + u < count) load_b<KK>(a, s_id[j0 + u], 32 * cg, b[u]);
+    for (int piece0 = 0; piece0 < count * kPieces; piece0 += kHeld) {
+      if (piece0 > 0) ask_b(piece0);
 #pragma unroll
       for (int u = 0; u < kHeld; ++u) {
-        if (j0 + u >= count) break;
+        const int piece = piece0 + u, r0 = piece % kPieces * kSteps * 16;
+        if (piece >= count * kPieces) break;
         float p[4][4] = {};
 #pragma unroll
-        for (int k = 0; k < KK; ++k) {
-          if (16 * k >= a.R16) break;
+        for (int k = 0; k < kSteps; ++k) {
+          if (r0 + 16 * k >= a.R16) break;
           uint32_t f[2][4];
 #pragma unroll
           for (int e = 0; e < 2; ++e)
             asm volatile(
                 "ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
                 : "=r"(f[e][0]), "=r"(f[e][1]), "=r"(f[e][2]), "=r"(f[e][3])
-                : "r"(u_at + e * kLo + 32 * k)
+                : "r"(u_at + e * kLo + 2 * r0 + 32 * k)
                 : "memory");
 #pragma unroll
           for (int t = 0; t < 4; ++t) {
@@ -490,7 +574,7 @@ lora_few_kernel(const LoraArgs a, int vec, int tile) {
             mma16816(p[t], f[0], b[u][k][t].x, b[u][k][t].y);
           }
         }
-        keep_rows(s_rows[j0 + u], p, c);
+        keep_rows(s_rows[piece / kPieces], p, c);
       }
     }
 #pragma unroll
@@ -499,12 +583,12 @@ lora_few_kernel(const LoraArgs a, int vec, int tile) {
                              pair_of(c[1][2 * half], c[1][2 * half + 1]),
                              pair_of(c[2][2 * half], c[2][2 * half + 1]),
                              pair_of(c[3][2 * half], c[3][2 * half + 1])};
-      if (vec)
-        store_row<true>(a, row0 + fr + 8 * half, end, 32 * cg + 8 * fc, w);
+      if (cut.vec)
+        store_row<true>(a, rows_of[half], 32 * cg + 8 * fc, w);
       else
-        store_row<false>(a, row0 + fr + 8 * half, end, 32 * cg + 8 * fc, w);
+        store_row<false>(a, rows_of[half], 32 * cg + 8 * fc, w);
     }
-    cg += kClCtas * kLoraWarps;
+    cg += step;
     ask();
   }
   cluster_wait();  // (a CTA's sums stay until all have read them)
@@ -824,13 +908,13 @@ cudaError_t once(std::atomic<bool> *done, Kernel kernel, cudaFuncAttribute what,
 }
 
 template <int KK>
-cudaError_t launch_few(const LoraArgs &a, bool vec, bool vec_k, int tile,
+cudaError_t launch_few(const LoraArgs &a, const FewCut &cut, bool vec_k,
                        cudaLaunchConfig_t &cfg) {
   static std::atomic<bool> done[2][64];
   auto go = [&](auto kernel, std::atomic<bool> *d) {
     const cudaError_t e =
         once(d, kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    return e != cudaSuccess ? e : cudaLaunchKernelEx(&cfg, kernel, a, int(vec), tile);
+    return e != cudaSuccess ? e : cudaLaunchKernelEx(&cfg, kernel, a, cut);
   };
   return vec_k ? go(lora_few_kernel<KK, true>, done[0])
                : go(lora_few_kernel<KK, false>, done[1]);
@@ -903,7 +987,7 @@ cudaError_t launch_lora(const LoraLaunch &l, cudaStream_t stream) {
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = kClCtas;
+  attr[1].val.clusterDim.x = 8;
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   const unsigned tiles = unsigned((l.M + kLoraRows - 1) / kLoraRows);
@@ -914,15 +998,25 @@ cudaError_t launch_lora(const LoraLaunch &l, cudaStream_t stream) {
   // (tensor maps' strides are below 2^40 bytes)
   if (!vec || l.M < kLoraTcRows || int64_t(a.R) * l.N >= (int64_t(1) << 38)) {
     cfg.numAttrs = 2;
-    // Tiles of 8 where all of them run at once (61 rows of 48 adapters, 3840 x
-    // 2560: 8.6 us, 10.8 with tiles of 16).
-    const int tile = 2 * tiles * kClCtas <= 2u * unsigned(device_sm_count()) ? 8 : kLoraRows;
-    cfg.gridDim = dim3(kClCtas, unsigned((l.M + tile - 1) / tile));
+    // Two CTAs an SM, clusters of 16 for a tile or two (a device has room for 14 of
+    // those, and 36 of 8).
+    FewCut cut{};
+    cut.vec = vec;
+    cut.sort = l.M > kLoraRows && l.M <= kSortMost;
+    cut.ctas = l.M <= kLoraRows ? 16 : 8;
+    const int room = device_sm_count() * 2 / cut.ctas;
+    cut.tile = (l.M + 7) / 8 <= room ? 8 : kLoraRows;
+    const int all = (l.M + cut.tile - 1) / cut.tile;
+    // clusters a tile: a warp has 32 columns then, where there is room
+    const int wide = ((l.N + 31) / 32 + cut.ctas * kLoraWarps - 1) / (cut.ctas * kLoraWarps);
+    const int z = std::max(1, std::min(wide, room / all));
+    attr[1].val.clusterDim.x = unsigned(cut.ctas);
+    cfg.gridDim = dim3(unsigned(cut.ctas), unsigned(all), unsigned(z));
     cfg.blockDim = dim3(kLoraThreads);
-    if (kk <= 1) return launch_few<1>(a, vec, vec_k, tile, cfg);
-    if (kk <= 2) return launch_few<2>(a, vec, vec_k, tile, cfg);
-    if (kk <= 4) return launch_few<4>(a, vec, vec_k, tile, cfg);
-    return launch_few<8>(a, vec, vec_k, tile, cfg);
+    if (kk <= 1) return launch_few<1>(a, cut, vec_k, cfg);
+    if (kk <= 2) return launch_few<2>(a, cut, vec_k, cfg);
+    if (kk <= 4) return launch_few<4>(a, cut, vec_k, cfg);
+    return launch_few<8>(a, cut, vec_k, cfg);
   }
   cfg.numAttrs = 1;
   auto shrink = [&](auto whole, auto any, int nt) {
