@@ -21,19 +21,18 @@
 //    16 consecutive bytes of an adapter's row for two products' fragments (and 8
 //    codes, made bf16 by four operations a pair), straight from global memory;
 //    and the columns of the second product, so a lane stores 16 bytes of out.
-//  * few rows: one launch, a cluster of 16 CTAs a tile (lora_few_kernel).  Two
-//    launches with u in memory between them took 4.7 us for one row of 2560 x 2560
-//    at rank 16 and 9.1 for 61 of 48 adapters, 3840 x 2560; so it is 4.3 and 8.6,
-//    of which the exchanges (loads of the numbers, of A, of the sums, of B) are
-//    most: 82 + 82 KB of weights come in well under 1.
-//  * many rows: u first, a CTA a tile, its adapters (two CTAs in turn, or a tile
-//    that two requests share holds up the rest) and up to 64 of its R rows, the
-//    warps cut the K axis and add up in shared memory; then the second product on
-//    tcgen05, 128 rows by 128 columns.
-// 2011 rows of 5 adapters of rank 64, 13824 x 2560: 34 us, 0.56 of the measured copy
-// rate (7 for u, 26 for the rest, which waits for y: with mma.sync and y in
-// registers that was 40, 500 instructions a warp for 32 x 32 outputs, 10 cycles
-// each).
+//  * few rows: one launch, a cluster of CTAs a tile (lora_few_kernel).  One row of
+//    2560 x 2560 at rank 16: 4.7 us; 61 rows of 48 adapters, 3840 x 2560: 9.4, of
+//    which the exchanges (loads of the numbers, of A, of the sums, of B) are most.
+//    (Two launches with u in memory between them took as long, and 1.7 more of the
+//    host's.)
+//  * many rows: u first, a cluster of CTAs for 32 rows and up to 64 of an adapter's
+//    R rows, the K axis cut over CTAs and warps; then the second product on tcgen05,
+//    128 rows by 128 columns.
+// 2011 rows of 5 adapters of rank 64, 13824 x 2560: 33 us, 0.57 of the measured copy
+// rate (the first product about 9 of it; the second waits for y: with mma.sync and
+// y in registers it was 40 by itself, 500 instructions a warp for 32 x 32 outputs,
+// 10 cycles each).
 #include <algorithm>
 
 #include "bw_serve.cuh"
@@ -45,8 +44,12 @@ namespace {
 constexpr int kLoraRows = 16;
 constexpr int kLoraWarps = 8;
 constexpr int kLoraThreads = kLoraWarps * 32;
-// From this many rows on the second product runs on tcgen05.
-constexpr int kLoraTcRows = 257;
+// From this many rows on there are two launches, the second on tcgen05.  That goes
+// by the distinct adapters of 32 and of 128 rows, one launch by those of the batch
+// (its rows are put in order): 512 rows of 4 requests by 13824, rank 64, take 19 us
+// in two launches and 34 in one; 512 rows of 64 adapters in any order, rank 128,
+// 470 and 69.
+constexpr int kLoraTcRows = 513;
 
 struct LoraArgs {
   const int8_t *x;
@@ -72,6 +75,15 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4],
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// A pair of bf16 as fp32, and back.
+__device__ __forceinline__ float low_of(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float high_of(uint32_t w) {
+  return __uint_as_float(w & 0xffff0000u);
+}
+__device__ __forceinline__ uint32_t pair_of(float lo, float hi) {
+  const __nv_bfloat162 t = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t *>(&t);
+}
 // Codes (bytes 2 h, 2 h + 1 of w) as a bf16 pair: 0x43 in front of a byte's low
 // seven bits reads as 128 + them; 128 (codes from 0 on) or 256 (below) less.
 template <int h>
@@ -83,19 +95,6 @@ __device__ __forceinline__ uint32_t codes2(uint32_t w) {
   return *reinterpret_cast<const uint32_t *>(&d);
 }
 
-// The adapter of this lane's row (lanes 0..15: row0 + lane), -1 for none.
-__device__ __forceinline__ int lane_adapter(const LoraArgs &a, int row0) {
-  const int lane = threadIdx.x & 31;
-  int id = -1;
-  if (lane < kLoraRows && row0 + lane < a.M) {
-    id = __ldcg(a.adapter + row0 + lane);
-    if (id < -1 || id >= a.n_adapters) {
-      atomicOr(a.err, kLoraErr);
-      id = -1;
-    }
-  }
-  return id;
-}
 // The distinct adapters of a tile in turn: id and the lanes (rows) that have it;
 // false after the last.
 __device__ __forceinline__ bool next_adapter(int mine, unsigned &left, int &id,
@@ -138,86 +137,147 @@ __device__ __forceinline__ uint2 load_x8(const int8_t *p, int n) {
   return r;
 }
 
-// u of a tile's rows for adapters z, z + gridDim.z, ... of the tile, rows
-// [8 NT y, 8 NT (y + 1)) of A; kAhead blocks of 32 values of K in flight a warp.
-template <int NT, int kAhead, bool Vec>
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// 16 bytes at `p`'s place in another CTA's shared memory.
+__device__ __forceinline__ float4 load_of_cta(const float *p, uint32_t rank) {
+  uint32_t at;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
+               : "=r"(at)
+               : "r"(pipe::smem_addr(p)), "r"(rank));
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(at)
+               : "memory");
+  return v;
+}
+// ---- the first product for many rows ----
+// A cluster takes a tile of 32 rows and 64 of an adapter's R rows (16 or 32 where R
+// is no larger), its CTAs a share of the K axis each; the warps cut that share once
+// more and take all 64 columns, kAhead blocks of 32 values in flight.  The sums of
+// warps and CTAs meet through shared memory, in one order, each CTA making some
+// rows.  A tile's adapters go to two clusters in turn, or a tile that two requests
+// share holds up the rest.  (Tiles of 16 rows without clusters: 36 us a call of 2560 x
+// 6912, 28.6 so; tiles through shared memory, copied five stages ahead: 50.)
+constexpr int kShRows = 32;
+template <int NT>  // groups of 8 columns
+struct ShrinkCfg {
+  static constexpr int kAhead = NT == 2 ? 5 : NT == 4 ? 3 : 2;
+  static constexpr int kLd = 8 * NT + 4;  // floats a row of sums
+  static constexpr uint32_t kWarp = 2 * NT * 32 * 16;  // a warp's sums
+  static constexpr uint32_t kPart = kLoraWarps * kWarp;
+  static constexpr uint32_t kSmem = kPart + kShRows * kLd * 4;
+};
+template <int NT>
 __global__ void __launch_bounds__(kLoraThreads, 1)
-lora_shrink_kernel(const LoraArgs a) {
-  __shared__ float s_sum[kLoraWarps][NT][32][4];
+lora_shrink_kernel(const LoraArgs a, int ctas) {
+  using C = ShrinkCfg<NT>;
+  constexpr int kAhead = C::kAhead;
+  extern __shared__ __align__(16) uint8_t smem[];
+  float4 *s_warp = reinterpret_cast<float4 *>(smem);  // [warp][row tile][NT][lane]
+  float *s_part = reinterpret_cast<float *>(smem + C::kPart);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = blockIdx.x, row0 = blockIdx.y * kShRows, r0 = (blockIdx.z >> 1) * 8 * NT;
+  const int fr = lane >> 2, fc = lane & 3;
   pipe::pdl_wait();
   pipe::pdl_trigger();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int row0 = blockIdx.x * kLoraRows, r0 = blockIdx.y * 8 * NT;
-  const int fr = lane >> 2, fc = lane & 3;
-  const int mine = lane_adapter(a, row0);
+  int mine = row0 + lane < a.M ? __ldcg(a.adapter + row0 + lane) : -1;
+  if (mine < -1 || mine >= a.n_adapters) {
+    atomicOr(a.err, kLoraErr);
+    mine = -1;
+  }
   unsigned left = __ballot_sync(0xffffffffu, mine >= 0), rows;
-  const int8_t *x0 = a.x + int64_t(min(row0 + fr, a.M - 1)) * a.K;
-  const int8_t *x1 = a.x + int64_t(min(row0 + fr + 8, a.M - 1)) * a.K;
-  // the row of the values that this thread adds up
-  const int out_row = ((threadIdx.x >> 3) & 7) + 8 * (threadIdx.x & 1);
+  // this CTA's blocks of 32 values of K, every kLoraWarps-th one this warp's
+  const int blocks = (a.K + 31) / 32;
+  const int lo = rank * blocks / ctas, hi = (rank + 1) * blocks / ctas;
+  const int8_t *x = a.x + int64_t(min(row0 + fr, a.M - 1)) * a.K;
+  int64_t x_at[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    x_at[e] = int64_t(min(row0 + fr + 8 * e, a.M - 1) - min(row0 + fr, a.M - 1)) * a.K;
   int id;
   for (int j = 0; next_adapter(mine, left, id, rows); ++j) {
-    if (j % int(gridDim.z) != int(blockIdx.z)) continue;
+    if ((j ^ int(blockIdx.z)) & 1) continue;
     const __nv_bfloat16 *A =
-        a.A + (int64_t(id) * a.R + r0 + fr) * a.K;  // row 8 t + fr of tile t
-    const float scale = a.scale ? __ldcg(a.scale + id) : 1.0f;
-    const float row_s = __ldcg(a.s + min(row0 + out_row, a.M - 1));
-    float c[NT][4] = {};
+        a.A + (int64_t(id) * a.R + r0 + fr) * a.K;  // row 8 t + fr of group t
+    float c[2][NT][4] = {};
 #pragma unroll 1
-    for (int k0 = warp * 32; k0 < a.K; k0 += kLoraWarps * 32 * kAhead) {
-      uint2 xa[kAhead], xb[kAhead];
+    for (int b0 = lo + warp; b0 < hi; b0 += kLoraWarps * kAhead) {
+      uint2 v[kAhead][4];
       uint4 b[kAhead][NT];
 #pragma unroll
       for (int h = 0; h < kAhead; ++h) {
-        const int k = k0 + h * kLoraWarps * 32 + 8 * fc;
-        const int n = min(a.K - k, 8);
-        xa[h] = load_x8<Vec>(x0 + k, n);
-        xb[h] = load_x8<Vec>(x1 + k, n);
+        const int blk = b0 + h * kLoraWarps, k = blk * 32 + 8 * fc;
+        const int n = blk < hi ? min(a.K - k, 8) : 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[h][e] = load_x8<true>(x + x_at[e] + k, n);
 #pragma unroll
         for (int t = 0; t < NT; ++t)
-          b[h][t] = load_a8<Vec>(A + int64_t(8 * t) * a.K + k,
-                                 r0 + 8 * t < a.R ? n : 0);
+          b[h][t] = load_a8<true>(A + int64_t(8 * t) * a.K + k, r0 + 8 * t < a.R ? n : 0);
       }
 #pragma unroll
-      for (int h = 0; h < kAhead; ++h) {
-        const uint32_t f0[4] = {codes2<0>(xa[h].x), codes2<0>(xb[h].x),
-                                codes2<1>(xa[h].x), codes2<1>(xb[h].x)};
-        const uint32_t f1[4] = {codes2<0>(xa[h].y), codes2<0>(xb[h].y),
-                                codes2<1>(xa[h].y), codes2<1>(xb[h].y)};
+      for (int h = 0; h < kAhead; ++h)
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          mma16816(c[t], f0, b[h][t].x, b[h][t].y);
-          mma16816(c[t], f1, b[h][t].z, b[h][t].w);
+        for (int rt = 0; rt < 2; ++rt) {
+          const uint2 xa = v[h][2 * rt], xb = v[h][2 * rt + 1];
+          const uint32_t f0[4] = {codes2<0>(xa.x), codes2<0>(xb.x), codes2<1>(xa.x),
+                                  codes2<1>(xb.x)};
+          const uint32_t f1[4] = {codes2<0>(xa.y), codes2<0>(xb.y), codes2<1>(xa.y),
+                                  codes2<1>(xb.y)};
+#pragma unroll
+          for (int t = 0; t < NT; ++t) {
+            mma16816(c[rt][t], f0, b[h][t].x, b[h][t].y);
+            mma16816(c[rt][t], f1, b[h][t].z, b[h][t].w);
+          }
         }
-      }
     }
-    __syncthreads();  // the sums of the adapter before have been read
 #pragma unroll
-    for (int t = 0; t < NT; ++t)
-      *reinterpret_cast<float4 *>(s_sum[warp][t][lane]) =
-          make_float4(c[t][0], c[t][1], c[t][2], c[t][3]);
+    for (int rt = 0; rt < 2; ++rt)
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+        s_warp[((warp * 2 + rt) * NT + t) * 32 + lane] =
+            make_float4(c[rt][t][0], c[rt][t][1], c[rt][t][2], c[rt][t][3]);
     __syncthreads();
-    // element e of lane l, tile t: row l / 4 (+ 8), column 8 t + 2 (l mod 4) + ..
-    for (int t = threadIdx.x >> 6; t < NT; t += kLoraWarps / 2) {
-      const int half = threadIdx.x & 1, l = (threadIdx.x >> 1) & 31;
-      const int row = out_row, col = r0 + 8 * t + 2 * (l & 3);
-      if (!(rows >> row & 1u) || col >= a.R16) continue;
-      float v0 = 0.0f, v1 = 0.0f;
+    // the warps' sums; of lane l: row l / 4 (+ 8), columns 2 (l mod 4) and on
+    for (int i = threadIdx.x; i < 2 * NT * 32; i += kLoraThreads) {
+      float4 v = s_warp[i];
 #pragma unroll
-      for (int w = 0; w < kLoraWarps; ++w) {
-        v0 += s_sum[w][t][l][2 * half];
-        v1 += s_sum[w][t][l][2 * half + 1];
+      for (int w = 1; w < kLoraWarps; ++w) {
+        const float4 p = s_warp[w * 2 * NT * 32 + i];
+        v.x += p.x, v.y += p.y, v.z += p.z, v.w += p.w;
       }
-      const float f = scale / row_s;
-      v0 *= f;
-      v1 *= f;
-      const __nv_bfloat162 hi = __floats2bfloat162_rn(v0, v1);
-      const __nv_bfloat162 lo = __floats2bfloat162_rn(
-          v0 - __low2float(hi), v1 - __high2float(hi));
-      __nv_bfloat16 *to = a.u + int64_t(row0 + row) * 2 * a.R16 + col;
-      *reinterpret_cast<__nv_bfloat162 *>(to) = hi;
-      *reinterpret_cast<__nv_bfloat162 *>(to + a.R16) = lo;
+      const int l = i & 31, t = (i >> 5) % NT, rt = (i >> 5) / NT;
+      float *to = s_part + (16 * rt + (l >> 2)) * C::kLd + 8 * t + 2 * (l & 3);
+      *reinterpret_cast<float2 *>(to) = make_float2(v.x, v.y);
+      *reinterpret_cast<float2 *>(to + 8 * C::kLd) = make_float2(v.z, v.w);
     }
+    cluster_arrive();
+    cluster_wait();
+    const float scale = a.scale ? __ldcg(a.scale + id) : 1.0f;
+    for (int i = threadIdx.x; i < kShRows / ctas * (2 * NT); i += kLoraThreads) {
+      const int row = rank * (kShRows / ctas) + i / (2 * NT), col = i % (2 * NT) * 4;
+      if (!(rows >> row & 1u) || r0 + col >= a.R16) continue;
+      float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      for (int k = 0; k < ctas; ++k) {
+        const float4 p = load_of_cta(s_part + row * C::kLd + col, k);
+        v.x += p.x, v.y += p.y, v.z += p.z, v.w += p.w;
+      }
+      const float f = scale / __ldcg(a.s + row0 + row);
+      v.x *= f, v.y *= f, v.z *= f, v.w *= f;
+      const uint32_t h0 = pair_of(v.x, v.y), h1 = pair_of(v.z, v.w);
+      __nv_bfloat16 *to = a.u + int64_t(row0 + row) * 2 * a.R16 + r0 + col;
+      *reinterpret_cast<uint2 *>(to) = make_uint2(h0, h1);
+      *reinterpret_cast<uint2 *>(to + a.R16) =
+          make_uint2(pair_of(v.x - low_of(h0), v.y - high_of(h0)),
+                     pair_of(v.z - low_of(h1), v.w - high_of(h1)));
+    }
+    cluster_arrive();  // the sums have been read
+    cluster_wait();
   }
 }
 
@@ -274,15 +334,6 @@ __device__ __forceinline__ uint4 load_y(const LoraArgs &a, int row, int col) {
       p[e >> 1] |= uint32_t(__bfloat16_as_ushort(y[e])) << (16 * (e & 1));
   return w;
 }
-// A pair of bf16 as fp32, and back.
-__device__ __forceinline__ float low_of(uint32_t w) { return __uint_as_float(w << 16); }
-__device__ __forceinline__ float high_of(uint32_t w) {
-  return __uint_as_float(w & 0xffff0000u);
-}
-__device__ __forceinline__ uint32_t pair_of(float lo, float hi) {
-  const __nv_bfloat162 t = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t *>(&t);
-}
 template <bool Vec>
 __device__ __forceinline__ void store_row(const LoraArgs &a, int row, int col,
                                           const uint32_t (&w)[4]) {
@@ -309,25 +360,6 @@ __device__ __forceinline__ void store_row(const LoraArgs &a, int row, int col,
 // projections have several clusters a tile, each with its share of the columns (u
 // is made by all of them).
 constexpr int kSortMost = 512;  // rows that are put in order
-__device__ __forceinline__ void cluster_arrive() {
-  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void cluster_wait() {
-  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-// 16 bytes at `p`'s place in another CTA's shared memory.
-__device__ __forceinline__ float4 load_of_cta(const float *p, uint32_t rank) {
-  uint32_t at;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
-               : "=r"(at)
-               : "r"(pipe::smem_addr(p)), "r"(rank));
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(at)
-               : "memory");
-  return v;
-}
 // Where u's value r lies in its row: the second product's reduction takes four
 // consecutive values of B's row a lane (c), as 2 c, 2 c + 1, 8 + 2 c and 9 + 2 c of
 // its 16, so u's are laid out in that order.
@@ -907,6 +939,18 @@ cudaError_t once(std::atomic<bool> *done, Kernel kernel, cudaFuncAttribute what,
   return e;
 }
 
+template <int NT>
+cudaError_t launch_shrink(const LoraArgs &a, int ctas, cudaLaunchConfig_t &cfg) {
+  static std::atomic<bool> done[64];
+  const cudaError_t e = once(done, lora_shrink_kernel<NT>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             int(ShrinkCfg<NT>::kSmem));
+  if (e != cudaSuccess) return e;
+  cfg.blockDim = dim3(kLoraThreads);
+  cfg.dynamicSmemBytes = ShrinkCfg<NT>::kSmem;
+  return cudaLaunchKernelEx(&cfg, lora_shrink_kernel<NT>, a, ctas);
+}
+
 template <int KK>
 cudaError_t launch_few(const LoraArgs &a, const FewCut &cut, bool vec_k,
                        cudaLaunchConfig_t &cfg) {
@@ -990,13 +1034,12 @@ cudaError_t launch_lora(const LoraLaunch &l, cudaStream_t stream) {
   attr[1].val.clusterDim.x = 8;
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  const unsigned tiles = unsigned((l.M + kLoraRows - 1) / kLoraRows);
   const bool vec_k = l.K % 8 == 0 && aligned_to(l.x, 8);
   const bool vec = l.y_ld % 8 == 0 && l.out_ld % 8 == 0 &&
                    aligned_to(l.y, 16) && aligned_to(l.out, 16);
   const int kk = a.R16 / 16;
   // (tensor maps' strides are below 2^40 bytes)
-  if (!vec || l.M < kLoraTcRows || int64_t(a.R) * l.N >= (int64_t(1) << 38)) {
+  if (!vec || !vec_k || l.M < kLoraTcRows || int64_t(a.R) * l.N >= (int64_t(1) << 38)) {
     cfg.numAttrs = 2;
     // Two CTAs an SM, clusters of 16 for a tile or two (a device has room for 14 of
     // those, and 36 of 8).
@@ -1018,20 +1061,17 @@ cudaError_t launch_lora(const LoraLaunch &l, cudaStream_t stream) {
     if (kk <= 4) return launch_few<4>(a, cut, vec_k, cfg);
     return launch_few<8>(a, cut, vec_k, cfg);
   }
+  // A x: about a CTA an SM (2011 rows: 63 tiles of two CTAs)
+  const int row_tiles = (l.M + kShRows - 1) / kShRows, col_tiles = (a.R16 + 63) / 64;
+  int ctas = 1;
+  while (ctas < 8 && 2 * ctas * row_tiles * col_tiles <= device_sm_count()) ctas *= 2;
+  cfg.numAttrs = 2;
+  attr[1].val.clusterDim.x = unsigned(ctas);
+  cfg.gridDim = dim3(unsigned(ctas), unsigned(row_tiles), unsigned(2 * col_tiles));
+  const cudaError_t e = a.R16 <= 16   ? launch_shrink<2>(a, ctas, cfg)
+                        : a.R16 <= 32 ? launch_shrink<4>(a, ctas, cfg)
+                                      : launch_shrink<8>(a, ctas, cfg);
   cfg.numAttrs = 1;
-  auto shrink = [&](auto whole, auto any, int nt) {
-    cfg.blockDim = dim3(kLoraThreads);
-    cfg.gridDim = dim3(tiles, unsigned((a.R16 + 8 * nt - 1) / (8 * nt)), 2);
-    return vec_k ? cudaLaunchKernelEx(&cfg, whole, a)
-                 : cudaLaunchKernelEx(&cfg, any, a);
-  };
-  const cudaError_t e =
-      a.R16 <= 16   ? shrink(lora_shrink_kernel<2, 5, true>,
-                             lora_shrink_kernel<2, 5, false>, 2)
-      : a.R16 <= 32 ? shrink(lora_shrink_kernel<4, 3, true>,
-                             lora_shrink_kernel<4, 3, false>, 4)
-                    : shrink(lora_shrink_kernel<8, 2, true>,
-                             lora_shrink_kernel<8, 2, false>, 8);
   if (e != cudaSuccess) return e;
   return kk <= 2   ? launch_expand<2>(a, cfg)
          : kk <= 4 ? launch_expand<4>(a, cfg)

@@ -734,7 +734,10 @@ bw_status bw_relu2_rms_norm_quant(const bw_bf16 *gu, int64_t gu_ld,
  *            16-byte aligned; adapters of smaller rank are padded with zeros
  *            (in both).
  *   scale    fp32 [n_adapters] device, 4-byte aligned, or NULL (1).
- *   adapter  int32 [M] device, 4-byte aligned, in any order.
+ *   adapter  int32 [M] device, 4-byte aligned, in any order.  (Up to 512 rows are
+ *            put in order by the call.  More are best taken by request, as prompts
+ *            lie in a batch: every adapter among 128 consecutive rows takes a turn
+ *            of its own.)
  *   y, out   bf16 [M][y_ld], [M][out_ld] device, 2-byte aligned, strides at
  *            least N and below 2^31 (columns of a fused projection, say); out
  *            may be y itself with the same stride, else must not overlap it.
@@ -744,7 +747,7 @@ bw_status bw_relu2_rms_norm_quant(const bw_bf16 *gu, int64_t gu_ld,
  *   1 <= M <= BW_MAX_M, 1 <= N <= BW_MAX_N, 4 <= K <= BW_MAX_K, K % 4 == 0,
  *   R a multiple of 8 up to BW_LORA_MAX_RANK, 1 <= n_adapters <=
  *   BW_LORA_MAX_ADAPTERS.  16-byte rows of y and out, and K % 8 == 0 with x on
- *   8 bytes, are read in vectors. */
+ *   8 bytes, are read in vectors; more than 512 rows take tcgen05 only so. */
 #define BW_LORA_MAX_RANK 128
 #define BW_LORA_MAX_ADAPTERS 65536
 size_t bw_lora_workspace_bytes(int M, int R);
