@@ -761,18 +761,26 @@ def bw_attn_paged_shared(q: torch.Tensor, k_pages: torch.Tensor,
     table = _vector(shared_table, _I32, dev, 1, "shared_table")
     length = _vector(shared_len, _I32, dev, 1, "shared_len")
     context, s = _where(dev, stream)
-    with context:
-        if out is None:
-            out = torch.empty((n, H, D), dtype=_BF16, device=q.device)
-        if workspace is None:
-            workspace = torch.zeros((max(16, bw_attn_paged_shared_workspace_bytes(
-                n, H, hkv, D)),), dtype=torch.uint8, device=q.device)
-        o, out_ld = _rows(out, (_BF16,), dev, n, H, D, "out")
-        _check(_lib.bw_attn_paged_shared(
-            ptr, ld, H, kv, table, shared_table.numel(), length,
-            1.0 / D ** 0.5 if scale is None else scale, o, out_ld,
-            _vector(workspace, torch.uint8, dev, 0, "workspace"),
-            workspace.numel(), s), "bw_attn_paged_shared")
+    if out is None or workspace is None:
+        with context:
+            if out is None:
+                out = torch.empty((n, H, D), dtype=_BF16, device=q.device)
+            if workspace is None:
+                workspace = torch.zeros(
+                    (max(16, bw_attn_paged_shared_workspace_bytes(n, H, hkv, D)),),
+                    dtype=torch.uint8, device=q.device)
+    o, out_ld = _rows(out, (_BF16,), dev, n, H, D, "out")
+    wp = _vector(workspace, torch.uint8, dev, 0, "workspace")
+    args = (ptr, ld, H, kv, table, shared_table.numel(), length,
+            1.0 / D ** 0.5 if scale is None else scale, o, out_ld, wp,
+            workspace.numel(), s)
+    if context is _NO_CONTEXT:
+        status = _lib.bw_attn_paged_shared(*args)
+    else:
+        with context:
+            status = _lib.bw_attn_paged_shared(*args)
+    if status:
+        _check(status, "bw_attn_paged_shared")
     return out
 
 

@@ -98,6 +98,11 @@ CASES = [
     (300, 1021, 68, 40, 20),
     (333, 513, 1028, 128, 3),
     (1000, 256, 512, 16, 2),
+    (12, 13824, 72, 16, 5),          # several clusters a tile
+    (40, 9000, 64, 128, 7),
+    (130, 4100, 40, 32, 3),
+    (512, 72, 48, 24, 200),
+    (512, 72, 48, 24, 1),
     (513, 8, 64, 8, 3),
     (640, 136, 260, 24, 40),
     (700, 200, 132, 128, 9),
@@ -227,6 +232,23 @@ def test_captured_and_on_another_stream(bw, M):
         c.adapter.copy_(torch.from_numpy(c.ids))
         graph.replay()
         c.check(out)
+
+
+@pytest.mark.parametrize("M", [1, 60, 600])
+def test_two_calls_at_once(bw, M):
+    """On two streams, each with a workspace of its own."""
+    a, b = Case(21, M, 512, 640, 16, 9), Case(22, M, 512, 640, 16, 9)
+    outs = [torch.zeros_like(c.y) for c in (a, b)]
+    size = bw.bw_lora_workspace_bytes(M, 16)
+    ws = [torch.zeros(size, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(30):
+        for c, o, w, st in zip((a, b), outs, ws, streams):
+            c.run(bw, out=o, workspace=w, stream=st)
+    torch.cuda.synchronize()
+    a.check(outs[0])
+    b.check(outs[1])
 
 
 def test_same_result_twice(bw):

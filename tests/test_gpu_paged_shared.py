@@ -316,6 +316,27 @@ def test_one_workspace_for_all_paged_calls(bw):  # noqa: F811
     bad(bw)
 
 
+def test_two_calls_at_once(bw):  # noqa: F811
+    """On two streams, each with a workspace of its own, beside other work."""
+    a = Batch(31, 900, [5 + i for i in range(40)], 20, 5, 128, 64)
+    b = Batch(32, 700, [i for i in range(33)], 16, 2, 64, 16)
+    outs = [torch.zeros_like(c.q) for c in (a, b)]
+    ws = [torch.zeros(bw.bw_attn_paged_shared_workspace_bytes(
+        len(c.lens), c.H, c.Hkv, c.D), dtype=torch.uint8, device="cuda") for c in (a, b)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    x = torch.zeros(1 << 24, device="cuda")
+    torch.cuda.synchronize()
+    for _ in range(30):
+        for c, o, w, st in zip((a, b), outs, ws, streams):
+            with torch.cuda.stream(st):
+                c.run(bw, out=o, workspace=w)
+        x.add_(1.0)
+    torch.cuda.synchronize()
+    a.check(outs[0])
+    b.check(outs[1])
+    assert bw.bw_device_error() == 0
+
+
 def test_long_prefix(bw):  # noqa: F811
     """100001 positions, against 64 bits on the GPU; many tiles a CTA."""
     shared, n, H, Hkv, D, page = 100001, 5, 8, 2, 128, 128
