@@ -1,11 +1,11 @@
 """The norms with 8-bit codes (GB300) where they could give way: a residual
-stream that is updated in place.
+stream that is updated in place, scales of the largest values.
 
 Forms and tolerances are those of test_gpu_norm_quant.py.
 """
 import pytest
 
-from test_gpu_norm_quant import bw, normals  # noqa: F401
+from test_gpu_norm_quant import bw, check, f64, normals  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -31,3 +31,28 @@ def test_in_place_is_as_into_another_buffer(bw, M, K, kind):  # noqa: F811
         q2, s2 = bw.bw_add_rms_norm_quant(x, gamma, h=h)
         assert torch.equal(h, out)
         assert torch.equal(s, s2) and torch.equal(q, q2)
+
+
+@pytest.mark.parametrize("K", [64, 67])
+@pytest.mark.parametrize("top", [2.0 ** 125, 2.0 ** 126, 1e38, 2.0 ** 127, 3.3e38])
+def test_values_up_to_the_largest(bw, K, top):  # noqa: F811
+    """A row that is finite has a scale, however large its values are."""
+    x = normals(1, 3, K).sign()
+    gamma = 1.0 + 0.25 * normals(2, K)
+    gamma[K // 2] = top
+    gamma[3] = -0.4 * top
+    q, s = bw.bw_add_rms_norm_quant(x, gamma, eps=0.0)
+    check(q, s, f64(x), f64(gamma), 0.0)
+    assert (q[:, K // 2].abs() == 127).all()
+
+
+def test_the_scale_is_the_quantisers(bw):  # noqa: F811
+    """Rows whose norm is 1 (64 values of 1 and -1, eps 0: every step is exact):
+    the same quotient as bw_quant_act's, to the bit."""
+    x = normals(3, 400, 64).sign()
+    for seed in range(20):
+        gamma = normals(seed + 10, 64) * 10.0 ** (seed % 7 - 3)
+        rows = x[seed:seed + 20]
+        _, s = bw.bw_add_rms_norm_quant(rows, gamma, eps=0.0)
+        _, want = bw.bw_quant_act((rows * gamma).contiguous())
+        assert torch.equal(s, want)
