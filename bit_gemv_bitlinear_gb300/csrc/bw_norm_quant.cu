@@ -12,8 +12,9 @@
 // largest |v gamma| come out of one pass and one exchange, and the codes are
 // rint(c v gamma (r s)), s = 127 / max(r max |c v gamma|, 1e-5).
 // Squares leave fp32's range where v is beyond 2^63 or all of a row is below
-// 2^-40: such a row is summed again with c the power of two that brings its
-// largest value near 1.  (Rows of zeros go that way too: two more exchanges.)
+// 2^-40, and products with gamma where gamma is as large: such a row is summed again
+// with c the power of two that brings its largest value near 1.  (Rows of zeros go
+// that way too: two more exchanges.)
 //
 // Bound by bytes (a few operations a value): a row's values stay in registers
 // between the sums and the codes, so each is read and written once.  A CTA takes
@@ -184,10 +185,10 @@ __device__ __forceinline__ RowScale row_scale(float2 t, float c,
   if (r.bad) r.s = __int_as_float(0x7fc00000);
   return r;
 }
-// Whether a row whose squares sum to this (with c = 1) is summed again; false
-// for NaN as well.
-__device__ __forceinline__ bool in_range(float sum) {
-  return sum >= 0x1p-80f && sum <= 0x1p126f;
+// Whether what came of a row with c = 1 serves (the sum of squares, and the largest
+// product with gamma); else the row is summed again.  False for NaN as well.
+__device__ __forceinline__ bool in_range(float2 t) {
+  return t.x >= 0x1p-80f && t.x <= 0x1p126f && t.y <= 3.402823466e38f;
 }
 // The row once more from memory, where the codes come from then too (rare: it
 // need not be fast).  h_out is written already.
@@ -262,7 +263,7 @@ norm_quant_kernel(const Rows rows, const float *gamma, float eps, float inv_K,
     }
   }
   t = block_sum_max(t, s_red[0]);
-  if (!in_range(t.x)) {  // (the whole block)
+  if (!in_range(t)) {  // (the whole block)
     again(rows, gamma, eps, inv_K, K, q, s_out, m, s_red);
     return;
   }
@@ -293,7 +294,7 @@ norm_quant_any_kernel(const Rows rows, const float *gamma, float eps, float inv_
     t.y = fmaxf(t.y, fabsf(v * gamma[k]));
   }
   t = block_sum_max(t, s_red[0]);
-  if (!in_range(t.x)) {
+  if (!in_range(t)) {
     again(rows, gamma, eps, inv_K, K, q, s_out, m, s_red);
     return;
   }

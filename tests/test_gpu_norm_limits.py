@@ -1,5 +1,6 @@
 """The norms with 8-bit codes (GB300) where they could give way: a residual
-stream that is updated in place, scales of the largest values.
+stream that is updated in place, scales of the largest values, products that leave
+fp32's range.
 
 Forms and tolerances are those of test_gpu_norm_quant.py.
 """
@@ -56,3 +57,15 @@ def test_the_scale_is_the_quantisers(bw):  # noqa: F811
         _, s = bw.bw_add_rms_norm_quant(rows, gamma, eps=0.0)
         _, want = bw.bw_quant_act((rows * gamma).contiguous())
         assert torch.equal(s, want)
+
+
+@pytest.mark.parametrize("K", [64, 67])
+@pytest.mark.parametrize("size,gain", [(2.0 ** 55, 2.0 ** 75), (2.0 ** 62, 2.0 ** 70),
+                                       (2.0 ** 61, 2.0 ** 110), (1e37, 1e30),
+                                       (2.0 ** 20, 2.0 ** 110)])
+def test_large_rows_of_large_gains(bw, K, size, gain):  # noqa: F811
+    """Their product leaves fp32's range; what the norm makes of it does not."""
+    x = normals(4, 3, K).clamp(-3, 3) * size
+    gamma = (1.0 + 0.25 * normals(5, K)) * gain
+    q, s = bw.bw_add_rms_norm_quant(x, gamma, eps=1e-5)
+    check(q, s, f64(x), f64(gamma), 1e-5)
