@@ -98,7 +98,9 @@ struct AddRows {
 __device__ __forceinline__ float gated(float g, float u) {
   // (not fmaxf, which would make 0 of a NaN)
   const float r = g < 0.0f ? 0.0f : g;
-  return r * r * u;
+  // r u first: of two bf16 values it is exact, and where it leaves fp32's range the
+  // result does too (r r does so from 2^64 on, whatever u is).
+  return r * u * r;
 }
 struct GateRows {
   static constexpr bool kStores = false;

@@ -4,6 +4,7 @@ fp32's range.
 
 Forms and tolerances are those of test_gpu_norm_quant.py.
 """
+import numpy as np
 import pytest
 
 from test_gpu_norm_quant import bw, check, f64, normals  # noqa: F401
@@ -69,3 +70,16 @@ def test_large_rows_of_large_gains(bw, K, size, gain):  # noqa: F811
     gamma = (1.0 + 0.25 * normals(5, K)) * gain
     q, s = bw.bw_add_rms_norm_quant(x, gamma, eps=1e-5)
     check(q, s, f64(x), f64(gamma), 1e-5)
+
+
+@pytest.mark.parametrize("F", [64, 67])
+@pytest.mark.parametrize("g,u", [(80, -100), (100, -120), (-75, 120), (-70, 125),
+                                 (63, -120), (-66, 100)])
+def test_squares_of_the_gate_beyond_the_range(bw, F, g, u):  # noqa: F811
+    """relu(g)^2 u is in fp32's range where relu(g)^2 is not, on either side."""
+    gu = torch.cat((normals(6, 3, F).clamp(-3, 3) * 2.0 ** g,
+                    normals(7, 3, F).clamp(-3, 3) * 2.0 ** u), 1).bfloat16()
+    gamma = 1.0 + 0.25 * normals(8, F)
+    q, s = bw.bw_relu2_rms_norm_quant(gu, gamma, eps=0.0)
+    v = np.maximum(f64(gu)[:, :F], 0) ** 2 * f64(gu)[:, F:]
+    check(q, s, v, f64(gamma), 0.0, more=4)
