@@ -82,7 +82,7 @@ struct PrefillArgs {
   // of a shared prefix: all key-value heads' items, how it shares the SMs
   int n_items, max_len;
   SharedRates rates;
-  int *ctas;
+  int2 *cut;  // CTAs that have a share, and positions, for the join
 };
 
 template <int D>
@@ -384,22 +384,34 @@ prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap qmap,
     int len = tid < a.v.n_seqs ? __ldcg(a.v.len + tid) : 0;
     shared = shared_positions(a.v, a.shared_len);
     void_call = false;
-    int own = 0;
+    int own = 0, longest = 0;
     for (int b = tid; b < a.v.n_seqs; b += kPfThreads) {
       if (b != tid) len = __ldcg(a.v.len + b);
-      const int t = len <= a.max_len ? shared_own_tiles(len, shared) : 0;
+      if (len > a.max_len) continue;  // (bad)
+      const int t = shared_own_tiles(len, shared);
       own += t + (t > 0);  // below 2^24
+      longest = max(longest, len);
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) own += __shfl_xor_sync(0xffffffffu, own, o);
-    if (lane == 0) before[warp] = own;
+    longest = __reduce_max_sync(0xffffffffu, longest);
+    if (lane == 0) {
+      before[warp] = own;
+      before[kPfThreads / 32 + warp] = longest;
+    }
     __syncthreads();
     float all = 0.0f;
-    for (int w = 0; w < kPfThreads / 32; ++w) all += float(before[w]);
+    for (int w = 0; w < kPfThreads / 32; ++w) {
+      all += float(before[w]);
+      longest = max(longest, before[kPfThreads / 32 + w]);
+    }
+    // Positions that no sequence sees may hold anything (and a value row that holds
+    // NaN is NaN times a weight of 0): the prefix ends where the longest does.
+    shared = min(shared, longest);
     const int n = shared_split(a.n_items, shared, all * float(a.v.hkv), a.rates);
     deal = shared_deal(a.n_items, shared, n);
     deal.share(int(blockIdx.x), &at, &share_end);
-    if (blockIdx.x == 0 && tid == 0) *a.ctas = n;
+    if (blockIdx.x == 0 && tid == 0) *a.cut = make_int2(n, shared);
   } else {
     const int b_lo = tid < kPfScan ? min(tid * per, a.v.n_seqs) : a.v.n_seqs;
     const int b_hi = min(b_lo + per, a.v.n_seqs);
@@ -1316,7 +1328,7 @@ cudaError_t launch_shared_prefix(const PagedView &v, const PagedAttnLaunch &l,
   a.n_items = x.cut.items;
   a.part = x.part;
   a.ml = x.ml;
-  a.ctas = x.ctas;
+  a.cut = x.at;
   a.max_len = x.max_len;
   a.rates = x.rates;
   if (l.D == 64) return launch_items<64, false, true>(a, l, grid, stream);

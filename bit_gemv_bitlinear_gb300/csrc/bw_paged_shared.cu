@@ -35,10 +35,9 @@ constexpr int kShThreads = 256;
 
 struct SharedJoinArgs {
   PagedView v;
-  const int *shared_len;
   int shared_pages;
   SharedCut cut;
-  const int *ctas;      // that have a share of the prefix
+  const int2 *at;       // CTAs that have a share of the prefix, its positions
   const float *pre;     // [slots][cut.seqs G][D]
   const float2 *pre_ml;
   const float *part;    // the decode kernel's parts
@@ -78,14 +77,15 @@ shared_join_kernel(const SharedJoinArgs a) {
     if (claims.x != 0u && claims.y != kDcFirst) atomicOr(a.v.err, kPagedErr);
   }
   // (asked for together; reported by the launches before)
-  const int shared_n = __ldcg(a.shared_len), len_n = __ldcg(a.v.len + b);
-  const int ctas = min(max(__ldcg(a.ctas), 0), kPfMostCtas);
+  const int2 at = __ldcg(a.at);
+  const int len_n = __ldcg(a.v.len + b);
   DcParts own = a.parts[int64_t(b) * a.v.hkv + g];
-  const int shared =
-      shared_n >= 0 && shared_n <= (a.shared_pages << a.v.page_shift) ? shared_n : 0;
   const bool there = head < a.v.n_seqs * a.H && len_n > 0 &&
                      len_n <= (a.v.max_pages << a.v.page_shift);
   // (a workspace that holds something else is not followed)
+  const int ctas = min(max(at.x, 0), kPfMostCtas);
+  const int shared =
+      at.y >= 0 && at.y <= (a.shared_pages << a.v.page_shift) ? at.y : 0;
   const int most = dc_max_units(D);
   if (own.unit0 < 0 || own.parts < 0 || own.parts > most ||
       own.unit0 > most - own.parts)
@@ -243,7 +243,7 @@ cudaError_t launch_paged_shared(const PagedView &v, const PagedAttnLaunch &l,
   uint8_t *ws = static_cast<uint8_t *>(l.workspace);
   x.part = reinterpret_cast<float *>(ws + at.part);
   x.ml = reinterpret_cast<float2 *>(ws + at.ml);
-  x.ctas = reinterpret_cast<int *>(ws + kPagedSharedAt);
+  x.at = reinterpret_cast<int2 *>(ws + kPagedSharedAt);
   x.max_len = v.max_pages << v.page_shift;
   x.rates = shared_rates(l.D, x.cut.seqs > kPfRows / (l.H / v.hkv), sms);
   PagedView prefix = v;
@@ -255,10 +255,9 @@ cudaError_t launch_paged_shared(const PagedView &v, const PagedAttnLaunch &l,
   if (e != cudaSuccess) return e;
   SharedJoinArgs a{};
   a.v = v;
-  a.shared_len = l.shared_len;
   a.shared_pages = l.shared_pages;
   a.cut = x.cut;
-  a.ctas = x.ctas;
+  a.at = x.at;
   a.pre = x.part;
   a.pre_ml = x.ml;
   // (as launch_paged_decode lays them out)

@@ -71,7 +71,7 @@ struct SharedPrefix {
   SharedCut cut;
   float *part;       // [slots][cut.seqs G][D]
   float2 *ml;        // [slots][cut.seqs G]
-  int *ctas;         // those that have a share, for the join
+  int2 *at;          // CTAs that have a share, and positions, for the join
   int max_len;       // of a sequence
   SharedRates rates;
 };
