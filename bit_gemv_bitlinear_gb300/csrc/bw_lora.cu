@@ -1038,11 +1038,13 @@ cudaError_t launch_lora(const LoraLaunch &l, cudaStream_t stream) {
   const bool vec = l.y_ld % 8 == 0 && l.out_ld % 8 == 0 &&
                    aligned_to(l.y, 16) && aligned_to(l.out, 16);
   const int kk = a.R16 / 16;
-  // (tensor maps' strides are below 2^40 bytes)
-  if (!vec || !vec_k || l.M < kLoraTcRows || int64_t(a.R) * l.N >= (int64_t(1) << 38)) {
+  // (tensor maps' strides are below 2^40 bytes whatever N and R are)
+  if (!vec || !vec_k || l.M < kLoraTcRows) {
     cfg.numAttrs = 2;
-    // Two CTAs an SM, clusters of 16 for a tile or two (a device has room for 14 of
-    // those, and 36 of 8).
+    // Clusters of 16 for a tile or two, else of 8; `room` is for two CTAs an SM, 19
+    // and 38 clusters.  (Clusters fill whole groups of SMs, so that 14 and 36 are
+    // there at once: one row of more than 57344 columns, and 289 to 304 rows, leave
+    // a few for a second round.)
     FewCut cut{};
     cut.vec = vec;
     cut.sort = l.M > kLoraRows && l.M <= kSortMost;

@@ -123,7 +123,7 @@ shared_join_kernel(const SharedJoinArgs a) {
       p = Piece{{y.x, y.y}};
     }
   };
-  // A running maximum over the parts, 8 in flight.  A part without visible
+  // A running maximum over the parts, kAhead in flight.  A part without visible
   // positions has the sum 0 and is left out; one that holds NaN keeps it.
   float mx = -INFINITY, sum = 0.0f;
   float acc[kE] = {};
@@ -233,9 +233,7 @@ cudaError_t launch_paged_shared(const PagedView &v, const PagedAttnLaunch &l,
   const int sms = device_sm_count();
   if (sms < 1) return cudaErrorInvalidDevice;
   SharedPrefix x{};
-  x.table = shared_table;
   x.len = l.shared_len;
-  x.pages = l.shared_pages;
   x.cut = shared_cut(v.n_seqs, l.H / v.hkv, v.hkv);
   const int grid =
       shared_grid(sms, x.cut, int64_t(l.shared_pages) << v.page_shift);

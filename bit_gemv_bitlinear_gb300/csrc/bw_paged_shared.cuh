@@ -65,14 +65,12 @@ inline SharedRates shared_rates(int D, bool two, int sms) {
   return r;
 }
 struct SharedPrefix {
-  const int *table;  // its pages
-  const int *len;    // its positions (one)
-  int pages;         // entries of the table
+  const int *len;  // its positions (one)
   SharedCut cut;
-  float *part;       // [slots][cut.seqs G][D]
-  float2 *ml;        // [slots][cut.seqs G]
-  int2 *at;          // CTAs that have a share, and positions, for the join
-  int max_len;       // of a sequence
+  float *part;     // [slots][cut.seqs G][D]
+  float2 *ml;      // [slots][cut.seqs G]
+  int2 *at;        // CTAs that have a share, and positions, for the join
+  int max_len;     // of a sequence
   SharedRates rates;
 };
 // Where the workspace's first 256 bytes keep it.
