@@ -11,7 +11,8 @@
 // maximum of the first positions seen and follows only when weights sum to
 // more than 2^16, so most tiles need no maximum and the running output is
 // rescaled rarely.  The weights are rounded to bf16 for the second product,
-// like the output; l sums them unrounded in fp32.
+// like the output (those of a shared prefix are kept as two bf16 values, see
+// below); l sums them unrounded in fp32.
 //
 // Bound by the tensor cores (4 D flops for each visible pair); few tokens over
 // a long past are bound by the bytes of the past.  Layout:
@@ -85,7 +86,7 @@ struct PrefillArgs {
   int2 *cut;  // CTAs that have a share, and positions, for the join
 };
 
-template <int D>
+template <int D, bool Shared>
 struct PfCfg {
   static constexpr uint32_t kQHalf = kPfRows * 128;       // 128 rows x 64 dims
   static constexpr uint32_t kQBytes = kQHalf * (D / 64);
@@ -135,8 +136,8 @@ struct PfCfg {
   // Tensor memory columns (of 512): scores of 128 columns and outputs of D for
   // each query tile.  Weights take 64: of their own where D leaves room (the
   // next scores then need not wait for the product that reads them), else
-  // the scores' first ones.
-  static constexpr bool kOwnP = D == 64;
+  // the scores' first ones.  Of a shared prefix they take 128, the scores' own.
+  static constexpr bool kOwnP = D == 64 && !Shared;
   static constexpr uint32_t kS = 0;                       // + 128 per tile
   static constexpr uint32_t kO = 256;                     // + D per tile
   static constexpr uint32_t kP = kOwnP ? kO + 2 * D : kS;
@@ -195,8 +196,11 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
 // In this order on purpose: the exponentials of four pairs are under way while
 // the four before them are summed and rounded.  360 cycles a warp (256 are the
 // exponentials' own); pair by pair it is 950, each waiting for the last.
+// lo, if given: w is cut off instead, and lo is what that left (which is exact),
+// rounded to bf16: 2^-15 of a weight is lost at most.
 __device__ __forceinline__ void weights64(const float *s, float scale2, float m,
-                                          uint32_t (&w)[32], float2 &sum) {
+                                          uint32_t (&w)[32], float2 &sum,
+                                          uint32_t *lo = nullptr) {
   constexpr int kAhead = 4;
   const float2 sc = make_float2(scale2, scale2), mm = make_float2(-m, -m);
   float2 e[2][kAhead];
@@ -220,8 +224,20 @@ __device__ __forceinline__ void weights64(const float *s, float scale2, float m,
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
       const float2 x = e[k & 1][i];
-      const __nv_bfloat162 t = __floats2bfloat162_rn(x.x, x.y);
-      w[k * kAhead + i] = *reinterpret_cast<const uint32_t *>(&t);
+      if (lo) {
+        // (five instructions; with a rounded w, which takes a conversion and two
+        // more, a pair of query tiles of 128 dims took 2.03 us, 1.83 so)
+        const uint32_t u = __float_as_uint(x.x), v = __float_as_uint(x.y);
+        w[k * kAhead + i] = __byte_perm(u, v, 0x7632);
+        const float2 d = fma2(make_float2(__uint_as_float(u & 0xffff0000u),
+                                          __uint_as_float(v & 0xffff0000u)),
+                              make_float2(-1.0f, -1.0f), x);
+        const __nv_bfloat162 r = __floats2bfloat162_rn(d.x, d.y);
+        lo[k * kAhead + i] = *reinterpret_cast<const uint32_t *>(&r);
+      } else {
+        const __nv_bfloat162 t = __floats2bfloat162_rn(x.x, x.y);
+        w[k * kAhead + i] = *reinterpret_cast<const uint32_t *>(&t);
+      }
       acc[i & 1] = add2(acc[i & 1], x);
     }
   }
@@ -335,12 +351,17 @@ __device__ __forceinline__ PfWork pf_work_shared(const PrefillArgs &a,
 // sequence, which sees the prefix up to its own length; the items' key tiles in
 // one order, dealt to the CTAs in equal contiguous shares, so a CTA's share is
 // a part of one item or of several, each left in the workspace for the join.
+// It stands for a decode call, so its weights keep the bits that they have there:
+// two bf16 values each, and two products (the error of an output that is rounded to
+// bf16 is 0.00165 of its norm then, as the decode call's; 0.0022 with one value).
+// Eight sequences behind 1027 positions take 12.9 us either way, 64 behind 8209 30.5
+// (30.1), 48 behind 100001, where the products are most of it, 77.4 (68.8).
 template <int D, bool Alone, bool Shared>
 __global__ void __launch_bounds__(kPfThreads, 1)
 prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap qmap,
                const __grid_constant__ CUtensorMap kmap,
                const __grid_constant__ CUtensorMap vmap) {
-  using C = PfCfg<D>;
+  using C = PfCfg<D, Shared>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t *smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
   uint64_t *bar = reinterpret_cast<uint64_t *>(smem + C::kBars);
@@ -715,8 +736,13 @@ prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap qmap,
 #pragma unroll
         for (int k = 0; k < kPfTile / 32; ++k) {
           const int ks = hh * (kPfTile / 32) + k;
-          tc_mma(t_o, t_p + ks * 8, vd + uint64_t(ks * (2048 / 16)), kIdO,
-                 !first || k > 0);
+          const uint64_t v = vd + uint64_t(ks * (2048 / 16));
+          if constexpr (Shared) {
+            tc_mma(t_o, t_p + hh * 64 + k * 8, v, kIdO, !first || k > 0);
+            tc_mma(t_o, t_p + hh * 64 + 32 + k * 8, v, kIdO, 1);
+          } else {
+            tc_mma(t_o, t_p + ks * 8, v, kIdO, !first || k > 0);
+          }
         }
       };
       // Three waits at the price of one (over 100 cycles even for what is
@@ -937,18 +963,7 @@ prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap qmap,
         // was summed before is rescaled, O_i too where it holds something
         // (has_o), once the products that were issued are done (phase `phase` of
         // the barrier `wait`, if any).
-        auto follow = [&](bool has_o, int wait, uint32_t phase) {
-          float mx[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) mx[k] = max3(s[3 * k], s[3 * k + 1], s[3 * k + 2]);
-#pragma unroll
-          for (int c = 12; c < 124; c += 8)
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              mx[k] = max3(mx[k], s[c + 2 * k], s[c + 2 * k + 1]);
-          mx[0] = max3(mx[0], s[124], s[125]);
-          mx[1] = max3(mx[1], s[126], s[127]);
-          const float top = max3(mx[0], mx[1], fmaxf(mx[2], mx[3])) * a.scale2;
+        auto follow_to = [&](float top, bool has_o, int wait, uint32_t phase) {
           const bool grow = top > m + 8.0f;
           // What a row that has seen nothing yet holds is zeros.  That goes by
           // its m, not by f: over a jump of 127 and more f is 0, and what the
@@ -972,6 +987,20 @@ prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap qmap,
           }
           unseen = __any_sync(0xffffffffu, m == -INFINITY);
         };
+        auto follow = [&](bool has_o, int wait, uint32_t phase) {
+          float mx[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) mx[k] = max3(s[3 * k], s[3 * k + 1], s[3 * k + 2]);
+#pragma unroll
+          for (int c = 12; c < 124; c += 8)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              mx[k] = max3(mx[k], s[c + 2 * k], s[c + 2 * k + 1]);
+          mx[0] = max3(mx[0], s[124], s[125]);
+          mx[1] = max3(mx[1], s[126], s[127]);
+          follow_to(max3(mx[0], mx[1], fmaxf(mx[2], mx[3])) * a.scale2, has_o, wait,
+                    phase);
+        };
         auto hand_over = [&](int hh) {
           tmem_wait_st();
           tc_fence_before();
@@ -984,7 +1013,66 @@ prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap qmap,
         // scale cancels in o / l, and neither bf16 nor the fp32 sums lose
         // anything by 2^16.
         constexpr float kMost = 65536.0f;
-        if constexpr (C::kOwnP) {
+        if constexpr (Shared) {
+          // The halves one after the other, by the same code, which is fetched
+          // anew for every tile (written out twice, as below: 8 sequences behind
+          // 1027 positions 15.0 us, 12.9 so).  A half's weights take the columns
+          // of its own scores, 32 their first values and 32 what is left.
+#pragma unroll 1
+          for (int hh = 0; hh < 2; ++hh) {
+            float h[64];
+            uint32_t lo[32];
+            tmem_ld32_issue(t_s + 64 * hh, h);
+            tmem_ld32_issue(t_s + 64 * hh + 32, h + 32);
+            tmem_landed(h);
+            tmem_landed(h + 32);
+            if (!all) {
+#pragma unroll
+              for (int c = 0; c < 64; c += 32) {
+                const uint32_t seen = below(p - x + 1 - 64 * hh - c);
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                  if (!(seen >> e & 1u)) h[c + e] = -INFINITY;
+              }
+            }
+            for (bool must = unseen;; must = true) {
+              if (must) {
+                float mx[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) mx[k] = fmaxf(h[2 * k], h[2 * k + 1]);
+#pragma unroll
+                for (int c = 8; c < 64; c += 8)
+#pragma unroll
+                  for (int k = 0; k < 4; ++k)
+                    mx[k] = max3(mx[k], h[c + 2 * k], h[c + 2 * k + 1]);
+                // (S_i(j) came after O_i(j - 1), but not if alone; the second half
+                // waits for the first one's product)
+                follow_to(max3(mx[0], mx[1], fmaxf(mx[2], mx[3])) * a.scale2,
+                          j + hh > 0, hh ? C::kDoneO + i : Alone ? C::kDoneO + 1 : -1,
+                          used - 1 + hh);
+              }
+              sum = make_float2(0.0f, 0.0f);
+              weights64(h, a.scale2, m == -INFINITY ? 0.0f : m, wt, sum, lo);
+              if (must || !__any_sync(0xffffffffu, sum.x + sum.y > kMost)) break;
+            }
+            uint32_t o_done = 0;
+            if (Alone && j > 0 && hh == 0)
+              o_done = mbar_test(&bar[C::kDoneO + 1], (used - 1) & 1u);
+            tmem_st32(t_p + 64 * hh, wt);
+            tmem_st32(t_p + 64 * hh + 32, lo);
+            // (as below)
+            if (Alone && j > 0 && hh == 0 && !__all_sync(0xffffffffu, o_done) &&
+                !warp_wait(&bar[C::kDoneO + 1], (used - 1) & 1u))
+              ok = false;
+            hand_over(hh);
+            if (Alone && hh == 0)
+              s_there = mbar_test(&bar[C::kFullS + ((used + 1) & 1u)],
+                                  ((used + 1) >> 1) & 1u);
+            l += sum.x + sum.y;
+          }
+          x += kPfTile;
+          continue;
+        } else if constexpr (C::kOwnP) {
 #pragma unroll
           for (int c = 0; c < 128; c += 32) tmem_ld32_issue(t_s + c, s + c);
 #pragma unroll
@@ -1017,8 +1105,7 @@ prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap qmap,
           // nothing branches in between, so nothing touches its registers)
           tmem_ld32_issue(t_s + 64, s + 64);
           tmem_ld32_issue(t_s + 96, s + 96);
-          // (Shared: not against an m that the next line looks for anyway)
-          if (!Shared || !unseen) weights64(s, a.scale2, m, wt, sum);
+          weights64(s, a.scale2, m, wt, sum);
           tmem_landed(s + 64);
           tmem_landed(s + 96);
           if (!all) mask();
@@ -1241,7 +1328,7 @@ cudaError_t launch_items(const PrefillArgs &a, const PagedAttnLaunch &l,
   static std::atomic<int> cached[64];
   int resident = 0;
   cudaError_t e = paged_resident(prefill_kernel<D, Alone, Shared>, cached,
-                                 kPfThreads, PfCfg<D>::kSmem, &resident);
+                                 kPfThreads, PfCfg<D, Shared>::kSmem, &resident);
   if (e != cudaSuccess) return e;
   // setmaxnreg draws on the registers of the launch: a build that gives the
   // threads fewer than the roles' sum would wait for ever, so it is refused.
@@ -1274,7 +1361,7 @@ cudaError_t launch_items(const PrefillArgs &a, const PagedAttnLaunch &l,
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(items < resident ? items : resident));
   cfg.blockDim = dim3(kPfThreads);
-  cfg.dynamicSmemBytes = PfCfg<D>::kSmem;
+  cfg.dynamicSmemBytes = PfCfg<D, Shared>::kSmem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -18,11 +18,12 @@
 //    gets, the first one's other CTAs leave at once, and the second does not wait
 //    for the first until its own work is done;
 //  * here, the join of a query head's parts of both, a warp per head or several.
-// 64 sequences of up to 500 positions behind 8209, 20 + 2 x 5 heads of 128: 29 us,
+// 64 sequences of up to 500 positions behind 8209, 20 + 2 x 5 heads of 128: 30 us,
 // of which the prefix's CTAs run from 3.5 to 24 (8 to the first scores, 2 a pair of
 // 128-row tiles, 2 to write the parts), the others' from 8 to 24, the join from 29
 // to 32 (the ends of two launches, 1.4 each, and two rounds of loads); 48 behind
-// 100001: 68, 0.60 of the measured copy rate, 720 TFLOP/s.
+// 100001: 77, 0.53 of the measured copy rate, 640 TFLOP/s, or 950 with the second
+// product's second half.
 #include <algorithm>
 
 #include "bw_paged_shared.cuh"

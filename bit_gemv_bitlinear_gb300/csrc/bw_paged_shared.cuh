@@ -49,17 +49,17 @@ inline size_t dc_parts_bytes(size_t items) {
 }
 
 // ---- the shared prefix ----
-// What things take, in us (shared_split), measured in calls of 48 to 230
-// sequences: a key tile of the prefix 1.65 with two query tiles of 128 dims (a
-// document of 100001 positions: 28 tiles a CTA in 48), 1.1 with one, 1.3 and 1.0
-// for 64 dims; a tile of the decode kernel 0.65, of which an SM has two at a time,
-// and 0.47 of three for 64 dims.  The prefix's first scores come about 3 later,
-// and its sums take 2 to write.  (64 sequences behind 8209 positions: 29.1 us; 41
-// without a split, the decode kernel's CTAs behind the prefix's.)
+// What things take, in us (shared_split), measured in calls of 16 to 230
+// sequences: a key tile of the prefix 1.85 with two query tiles of 128 dims (from 12
+// to 24 tiles a CTA), 1.4 with one, 1.6 and 1.35 for 64 dims; a tile of the decode
+// kernel 0.65, of which an SM has two at a time, and 0.47 of three for 64 dims.  The
+// prefix's first scores come about 3 later, and its sums take 2 to write.  (64
+// sequences behind 8209 positions: 29.1 us; 41 without a split, the decode kernel's
+// CTAs behind the prefix's; both with weights of one value.)
 inline SharedRates shared_rates(int D, bool two, int sms) {
   SharedRates r{};
   r.sms = sms < kPfMostCtas ? sms : kPfMostCtas;
-  r.pre_us = D == 64 ? (two ? 1.3f : 1.0f) : (two ? 1.65f : 1.1f);
+  r.pre_us = D == 64 ? (two ? 1.6f : 1.35f) : (two ? 1.85f : 1.4f);
   r.own_us = D == 64 ? 0.47f : 0.65f;
   r.late_us = D == 64 ? 6.0f : 8.0f;
   return r;

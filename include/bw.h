@@ -655,9 +655,9 @@ bw_status bw_attn_paged_prefill(const bw_bf16 *q, int64_t q_ld, int n_tokens,
  * zeros.  Entries of page_table below *shared_len / page_size are not used;
  * where the prefix ends inside a page, the sequence's own page is read from
  * there on.
- * No window; bf16 output.  The shared positions' products run on the tensor
- * cores and their exp weights are rounded to bf16, like the output; the others
- * are as in bw_attn_paged_decode.  What a shared position that some sequence
+ * No window; bf16 output.  All products run on the tensor cores, with exp
+ * weights of two bf16 values as in bw_attn_paged_decode (the shared positions' lose
+ * 2^-15 at most).  What a shared position that some sequence
  * sees holds must be finite; others may hold anything.  A visible score that
  * is NaN or +infinity and scores that are all -infinity give NaN in that head.
  *   shared_table int32 [n_shared_pages] device, 4-byte aligned (a row of the
