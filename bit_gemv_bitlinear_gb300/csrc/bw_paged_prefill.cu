@@ -384,6 +384,17 @@ prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap qmap,
     prefetch_map(&vmap);
   }
   if (warp == kPfMmaWarp) tmem_alloc(tmem_slot, 512);
+  // Rows of a query tile that no query fills (G does not divide 128) are read by the
+  // products all the same, and what comes of them has a say in when a warp follows
+  // its maximum: zeros, not what the SM's last CTA left, or calls would differ in
+  // their last bits.
+  for (int r = TQ * G * 8 + tid; r < kPfRows * 8; r += kPfThreads) {
+#pragma unroll
+    for (int h = 0; h < 2 * (D / 64); ++h)
+      *reinterpret_cast<uint4 *>(smem + C::kQ + h * C::kQHalf + r * 16) =
+          make_uint4(0u, 0u, 0u, 0u);
+    fence_async_smem();
+  }
   pdl_wait();
   pdl_trigger();
 
