@@ -230,8 +230,9 @@ norm_quant_kernel(const Rows rows, const float *gamma, float eps, float inv_K,
   const int m = blockIdx.x, nv = K / 4;
   // Every load without a branch around it (the last vector again where there is
   // none): with one, the compiler waits for each load before it makes the next
-  // (2039 x 6912 gated: 32 us, and 20.7 so).  In place, the last vector's owner may
-  // have written it by then: nothing is made of what such a lane reads.
+  // (2039 x 6912 gated, 4 vectors a thread: 32 us, and 20.9 so).  In place, the
+  // last vector's owner may have written it by then: nothing is made of what such a
+  // lane reads.
   typename Rows::Raw raw[V];
   float4 v[V];
 #pragma unroll
@@ -331,9 +332,10 @@ cudaError_t launch_rows(const Rows &rows, bool vec, const NormQuantLaunch &l,
                               l.q, l.s);
   };
   // Up to 320 threads: a CTA's loads are under way while others' sums are
-  // exchanged (us with 2, 4 and 8 vectors a thread: 4096 x 2560 with residual
-  // 18.3, 18.7, 26; 2039 x 6912 gated 19.3, 20.7, 16.5).  Where every row has an
-  // SM to itself, the shortest chain (64 x 6912: 2.1, 2.1, 2.5).
+  // exchanged (us with 2, 4 and 8 vectors a thread: 4096 x 2560 with residual 18.1,
+  // 18.4, 18.6; gated 2039 x 6912 19.8, 20.9, 17.2, 1000 x 13824 51, 23.5, 18.0).
+  // Where every row has an SM to itself, the shortest chain (64 x 6912: 2.05, 2.05,
+  // 2.2).
   const bool few = l.M <= device_sm_count();
   if (vec && nv <= (few ? 2048 : 640))
     return go(norm_quant_kernel<Rows, 2>, (nv + 1) / 2);

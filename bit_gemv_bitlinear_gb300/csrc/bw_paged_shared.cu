@@ -56,7 +56,7 @@ shared_join_kernel(const SharedJoinArgs a) {
   constexpr int kE = D / 32;  // dims a lane
   constexpr int kHeads = kShThreads / 32 / kWarps;
   // Alone a warp has few parts, and all CTAs should be there at once (7360 heads
-  // of 64 dims: a call of 30.0 us, 30.9 with 8 parts in flight, half of the CTAs
+  // of 64 dims: a call of 31.35 us, 31.7 with 8 parts in flight, half of the CTAs
   // waiting for the others' registers).
   constexpr int kAhead = kWarps == 1 ? 3 : 8;
   struct alignas(kE * 4) Piece {
